@@ -51,7 +51,7 @@
 extern "C" {
 #endif
 
-#define SIGNMUON_ABI_VERSION 4
+#define SIGNMUON_ABI_VERSION 5
 
 /* Status codes. */
 enum {
@@ -300,6 +300,60 @@ size_t signmuon_packed_words(int64_t n);
  * workspace serves both entry points. */
 size_t signmuon_workspace_bytes(const signmuon_matrix *mats, int32_t n_mats,
                                 const signmuon_params *p);
+
+/* ------------------------------------------------------------------------
+ * Gradients of the step's inputs.
+ *
+ * The step takes each weight's gradient as a stack [Mw][R][C], one matrix per
+ * worker (summary §2 "Algorithmic flow", step 1: each worker's stochastic
+ * gradient). The entry points below are the operators of a transformer's
+ * training pass whose weight gradients go into such a stack as they are: the
+ * embedding lookup and its gradient. The workers'
+ * batches sit side by side: worker m's tokens at offset m * tokens. They
+ * follow the conventions at the head of this file (device pointers, 16-byte
+ * aligned bases, every argument checked before anything is enqueued, kernel
+ * launches only), allocate nothing and keep nothing between calls. A
+ * workspace belongs to one call at a time: calls that may overlap, and graphs
+ * that may be replayed at once, take one each. Every result is the same on
+ * every run: no sum depends on the order in which the hardware runs it.
+ * Activations and weight gradients are F32 or BF16; sums and statistics are
+ * fp32, and each result is rounded once to its storage type.
+ * ---------------------------------------------------------------------- */
+
+/* Element type of token numbers. */
+typedef enum { SIGNMUON_I32 = 0, SIGNMUON_I64 = 1 } signmuon_itype;
+
+/*
+ * signmuon_embedding -- y[t][c] = scale * table[ids[t]][c], rounded once to
+ * y_dtype. ids is [tokens], table [vocab][cols], y [tokens][cols]. An id
+ * below 0 or at least vocab (padding) gives a row of zeros. tokens is the
+ * count over all workers.
+ */
+int signmuon_embedding(const void *ids, signmuon_itype id_type, const void *table,
+                       signmuon_dtype table_dtype, int64_t tokens, int64_t vocab, int64_t cols,
+                       float scale, void *y, signmuon_dtype y_dtype, signmuon_stream stream);
+
+/*
+ * signmuon_embedding_backward -- the gradient of the table for each worker:
+ *   grad[m][v][c] = scale * sum over the tokens t of worker m with ids[m][t] = v of dy[m][t][c]
+ * ids is [workers][tokens], dy [workers][tokens][cols] of dy_dtype, grad
+ * [workers][vocab][cols] of grad_dtype, the layout of signmuon_matrix.grad.
+ * accumulate = 0 writes every row (zeros where no token has that id);
+ * accumulate = 1 adds to what grad holds (the gradient of an output layer
+ * that shares the table) and touches no other row. Ids outside [0, vocab)
+ * add nothing. Tokens are sorted by id (stable) and each row's terms are
+ * added in a fixed order in fp32. workspace:
+ * signmuon_embedding_workspace_bytes(workers, tokens, vocab, cols) bytes.
+ */
+int signmuon_embedding_backward(const void *ids, signmuon_itype id_type, const void *dy,
+                                signmuon_dtype dy_dtype, int32_t workers, int64_t tokens,
+                                int64_t vocab, int64_t cols, float scale, void *grad,
+                                signmuon_dtype grad_dtype, int32_t accumulate, void *workspace,
+                                size_t workspace_bytes, signmuon_stream stream);
+
+/* Device workspace of signmuon_embedding_backward in bytes (0 on invalid
+ * arguments). */
+size_t signmuon_embedding_workspace_bytes(int32_t workers, int64_t tokens, int64_t vocab, int64_t cols);
 
 /* Text for a status code; for SIGNMUON_EHIP it names the HIP error of the
  * calling thread's last failure. Never NULL. */

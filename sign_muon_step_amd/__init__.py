@@ -21,7 +21,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsignmuon.so")
 
 F32, BF16 = 0, 1
-ABI_VERSION = 4
+ABI_VERSION = 5
 # device bytes of the static scratch behind signmuon_step_noalloc
 STATIC_SCRATCH_BYTES = 128 << 20
 
@@ -93,6 +93,13 @@ def library() -> ctypes.CDLL:
     lib.signmuon_sign_int8.argtypes = [vp, ctypes.c_int, i64, i32, vp, vp]
     lib.signmuon_vote_update_int8.restype = ctypes.c_int
     lib.signmuon_vote_update_int8.argtypes = [vp, i32, i64, vp, ctypes.c_float, vp, vp]
+    f32, size = ctypes.c_float, ctypes.c_size_t
+    for name, result, args in (
+            ("embedding", i32, [vp, i32, vp, i32, i64, i64, i64, f32, vp, i32, vp]),
+            ("embedding_backward", i32, [vp, i32, vp, i32, i32, i64, i64, i64, f32, vp, i32, i32, vp, size, vp]),
+            ("embedding_workspace_bytes", size, [i32, i64, i64, i64])):
+        fn = getattr(lib, "signmuon_" + name)
+        fn.restype, fn.argtypes = result, args
     lib.signmuon_packed_words.restype = ctypes.c_size_t
     lib.signmuon_packed_words.argtypes = [i64]
     lib.signmuon_workspace_bytes.restype = ctypes.c_size_t
@@ -405,3 +412,94 @@ def workspace_tensor(mats: Sequence[Matrix], params: Params, device) -> Optional
     if nbytes == 0:
         return None
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+# ---------------------------------------------------------------------------
+# Gradients of the step's inputs. Sizes come from the tensors' shapes; every
+# tensor is checked for type, shape, contiguity and device, and all tensors of
+# a call lie on one GPU. The call runs on that GPU, on the given stream or on
+# that GPU's current one.
+# ---------------------------------------------------------------------------
+_ACT = (torch.float32, torch.bfloat16)
+_ITYPE = {torch.int32: 0, torch.int64: 1}
+
+
+def _operand(t: torch.Tensor, name: str, dtypes, shape) -> int:
+    """The address of a tensor of one of `dtypes` and exactly `shape`. Where it
+    lies is for _on."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _space(workspace: Optional[torch.Tensor]):
+    """Address and bytes of a workspace."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _on(stream, fn, args, *tensors) -> None:
+    """fn(*args, stream) on the GPU that holds every tensor of the call."""
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise ValueError(f"tensors passed to the library must be in GPU memory (device {t.device})")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"tensors of one call must be on one GPU ({device} and {t.device})")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream on {stream.device}, tensors on {device}")
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)))
+
+
+def _rank(t: torch.Tensor, name: str, dims) -> tuple:
+    if t.dim() not in dims:
+        raise ValueError(f"{name}: {t.dim()} dimensions, expected {' or '.join(map(str, dims))}")
+    return tuple(t.shape)
+
+
+def bytes_tensor(nbytes: int, device) -> Optional[torch.Tensor]:
+    """A device workspace of `nbytes` bytes (None for 0)."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def signmuon_embedding(ids: torch.Tensor, table: torch.Tensor, scale: float, y: torch.Tensor, stream=None) -> None:
+    """y = scale * table[ids]; ids of any shape, y of that shape and table's
+    columns. Ids outside the table (padding) give rows of zeros."""
+    vocab, cols = _rank(table, "table", (2,))
+    args = (_operand(ids, "ids", _ITYPE, ids.shape), _ITYPE[ids.dtype], _operand(table, "table", _ACT, table.shape),
+            _dtype_code(table), ids.numel(), vocab, cols, scale,
+            _operand(y, "y", _ACT, tuple(ids.shape) + (cols,)), _dtype_code(y))
+    _on(stream, library().signmuon_embedding, args, ids, table, y)
+
+
+def signmuon_embedding_workspace_bytes(workers: int, tokens: int, vocab: int, cols: int) -> int:
+    return int(library().signmuon_embedding_workspace_bytes(workers, tokens, vocab, cols))
+
+
+def signmuon_embedding_backward(ids: torch.Tensor, dy: torch.Tensor, scale: float, grad: torch.Tensor,
+                                workspace: Optional[torch.Tensor], accumulate: bool = False, stream=None) -> None:
+    """grad[m][v] = scale * sum of dy[m][t] over the tokens t with ids[m][t] =
+    v, or added to grad with accumulate. ids [Mw][T], dy [Mw][T][C], grad
+    [Mw][V][C] (the layout of Matrix.grad)."""
+    workers, tokens = _rank(ids, "ids", (2,))
+    vocab, cols = _rank(grad, "grad", (3,))[1:]
+    args = (_operand(ids, "ids", _ITYPE, ids.shape), _ITYPE[ids.dtype],
+            _operand(dy, "dy", _ACT, (workers, tokens, cols)), _dtype_code(dy), workers, tokens, vocab, cols, scale,
+            _operand(grad, "grad", _ACT, (workers, vocab, cols)), _dtype_code(grad), int(bool(accumulate)),
+            *_space(workspace))
+    _on(stream, library().signmuon_embedding_backward, args, ids, dy, grad, workspace)

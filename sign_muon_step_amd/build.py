@@ -11,7 +11,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libsignmuon.so")
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("api.hip", "elementwise.hip", "ns_gemm.hip", "spectral.hip")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in (
+    "api.hip", "elementwise.hip", "ns_gemm.hip", "spectral.hip", "grad_api.hip", "embedding.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

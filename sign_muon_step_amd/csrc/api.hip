@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "signmuon.h"
+#include "grad_internal.h"
 #include "sm_internal.h"
 
 // Device scratch of signmuon_step_noalloc: the workspace of an allocation-
@@ -742,6 +743,12 @@ int noalloc_scratch(void **out) {
 }
 
 }  // namespace
+
+// Shared with the gradient operators' entry points.
+namespace sm {
+int launch_status() { return last_launch(); }
+int device_cus() { return ::device_cus(); }
+}  // namespace sm
 
 extern "C" {
 

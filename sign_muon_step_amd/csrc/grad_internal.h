@@ -1,0 +1,159 @@
+// grad_internal.h -- launch descriptors and device helpers of the gradient
+// operators (embedding, layer norm, 8-bit quantisation and products). Not
+// part of the public C ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace sm {
+
+// The calling thread's last HIP failure is kept for signmuon_strerror; returns
+// the status of the launch just made.
+int launch_status();
+
+// Compute units of the current device.
+int device_cus();
+
+// ---------------------------------------------------------------------------
+// Embedding.
+// ---------------------------------------------------------------------------
+struct Embed {
+    const void *ids;
+    const void *table;
+    void *y;
+    int64_t tokens, vocab, cols;
+    float scale;
+    bool id64, table_bf16, y_bf16;
+};
+void launch_embedding(const Embed &e, hipStream_t s);
+
+// Tokens sorted by one workgroup in LDS; longer batches are merged from runs
+// of this length.
+constexpr int kSortChunk = 4096;
+
+struct EmbedGrad {
+    const void *ids;
+    const void *dy;
+    void *grad;
+    uint64_t *keys[2];  // [workers][tokens]: id << 32 | token; the second only where tokens > kSortChunk
+    float *partial;     // [workers][segments][2][cols]: a segment's first and last rows where they are
+                        // shared with its neighbours
+    int64_t tokens, vocab, cols;
+    int32_t workers;
+    int32_t seg;        // sorted tokens per segment
+    int32_t segments;   // per worker
+    float scale;
+    bool id64, dy_bf16, grad_bf16, accumulate;
+};
+// Columns that one wave sums: 4 a lane.
+constexpr int kEmbedCols = 256;
+// Merge passes after the chunks' sorts; the sorted keys are in keys[passes & 1].
+int embed_merge_passes(int64_t tokens);
+int32_t embed_segment(int32_t workers, int64_t tokens, int64_t cols);
+void launch_embedding_sort(const EmbedGrad &e, hipStream_t s);
+void launch_embedding_merge(const EmbedGrad &e, int pass, hipStream_t s);
+void launch_embedding_sums(const EmbedGrad &e, hipStream_t s);
+void launch_embedding_join(const EmbedGrad &e, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// Device helpers
+// ---------------------------------------------------------------------------
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+// Vectors at any element's address: rows of an odd length start anywhere, and
+// the memory pipes take vectors at any address.
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
+__device__ __forceinline__ float from_bf16(uint32_t h) { return __uint_as_float(h << 16); }
+
+// Two fp32 values rounded to nearest even, as bf16 pairs (one v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint32_t to_bf16x2(float lo, float hi) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    const f32x2_t v = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load1(const void *p, int64_t i) {
+    if (BF16) return from_bf16(static_cast<const uint16_t *>(p)[i]);
+    return static_cast<const float *>(p)[i];
+}
+template <bool BF16>
+__device__ __forceinline__ void store1(void *p, int64_t i, float v) {
+    if (BF16)
+        static_cast<uint16_t *>(p)[i] = (uint16_t)to_bf16x2(v, v);
+    else
+        static_cast<float *>(p)[i] = v;
+}
+
+// N = 4 or 8 consecutive values from element i on, of which `count` exist
+// (the others are 0).
+template <bool BF16, int N>
+__device__ __forceinline__ void load_n(const void *p, int64_t i, int count, float (&v)[N]) {
+    static_assert(N == 4 || N == 8, "vector length");
+    if (count >= N) {
+        if (BF16) {
+            const uint16_t *q = static_cast<const uint16_t *>(p) + i;
+            uint32_t w[N / 2];
+            if (N == 8) {
+                const u32x4 t = *reinterpret_cast<const u32x4_any *>(q);
+#pragma unroll
+                for (int j = 0; j < N / 2; ++j) w[j] = t[j];
+            } else {
+                const u32x2 t = *reinterpret_cast<const u32x2_any *>(q);
+#pragma unroll
+                for (int j = 0; j < N / 2; ++j) w[j] = t[j];
+            }
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) {
+                v[2 * j] = __uint_as_float(w[j] << 16);
+                v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            }
+        } else {
+            const float *q = static_cast<const float *>(p) + i;
+#pragma unroll
+            for (int h = 0; h < N / 4; ++h) {
+                const f32x4 t = *reinterpret_cast<const f32x4_any *>(q + 4 * h);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[4 * h + j] = t[j];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = j < count ? load1<BF16>(p, i + j) : 0.0f;
+    }
+}
+
+template <bool BF16, int N>
+__device__ __forceinline__ void store_n(void *p, int64_t i, int count, const float (&v)[N]) {
+    static_assert(N == 4 || N == 8, "vector length");
+    if (count >= N) {
+        if (BF16) {
+            uint16_t *q = static_cast<uint16_t *>(p) + i;
+            uint32_t w[N / 2];
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) w[j] = to_bf16x2(v[2 * j], v[2 * j + 1]);
+            if constexpr (N == 8)
+                *reinterpret_cast<u32x4_any *>(q) = u32x4{w[0], w[1], w[2], w[3]};
+            else
+                *reinterpret_cast<u32x2_any *>(q) = u32x2{w[0], w[1]};
+        } else {
+            float *q = static_cast<float *>(p) + i;
+#pragma unroll
+            for (int h = 0; h < N / 4; ++h)
+                *reinterpret_cast<f32x4_any *>(q + 4 * h) = f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j < count) store1<BF16>(p, i + j, v[j]);
+    }
+}
+
+}  // namespace sm

@@ -1,0 +1,90 @@
+"""Host-side checks of the gradient operators: bad arguments are refused before
+any launch (fake, never dereferenced device addresses), and the binding refuses
+tensors of another type, shape, layout or device (no GPU needed)."""
+import pytest
+import torch
+
+import sign_muon_step_amd as sm
+
+A = 0x7f0000000000
+WS = (0x7f1000000000, 1 << 40)
+EINVAL, EDTYPE, EALIGN, EWORKSPACE, ERANGE = -1, -2, -3, -4, -6
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return sm.library()
+
+
+def calls_with(fn, names, good, **change):
+    args = dict(zip(names, good))
+    for k in change:
+        assert k in args
+    args.update(change)
+    return fn(*args.values())
+
+
+def test_embedding_arguments(lib):
+    names = "ids id_type table table_dtype tokens vocab cols scale y y_dtype stream".split()
+    good = [A, 0, A, 0, 10, 20, 30, 1.0, A, 0, None]
+    for change, status in [(dict(ids=None), EINVAL), (dict(table=None), EINVAL), (dict(y=None), EINVAL),
+                           (dict(tokens=0), EINVAL), (dict(vocab=0), EINVAL), (dict(cols=-1), EINVAL),
+                           (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL),
+                           (dict(id_type=2), EDTYPE), (dict(table_dtype=2), EDTYPE), (dict(y_dtype=-1), EDTYPE),
+                           (dict(ids=A + 8), EALIGN), (dict(table=A + 4), EALIGN), (dict(y=A + 2), EALIGN),
+                           (dict(tokens=(1 << 25) + 1), ERANGE), (dict(vocab=(1 << 20) + 1), ERANGE),
+                           (dict(cols=(1 << 20) + 1), ERANGE), (dict(vocab=1 << 20, cols=2048), ERANGE)]:
+        assert calls_with(lib.signmuon_embedding, names, good, **change) == status, change
+
+
+def test_embedding_backward_arguments(lib):
+    names = ("ids id_type dy dy_dtype workers tokens vocab cols scale grad grad_dtype accumulate workspace "
+             "workspace_bytes stream").split()
+    good = [A, 1, A, 1, 2, 10, 20, 30, 1.0, A, 0, 0, *WS, None]
+    need = sm.signmuon_embedding_workspace_bytes(2, 10, 20, 30)
+    assert need >= 2 * 10 * 8
+    for change, status in [(dict(ids=None), EINVAL), (dict(dy=None), EINVAL), (dict(grad=None), EINVAL),
+                           (dict(workers=0), EINVAL), (dict(tokens=0), EINVAL), (dict(vocab=-5), EINVAL),
+                           (dict(cols=0), EINVAL), (dict(scale=float("-inf")), EINVAL), (dict(accumulate=2), EINVAL),
+                           (dict(id_type=-1), EDTYPE), (dict(dy_dtype=7), EDTYPE), (dict(grad_dtype=2), EDTYPE),
+                           (dict(ids=A + 4), EALIGN), (dict(dy=A + 8), EALIGN), (dict(grad=A + 1), EALIGN),
+                           (dict(workspace=WS[0] + 8), EALIGN), (dict(workspace=None), EWORKSPACE),
+                           (dict(workspace_bytes=need - 1), EWORKSPACE), (dict(workers=256), ERANGE),
+                           (dict(tokens=1 << 25), ERANGE), (dict(tokens=1 << 62), ERANGE),
+                           (dict(vocab=1 << 20, cols=1 << 11), ERANGE)]:
+        assert calls_with(lib.signmuon_embedding_backward, names, good, **change) == status, change
+
+
+def test_embedding_workspace_sizes():
+    size = sm.signmuon_embedding_workspace_bytes
+    assert size(0, 1, 1, 1) == size(1, 0, 1, 1) == size(1, 1, 0, 1) == size(1, 1, 1, 0) == 0
+    assert size(1, 4096, 100, 8) < size(1, 4097, 100, 8)  # several sorted runs: room to merge them
+    # partial sums stay a small part of what a large batch reads
+    assert size(8, 4096, 32000, 768) < 8 * 4096 * 768 * 2
+
+
+def test_embedding_binding_refuses_other_tensors():
+    ids, table = torch.zeros(2, 5, dtype=torch.int64), torch.zeros(7, 6)
+    y = torch.zeros(2, 5, 6)
+    with pytest.raises(TypeError, match="ids"):
+        sm.signmuon_embedding(ids.float(), table, 1.0, y)
+    with pytest.raises(TypeError, match="table"):
+        sm.signmuon_embedding(ids, table.half(), 1.0, y)
+    with pytest.raises(ValueError, match="table"):
+        sm.signmuon_embedding(ids, table[0], 1.0, y)
+    with pytest.raises(ValueError, match="y: shape"):
+        sm.signmuon_embedding(ids, table, 1.0, y[:, :, :5])
+    with pytest.raises(ValueError, match="contiguous"):
+        sm.signmuon_embedding(ids, torch.zeros(6, 7).t(), 1.0, y)
+    with pytest.raises(ValueError, match="GPU memory"):
+        sm.signmuon_embedding(ids, table, 1.0, y)
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+    grad = torch.zeros(2, 7, 6)
+    with pytest.raises(ValueError, match="dy"):
+        sm.signmuon_embedding_backward(ids, y[:1], 1.0, grad, ws)
+    with pytest.raises(ValueError, match="grad"):
+        sm.signmuon_embedding_backward(ids, y, 1.0, grad[:1].contiguous(), ws)
+    with pytest.raises(ValueError, match="ids"):
+        sm.signmuon_embedding_backward(ids[0], y, 1.0, grad, ws)
+    with pytest.raises(ValueError, match="GPU memory"):
+        sm.signmuon_embedding_backward(ids, y, 1.0, grad, ws)
