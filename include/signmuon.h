@@ -308,7 +308,7 @@ size_t signmuon_workspace_bytes(const signmuon_matrix *mats, int32_t n_mats,
  * worker (summary §2 "Algorithmic flow", step 1: each worker's stochastic
  * gradient). The entry points below are the operators of a transformer's
  * training pass whose weight gradients go into such a stack as they are: the
- * embedding lookup and its gradient. The workers'
+ * embedding lookup and its gradient, layer norm and its gradients. The workers'
  * batches sit side by side: worker m's tokens at offset m * tokens. They
  * follow the conventions at the head of this file (device pointers, 16-byte
  * aligned bases, every argument checked before anything is enqueued, kernel
@@ -354,6 +354,40 @@ int signmuon_embedding_backward(const void *ids, signmuon_itype id_type, const v
 /* Device workspace of signmuon_embedding_backward in bytes (0 on invalid
  * arguments). */
 size_t signmuon_embedding_workspace_bytes(int32_t workers, int64_t tokens, int64_t vocab, int64_t cols);
+
+/*
+ * signmuon_layer_norm -- for each of rows rows of cols values:
+ *   mean = sum(x) / cols, rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps)
+ *   y = (x - mean) * rstd * gamma + beta
+ * x and y are [rows][cols] of x_dtype, gamma and beta [cols] fp32 (beta may
+ * be NULL: no bias). mean and rstd [rows] fp32 receive the statistics for the
+ * backward pass (either may be NULL). eps is positive and finite. The
+ * variance is summed from the differences to the mean, not from squares.
+ */
+int signmuon_layer_norm(const void *x, signmuon_dtype x_dtype, int64_t rows, int64_t cols,
+                        const float *gamma, const float *beta, float eps, void *y, float *mean,
+                        float *rstd, signmuon_stream stream);
+
+/*
+ * signmuon_layer_norm_backward -- with xh = (x - mean) * rstd and t = dy * gamma:
+ *   dx = rstd * (t - mean_c(t) - xh * mean_c(t * xh))
+ *   dgamma[m] = sum over worker m's rows of dy * xh,  dbeta[m] = sum of dy
+ * x, dy and dx are [workers][rows][cols] of x_dtype; mean and rstd are those
+ * of signmuon_layer_norm, [workers][rows]; dgamma and dbeta are
+ * [workers][cols] of grad_dtype, the layout of signmuon_matrix.grad for a
+ * 1 x cols matrix. dx, dgamma and dbeta may each be NULL (not wanted), not
+ * all three. workspace:
+ * signmuon_layer_norm_workspace_bytes(workers, rows, cols) bytes.
+ */
+int signmuon_layer_norm_backward(const void *dy, const void *x, signmuon_dtype x_dtype,
+                                 int32_t workers, int64_t rows, int64_t cols, const float *gamma,
+                                 const float *mean, const float *rstd, void *dx, void *dgamma,
+                                 void *dbeta, signmuon_dtype grad_dtype, void *workspace,
+                                 size_t workspace_bytes, signmuon_stream stream);
+
+/* Device workspace of signmuon_layer_norm_backward in bytes (0 on invalid
+ * arguments). */
+size_t signmuon_layer_norm_workspace_bytes(int32_t workers, int64_t rows, int64_t cols);
 
 /* Text for a status code; for SIGNMUON_EHIP it names the HIP error of the
  * calling thread's last failure. Never NULL. */

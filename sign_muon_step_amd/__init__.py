@@ -97,7 +97,10 @@ def library() -> ctypes.CDLL:
     for name, result, args in (
             ("embedding", i32, [vp, i32, vp, i32, i64, i64, i64, f32, vp, i32, vp]),
             ("embedding_backward", i32, [vp, i32, vp, i32, i32, i64, i64, i64, f32, vp, i32, i32, vp, size, vp]),
-            ("embedding_workspace_bytes", size, [i32, i64, i64, i64])):
+            ("embedding_workspace_bytes", size, [i32, i64, i64, i64]),
+            ("layer_norm", i32, [vp, i32, i64, i64, vp, vp, f32, vp, vp, vp, vp]),
+            ("layer_norm_backward", i32, [vp, vp, i32, i32, i64, i64, vp, vp, vp, vp, vp, vp, i32, vp, size, vp]),
+            ("layer_norm_workspace_bytes", size, [i32, i64, i64])):
         fn = getattr(lib, "signmuon_" + name)
         fn.restype, fn.argtypes = result, args
     lib.signmuon_packed_words.restype = ctypes.c_size_t
@@ -436,6 +439,10 @@ def _operand(t: torch.Tensor, name: str, dtypes, shape) -> int:
     return t.data_ptr()
 
 
+def _optional(t: Optional[torch.Tensor], name: str, dtypes, shape) -> Optional[int]:
+    return None if t is None else _operand(t, name, dtypes, shape)
+
+
 def _space(workspace: Optional[torch.Tensor]):
     """Address and bytes of a workspace."""
     if workspace is None:
@@ -503,3 +510,45 @@ def signmuon_embedding_backward(ids: torch.Tensor, dy: torch.Tensor, scale: floa
             _operand(grad, "grad", _ACT, (workers, vocab, cols)), _dtype_code(grad), int(bool(accumulate)),
             *_space(workspace))
     _on(stream, library().signmuon_embedding_backward, args, ids, dy, grad, workspace)
+
+
+def signmuon_layer_norm(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[torch.Tensor], eps: float,
+                        y: torch.Tensor, mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+                        stream=None) -> None:
+    """Layer norm over x's last dimension; mean and rstd (x's other dimensions,
+    fp32) are kept for the backward pass when given."""
+    f32 = (torch.float32,)
+    cols = x.shape[-1] if x.dim() else 0
+    args = (_operand(x, "x", _ACT, x.shape), _dtype_code(x), x.numel() // max(cols, 1), cols,
+            _operand(gamma, "gamma", f32, (cols,)), _optional(beta, "beta", f32, (cols,)), eps,
+            _operand(y, "y", (x.dtype,), x.shape), _optional(mean, "mean", f32, x.shape[:-1]),
+            _optional(rstd, "rstd", f32, x.shape[:-1]))
+    _on(stream, library().signmuon_layer_norm, args, x, gamma, beta, y, mean, rstd)
+
+
+def signmuon_layer_norm_workspace_bytes(workers: int, rows: int, cols: int) -> int:
+    return int(library().signmuon_layer_norm_workspace_bytes(workers, rows, cols))
+
+
+def signmuon_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor, mean: torch.Tensor,
+                                 rstd: torch.Tensor, dx: Optional[torch.Tensor], dgamma: Optional[torch.Tensor],
+                                 dbeta: Optional[torch.Tensor], workspace: Optional[torch.Tensor],
+                                 workers: int = 1, stream=None) -> None:
+    """Gradients of layer norm. x's rows are those of `workers` workers, one
+    after the other; dgamma and dbeta are [Mw][C] or [Mw][1][C] (the layout of
+    Matrix.grad), one sum for each worker. Each of the three may be None."""
+    f32 = (torch.float32,)
+    cols = x.shape[-1] if x.dim() else 0
+    rows = x.numel() // max(cols, 1)
+    if workers < 1 or rows % workers:
+        raise ValueError(f"x: {rows} rows are not those of {workers} workers")
+    sums = [t for t in (dgamma, dbeta) if t is not None]
+    grad = sums[0].dtype if sums else torch.float32
+    shape = (workers, 1, cols) if sums and sums[0].dim() == 3 else (workers, cols)
+    args = (_operand(dy, "dy", (x.dtype,), x.shape), _operand(x, "x", _ACT, x.shape), _dtype_code(x), workers,
+            rows // workers, cols, _operand(gamma, "gamma", f32, (cols,)),
+            _operand(mean, "mean", f32, x.shape[:-1]), _operand(rstd, "rstd", f32, x.shape[:-1]),
+            _optional(dx, "dx", (x.dtype,), x.shape),
+            _optional(dgamma, "dgamma", (grad,), shape), _optional(dbeta, "dbeta", (grad,), shape),
+            _dtype_code(sums[0]) if sums else F32, *_space(workspace))
+    _on(stream, library().signmuon_layer_norm_backward, args, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace)

@@ -12,7 +12,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libsignmuon.so")
 SOURCES = [os.path.join(HERE, "csrc", f) for f in (
-    "api.hip", "elementwise.hip", "ns_gemm.hip", "spectral.hip", "grad_api.hip", "embedding.hip")]
+    "api.hip", "elementwise.hip", "ns_gemm.hip", "spectral.hip", "grad_api.hip", "embedding.hip",
+    "layer_norm.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

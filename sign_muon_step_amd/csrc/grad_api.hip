@@ -54,6 +54,20 @@ EmbedPlan embedding_plan(int64_t workers, int64_t tokens, int64_t cols) {
     return p;
 }
 
+// ---------------------------------------------------------------------------
+// Layer norm
+// ---------------------------------------------------------------------------
+int check_norm(int64_t workers, int64_t rows, int64_t cols) {
+    if (workers < 1 || rows < 1 || cols < 1) return SIGNMUON_EINVAL;
+    if (workers > kMaxWorkers || rows > kMaxTokens / workers || cols > kMaxDim) return SIGNMUON_ERANGE;
+    return SIGNMUON_OK;
+}
+
+size_t norm_workspace(int32_t workers, int64_t rows, int64_t cols) {
+    const int32_t parts = sm::norm_parts(workers, rows, cols);
+    return parts > 1 ? (size_t)((int64_t)workers * parts * 2 * cols) * sizeof(float) : 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -130,6 +144,68 @@ int signmuon_embedding_backward(const void *ids, signmuon_itype id_type, const v
     if (int rc = sm::launch_status()) return rc;
     if (e.segments == 1) return SIGNMUON_OK;
     sm::launch_embedding_join(e, st);
+    return sm::launch_status();
+}
+
+int signmuon_layer_norm(const void *x, signmuon_dtype x_dtype, int64_t rows, int64_t cols,
+                        const float *gamma, const float *beta, float eps, void *y, float *mean,
+                        float *rstd, signmuon_stream stream) {
+    if (!x || !gamma || !y) return SIGNMUON_EINVAL;
+    if (int rc = check_norm(1, rows, cols)) return rc;
+    if (!std::isfinite(eps) || eps <= 0.0f) return SIGNMUON_EINVAL;
+    if (!dtype_ok(x_dtype)) return SIGNMUON_EDTYPE;
+    if (!all_aligned(x, gamma, beta, y, mean, rstd)) return SIGNMUON_EALIGN;
+    sm::Norm n{};
+    n.x = x;
+    n.gamma = gamma;
+    n.beta = beta;
+    n.y = y;
+    n.mean = mean;
+    n.rstd = rstd;
+    n.rows = rows;
+    n.cols = cols;
+    n.eps = eps;
+    n.bf16 = x_dtype == SIGNMUON_BF16;
+    sm::launch_layer_norm(n, static_cast<hipStream_t>(stream));
+    return sm::launch_status();
+}
+
+size_t signmuon_layer_norm_workspace_bytes(int32_t workers, int64_t rows, int64_t cols) {
+    if (check_norm(workers, rows, cols) != SIGNMUON_OK) return 0;
+    return norm_workspace(workers, rows, cols);
+}
+
+int signmuon_layer_norm_backward(const void *dy, const void *x, signmuon_dtype x_dtype,
+                                 int32_t workers, int64_t rows, int64_t cols, const float *gamma,
+                                 const float *mean, const float *rstd, void *dx, void *dgamma,
+                                 void *dbeta, signmuon_dtype grad_dtype, void *workspace,
+                                 size_t workspace_bytes, signmuon_stream stream) {
+    if (!dy || !x || !gamma || !mean || !rstd || (!dx && !dgamma && !dbeta)) return SIGNMUON_EINVAL;
+    if (int rc = check_norm(workers, rows, cols)) return rc;
+    if (!dtype_ok(x_dtype) || !dtype_ok(grad_dtype)) return SIGNMUON_EDTYPE;
+    if (!all_aligned(dy, x, gamma, mean, rstd, dx, dgamma, dbeta)) return SIGNMUON_EALIGN;
+    if (int rc = check_workspace(workspace, workspace_bytes, norm_workspace(workers, rows, cols))) return rc;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    sm::NormGrad n{};
+    n.dy = dy;
+    n.x = x;
+    n.gamma = gamma;
+    n.mean = mean;
+    n.rstd = rstd;
+    n.dx = dx;
+    n.dgamma = dgamma;
+    n.dbeta = dbeta;
+    n.partial = static_cast<float *>(workspace);
+    n.rows = rows;
+    n.cols = cols;
+    n.workers = workers;
+    n.parts = sm::norm_parts(workers, rows, cols);
+    n.bf16 = x_dtype == SIGNMUON_BF16;
+    n.grad_bf16 = grad_dtype == SIGNMUON_BF16;
+    sm::launch_layer_norm_backward(n, st);
+    if (int rc = sm::launch_status()) return rc;
+    if (n.parts == 1 || (!dgamma && !dbeta)) return SIGNMUON_OK;
+    sm::launch_layer_norm_sums(n, st);
     return sm::launch_status();
 }
 

@@ -58,6 +58,36 @@ void launch_embedding_sums(const EmbedGrad &e, hipStream_t s);
 void launch_embedding_join(const EmbedGrad &e, hipStream_t s);
 
 // ---------------------------------------------------------------------------
+// Layer norm.
+// ---------------------------------------------------------------------------
+struct Norm {
+    const void *x;
+    const float *gamma, *beta;
+    void *y;
+    float *mean, *rstd;
+    int64_t rows, cols;
+    float eps;
+    bool bf16;
+};
+void launch_layer_norm(const Norm &n, hipStream_t s);
+
+struct NormGrad {
+    const void *dy, *x;
+    const float *gamma, *mean, *rstd;
+    void *dx, *dgamma, *dbeta;
+    float *partial;  // [workers][parts][2][cols] sums of dy * xh and of dy; unused where parts = 1
+    int64_t rows;    // per worker
+    int64_t cols;
+    int32_t workers;
+    int32_t parts;  // blocks of rows per worker, each with a sum of its own
+    bool bf16, grad_bf16;
+};
+int32_t norm_parts(int32_t workers, int64_t rows, int64_t cols);
+void launch_layer_norm_backward(const NormGrad &n, hipStream_t s);
+// Adds the parts' sums (parts > 1).
+void launch_layer_norm_sums(const NormGrad &n, hipStream_t s);
+
+// ---------------------------------------------------------------------------
 // Device helpers
 // ---------------------------------------------------------------------------
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));

@@ -88,3 +88,59 @@ def test_embedding_binding_refuses_other_tensors():
         sm.signmuon_embedding_backward(ids[0], y, 1.0, grad, ws)
     with pytest.raises(ValueError, match="GPU memory"):
         sm.signmuon_embedding_backward(ids, y, 1.0, grad, ws)
+
+
+def test_layer_norm_arguments(lib):
+    names = "x x_dtype rows cols gamma beta eps y mean rstd stream".split()
+    good = [A, 1, 10, 20, A, None, 1e-5, A, None, None, None]
+    for change, status in [(dict(x=None), EINVAL), (dict(gamma=None), EINVAL), (dict(y=None), EINVAL),
+                           (dict(rows=0), EINVAL), (dict(cols=0), EINVAL), (dict(eps=0.0), EINVAL),
+                           (dict(eps=-1e-5), EINVAL), (dict(eps=float("nan")), EINVAL), (dict(x_dtype=2), EDTYPE),
+                           (dict(x=A + 2), EALIGN), (dict(gamma=A + 4), EALIGN), (dict(beta=A + 8), EALIGN),
+                           (dict(y=A + 4), EALIGN), (dict(mean=A + 4), EALIGN), (dict(rstd=A + 12), EALIGN),
+                           (dict(rows=(1 << 25) + 1), ERANGE), (dict(cols=(1 << 20) + 1), ERANGE)]:
+        assert calls_with(lib.signmuon_layer_norm, names, good, **change) == status, change
+
+
+def test_layer_norm_backward_arguments(lib):
+    names = ("dy x x_dtype workers rows cols gamma mean rstd dx dgamma dbeta grad_dtype workspace workspace_bytes "
+             "stream").split()
+    good = [A, A, 0, 2, 1000, 20, A, A, A, A, A, A, 1, *WS, None]
+    need = sm.signmuon_layer_norm_workspace_bytes(2, 1000, 20)
+    assert need > 0
+    for change, status in [(dict(dy=None), EINVAL), (dict(x=None), EINVAL), (dict(gamma=None), EINVAL),
+                           (dict(mean=None), EINVAL), (dict(rstd=None), EINVAL),
+                           (dict(dx=None, dgamma=None, dbeta=None), EINVAL), (dict(workers=0), EINVAL),
+                           (dict(rows=0), EINVAL), (dict(cols=-1), EINVAL), (dict(x_dtype=2), EDTYPE),
+                           (dict(grad_dtype=3), EDTYPE), (dict(dx=A + 8), EALIGN), (dict(dgamma=A + 4), EALIGN),
+                           (dict(dbeta=A + 2), EALIGN), (dict(dy=A + 2), EALIGN), (dict(workspace=None), EWORKSPACE),
+                           (dict(workspace_bytes=need - 1), EWORKSPACE), (dict(workspace=WS[0] + 4), EALIGN),
+                           (dict(workers=256), ERANGE), (dict(rows=1 << 25), ERANGE), (dict(rows=1 << 62), ERANGE),
+                           (dict(cols=1 << 21), ERANGE)]:
+        assert calls_with(lib.signmuon_layer_norm_backward, names, good, **change) == status, change
+
+
+def test_layer_norm_binding_refuses_other_tensors():
+    x, gamma, y = torch.zeros(4, 6), torch.zeros(6), torch.zeros(4, 6)
+    s = torch.zeros(4)
+    with pytest.raises(TypeError, match="gamma"):
+        sm.signmuon_layer_norm(x, gamma.bfloat16(), None, 1e-5, y)
+    with pytest.raises(ValueError, match="beta"):
+        sm.signmuon_layer_norm(x, gamma, gamma[:5], 1e-5, y)
+    with pytest.raises(TypeError, match="y"):
+        sm.signmuon_layer_norm(x, gamma, None, 1e-5, y.bfloat16())
+    with pytest.raises(ValueError, match="mean"):
+        sm.signmuon_layer_norm(x, gamma, None, 1e-5, y, torch.zeros(5))
+    with pytest.raises(ValueError, match="contiguous"):
+        sm.signmuon_layer_norm(torch.zeros(6, 4).t(), gamma, None, 1e-5, y)
+    with pytest.raises(ValueError, match="GPU memory"):
+        sm.signmuon_layer_norm(x, gamma, None, 1e-5, y)
+    back = sm.signmuon_layer_norm_backward
+    with pytest.raises(ValueError, match="workers"):
+        back(y, x, gamma, s, s, x, None, None, None, workers=3)
+    with pytest.raises(ValueError, match="dgamma"):
+        back(y, x, gamma, s, s, x, torch.zeros(1, 6), None, None, workers=2)
+    with pytest.raises(TypeError, match="dbeta"):
+        back(y, x, gamma, s, s, x, torch.zeros(2, 6), torch.zeros(2, 6).bfloat16(), None, workers=2)
+    with pytest.raises(TypeError, match="dy"):
+        back(y.bfloat16(), x, gamma, s, s, x, None, None, None)
