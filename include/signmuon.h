@@ -308,7 +308,8 @@ size_t signmuon_workspace_bytes(const signmuon_matrix *mats, int32_t n_mats,
  * worker (summary §2 "Algorithmic flow", step 1: each worker's stochastic
  * gradient). The entry points below are the operators of a transformer's
  * training pass whose weight gradients go into such a stack as they are: the
- * embedding lookup and its gradient, layer norm and its gradients. The workers'
+ * embedding lookup and its gradient, layer norm and its gradients, and linear
+ * layers in 8-bit floating point (quantisation and products). The workers'
  * batches sit side by side: worker m's tokens at offset m * tokens. They
  * follow the conventions at the head of this file (device pointers, 16-byte
  * aligned bases, every argument checked before anything is enqueued, kernel
@@ -322,6 +323,10 @@ size_t signmuon_workspace_bytes(const signmuon_matrix *mats, int32_t n_mats,
 
 /* Element type of token numbers. */
 typedef enum { SIGNMUON_I32 = 0, SIGNMUON_I64 = 1 } signmuon_itype;
+
+/* 8-bit floating point formats (OCP): E4M3 (largest value 448, no infinity)
+ * and E5M2 (largest value 57344, with infinities). */
+typedef enum { SIGNMUON_E4M3 = 0, SIGNMUON_E5M2 = 1 } signmuon_f8;
 
 /*
  * signmuon_embedding -- y[t][c] = scale * table[ids[t]][c], rounded once to
@@ -388,6 +393,53 @@ int signmuon_layer_norm_backward(const void *dy, const void *x, signmuon_dtype x
 /* Device workspace of signmuon_layer_norm_backward in bytes (0 on invalid
  * arguments). */
 size_t signmuon_layer_norm_workspace_bytes(int32_t workers, int64_t rows, int64_t cols);
+
+/*
+ * 8-bit operands. A row of k values is stored as signmuon_f8_pitch(k) bytes
+ * (k rounded up to a multiple of 128, zeros past k) with one scale byte for
+ * each block of 128 consecutive values, signmuon_f8_scale_pitch(k) bytes a
+ * row (ceil(k / 128) rounded up to a multiple of 4). Byte b stands for the
+ * scale 2^(b - 127): powers of two, which the matrix cores apply themselves
+ * and which make x / scale exact. Byte 255 is not a scale.
+ *
+ * signmuon_f8_quant -- quantises x [batch][rows][cols] of x_dtype along its
+ * rows, along its columns, or both in one pass over x:
+ *   q  [batch][rows][f8_pitch(cols)], q_scale  [batch][rows][f8_scale_pitch(cols)]
+ *   qt [batch][cols][f8_pitch(rows)], qt_scale [batch][cols][f8_scale_pitch(rows)]
+ * (qt: the transposed matrix, in blocks of 128 along rows). Each pair may be
+ * NULL, not both. For each block: e is the least integer >= -127 with
+ * |x| <= 2^e * (largest value of the format) for every finite x of the
+ * block (0 for a block with no finite nonzero value), the scale byte e + 127,
+ * and q = x * 2^-e rounded to nearest even. NaN gives NaN; an infinity gives
+ * NaN in E4M3 and itself in E5M2. Padding bytes of q and qt are written as
+ * zeros, padding scale bytes as 127.
+ */
+int signmuon_f8_quant(const void *x, signmuon_dtype x_dtype, int32_t batch, int64_t rows,
+                      int64_t cols, signmuon_f8 format, void *q, uint8_t *q_scale, void *qt,
+                      uint8_t *qt_scale, signmuon_stream stream);
+
+size_t signmuon_f8_pitch(int64_t k);
+size_t signmuon_f8_scale_pitch(int64_t k);
+
+/*
+ * signmuon_f8_matmul -- out[i][r][c] = sum over k of a[i][r][k] * b[i][c][k]
+ * of the values that the operands stand for, accumulated in fp32 on the matrix
+ * cores and rounded once to out_dtype. a is [batch][m] rows of k values, b
+ * [batch][n] rows, or [n] rows shared by every i (b_shared = 1), both laid out
+ * and padded as signmuon_f8_quant writes them (the bytes past k must be zero);
+ * out is [batch][m][n]. For a linear layer y = x w^T with w [n][k]: the output
+ * takes x and w by rows; the input's gradient dy by rows and w by columns; the
+ * weight's gradient of each worker dy and x by columns, batch = workers, which
+ * fills signmuon_matrix.grad. workspace:
+ * signmuon_f8_matmul_workspace_bytes(batch, m, n, k) bytes (may be 0, then NULL).
+ */
+int signmuon_f8_matmul(const void *a, const uint8_t *a_scale, signmuon_f8 a_format, const void *b,
+                       const uint8_t *b_scale, signmuon_f8 b_format, int32_t batch, int64_t m,
+                       int64_t n, int64_t k, int32_t b_shared, void *out, signmuon_dtype out_dtype,
+                       void *workspace, size_t workspace_bytes, signmuon_stream stream);
+
+/* Device workspace of signmuon_f8_matmul in bytes (0 on invalid arguments). */
+size_t signmuon_f8_matmul_workspace_bytes(int32_t batch, int64_t m, int64_t n, int64_t k);
 
 /* Text for a status code; for SIGNMUON_EHIP it names the HIP error of the
  * calling thread's last failure. Never NULL. */

@@ -100,7 +100,12 @@ def library() -> ctypes.CDLL:
             ("embedding_workspace_bytes", size, [i32, i64, i64, i64]),
             ("layer_norm", i32, [vp, i32, i64, i64, vp, vp, f32, vp, vp, vp, vp]),
             ("layer_norm_backward", i32, [vp, vp, i32, i32, i64, i64, vp, vp, vp, vp, vp, vp, i32, vp, size, vp]),
-            ("layer_norm_workspace_bytes", size, [i32, i64, i64])):
+            ("layer_norm_workspace_bytes", size, [i32, i64, i64]),
+            ("f8_quant", i32, [vp, i32, i32, i64, i64, i32, vp, vp, vp, vp, vp]),
+            ("f8_pitch", size, [i64]),
+            ("f8_scale_pitch", size, [i64]),
+            ("f8_matmul", i32, [vp, vp, i32, vp, vp, i32, i32, i64, i64, i64, i32, vp, i32, vp, size, vp]),
+            ("f8_matmul_workspace_bytes", size, [i32, i64, i64, i64])):
         fn = getattr(lib, "signmuon_" + name)
         fn.restype, fn.argtypes = result, args
     lib.signmuon_packed_words.restype = ctypes.c_size_t
@@ -552,3 +557,73 @@ def signmuon_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch
             _optional(dgamma, "dgamma", (grad,), shape), _optional(dbeta, "dbeta", (grad,), shape),
             _dtype_code(sums[0]) if sums else F32, *_space(workspace))
     _on(stream, library().signmuon_layer_norm_backward, args, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace)
+
+
+_F8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+_U8 = (torch.uint8,)
+
+
+def signmuon_f8_pitch(k: int) -> int:
+    return int(library().signmuon_f8_pitch(k))
+
+
+def signmuon_f8_scale_pitch(k: int) -> int:
+    return int(library().signmuon_f8_scale_pitch(k))
+
+
+def f8_empty(shape, dtype: torch.dtype, device):
+    """(values, scales) of an 8-bit operand of `shape`, blocks along the last
+    dimension: the buffers that signmuon_f8_quant fills."""
+    k = shape[-1]
+    return (torch.empty(tuple(shape[:-1]) + (signmuon_f8_pitch(k),), dtype=dtype, device=device),
+            torch.empty(tuple(shape[:-1]) + (signmuon_f8_scale_pitch(k),), dtype=torch.uint8, device=device))
+
+
+def _f8_operand(q, scale, name: str, lead, k: int):
+    """Address, scales' address and format of an 8-bit operand (None: not given)."""
+    if q is None and scale is None:
+        return None, None, None
+    if q is None or scale is None:
+        raise ValueError(f"{name}: values and scales go together")
+    return (_operand(q, name, _F8, lead + (signmuon_f8_pitch(k),)),
+            _operand(scale, name + "_scale", _U8, lead + (signmuon_f8_scale_pitch(k),)), _F8[q.dtype])
+
+
+def signmuon_f8_quant(x: torch.Tensor, q: Optional[torch.Tensor], q_scale: Optional[torch.Tensor],
+                      qt: Optional[torch.Tensor] = None, qt_scale: Optional[torch.Tensor] = None,
+                      stream=None) -> None:
+    """x [R][C] or [B][R][C] to 8 bits: q [..][R][pitch(C)] in blocks of 128
+    along the rows, qt [..][C][pitch(R)] the transposed matrix in blocks along
+    x's columns. Either pair may be None; both are of one format (the dtype)."""
+    shape = _rank(x, "x", (2, 3))
+    rows, cols = shape[-2:]
+    pq, ps, fmt = _f8_operand(q, q_scale, "q", shape[:-1], cols)
+    pt, pts, tfmt = _f8_operand(qt, qt_scale, "qt", shape[:-2] + (cols,), rows)
+    if fmt is not None and tfmt is not None and fmt != tfmt:
+        raise TypeError("q and qt: formats differ")
+    args = (_operand(x, "x", _ACT, x.shape), _dtype_code(x), shape[0] if len(shape) == 3 else 1, rows, cols,
+            tfmt if fmt is None else fmt, pq, ps, pt, pts)
+    if args[5] is None:
+        raise ValueError("neither q nor qt given")
+    _on(stream, library().signmuon_f8_quant, args, x, q, q_scale, qt, qt_scale)
+
+
+def signmuon_f8_matmul_workspace_bytes(batch: int, m: int, n: int, k: int) -> int:
+    return int(library().signmuon_f8_matmul_workspace_bytes(batch, m, n, k))
+
+
+def signmuon_f8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, k: int,
+                       out: torch.Tensor, workspace: Optional[torch.Tensor], stream=None) -> None:
+    """out [m][n] (or [B][m][n]) = a b^T over k values, of 8-bit operands as
+    signmuon_f8_quant writes them: a [..][m][pitch(k)], b [..][n][pitch(k)].
+    With a batch, b may be one matrix ([n] or [1][n] rows) for every entry."""
+    shape = _rank(out, "out", (2, 3))
+    m, n = shape[-2:]
+    lead = shape[:-2]
+    batch = lead[0] if lead else 1
+    pa, pas, fa = _f8_operand(a, a_scale, "a", lead + (m,), k)
+    one = lead and (b.dim() == 2 or (b.dim() == 3 and b.shape[0] == 1))
+    pb, pbs, fb = _f8_operand(b, b_scale, "b", tuple(b.shape[:-2]) + (n,) if one else lead + (n,), k)
+    args = (pa, pas, fa, pb, pbs, fb, batch, m, n, k, int(bool(one)), _operand(out, "out", _ACT, shape),
+            _dtype_code(out), *_space(workspace))
+    _on(stream, library().signmuon_f8_matmul, args, a, a_scale, b, b_scale, out, workspace)

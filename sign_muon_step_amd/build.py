@@ -13,7 +13,7 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libsignmuon.so")
 SOURCES = [os.path.join(HERE, "csrc", f) for f in (
     "api.hip", "elementwise.hip", "ns_gemm.hip", "spectral.hip", "grad_api.hip", "embedding.hip",
-    "layer_norm.hip")]
+    "layer_norm.hip", "f8_quant.hip", "f8_matmul.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

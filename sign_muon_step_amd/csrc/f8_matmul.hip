@@ -1,0 +1,493 @@
+// f8_matmul.hip -- products of 8-bit floating point operands with a
+// power-of-two scale for each block of 128, on the gfx950 matrix cores.
+//
+//   out[r][c] = sum over blocks b of 2^(ea[r][b] + eb[c][b]) sum over k in b of a[r][k] b[c][k]
+//
+// Two forms of the product, chosen by out's type:
+//  BF16  v_mfma_scale_f32_*_f8f6f4 on the bytes themselves. It takes a scale
+//        byte per lane, i.e. per row and 32 values, and applies 2^(byte - 127)
+//        itself: a block's byte serves the instructions of its 128 values, and
+//        no accumulator is touched in between. Before it adds in fp32 it cuts
+//        the products of each 8 consecutive k below 2^-13 of the power of two
+//        of the largest one (seen with one large and one small product, at
+//        every distance and place): 1.4e-5 of a sum of random products, far
+//        below BF16's 2^-8.
+//  F32   the bytes are converted to BF16 with their scale (exact: 4 bits of
+//        mantissa or less, and BF16 has fp32's exponents) and multiplied by
+//        v_mfma_f32_*_bf16, which adds with fp32's accuracy at half the rate
+//        (6e-9 of the same sums).
+// Sums are fp32 in both.
+//
+// The products are computed as b a^T: the instruction's rows are out's columns,
+// so that a lane's accumulators hold four consecutive columns of one row of
+// out.
+//
+// f8_tile_kernel: a workgroup computes a TILE x TILE tile from 64-byte slices
+// of both operands that stream from memory straight into LDS, kStages slices
+// deep. A slice's rows are 64 bytes, their 16-byte chunks XOR-swizzled so that
+// 16 consecutive rows' reads fall on all banks.
+// f8_rows_kernel: up to 64 rows of a. Bound by reading b once: no LDS on the
+// way, each wave reads whole 128-byte lines of b into the instruction's
+// layout, and the waves of a workgroup share k.
+// f8_sums_kernel: adds the parts of k that several workgroups computed.
+#include <type_traits>
+
+#include "grad_internal.h"
+
+namespace sm {
+namespace {
+
+constexpr int kWave = 64;
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ int first_lane(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ v8i join(u32x4 lo, u32x4 hi) {
+    return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+// 2^(byte - 127) of byte `shift / 8` of a dword of scales.
+__device__ __forceinline__ float scale_of(int scales, int shift) {
+    return __int_as_float(((scales >> shift) & 255) << 23);
+}
+
+// Bytes 8 i .. 8 i + 7 of a fragment as BF16, scaled.
+template <bool E5M2>
+__device__ __forceinline__ bf16x8 widen(const v8i &f, int i, float scale) {
+    bf16x2 v[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const unsigned w = (unsigned)f[2 * i + j];
+        if (E5M2) {
+            v[2 * j] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, scale, false);
+            v[2 * j + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, scale, true);
+        } else {
+            v[2 * j] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false);
+            v[2 * j + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true);
+        }
+    }
+    return bf16x8{v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
+}
+
+// Four consecutive columns of out.
+__device__ __forceinline__ void store_out(const F8Matmul &f, int64_t at, int have, const float (&v)[4]) {
+    if (f.out_bf16)
+        store_n<true>(f.out, at, have, v);
+    else
+        store_n<false>(f.out, at, have, v);
+}
+
+// ---------------------------------------------------------------------------
+// Tiles
+// ---------------------------------------------------------------------------
+constexpr int kSliceBytes = 64;  // bytes, i.e. values, of k per row and slice
+constexpr int kStages = 4;
+
+// s_waitcnt with vmcnt = N, lgkmcnt = 0, behind every LDS read before it.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+}
+
+// Workgroup barrier that does not wait for the loads into LDS still in flight.
+__device__ __forceinline__ void barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+constexpr uint32_t kOutside = 0x80000000u;  // buffer offset beyond every extent: loads zeros
+
+// A load of 16 (or 4) bytes a lane straight into LDS at lds + 16 (4) * lane.
+// Asm without outputs, so that the compiler does not order every LDS read
+// behind the loads in flight; M0 is reserved, and nothing else here reads it.
+__device__ __forceinline__ void load16_lds(uint32_t lds, uint32_t offset, u32x4 buffer) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(offset), "s"(buffer)
+                 : "memory");
+}
+__device__ __forceinline__ void load4_lds(uint32_t lds, uint32_t offset, u32x4 buffer) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(offset), "s"(buffer)
+                 : "memory");
+}
+
+// A raw buffer over `bytes` bytes (below 2^31) from p on.
+__device__ __forceinline__ u32x4 make_buffer(const uint8_t *p, int64_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    return u32x4{(uint32_t)first_lane((int)(uint32_t)a), (uint32_t)first_lane((int)((uint32_t)(a >> 32) & 0xffffu)),
+                 (uint32_t)first_lane((int)bytes), 0x00020000u};
+}
+
+// LDS byte of 16-byte chunk c of a slice's row r.
+__device__ __forceinline__ uint32_t slice_at(int r, int c) {
+    return (uint32_t)(r * kSliceBytes + ((c ^ ((r >> 2) & 3)) << 4));
+}
+
+// One operand's rows of a tile (ROWS rows of which `valid` exist) on their way
+// into LDS, by WAVES waves. base: the tile's first row at the k of slice 0.
+template <int ROWS, int WAVES>
+struct Slices {
+    static constexpr int kLoads = ROWS * kSliceBytes / 1024 / WAVES;  // per wave and slice
+    static_assert(kLoads * WAVES * 1024 == ROWS * kSliceBytes, "whole loads");
+    u32x4 buffer;
+    uint32_t offset[kLoads];
+    int slices;
+
+    __device__ __forceinline__ void init(const uint8_t *base, int64_t pitch, int valid, int slices_, int wave, int lane) {
+        slices = slices_;
+        // rows past the last one start beyond the buffer's end, which is the end of the last row's slices
+        buffer = make_buffer(base, (valid - 1) * pitch + (int64_t)slices_ * kSliceBytes);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int row = (i * WAVES + wave) * 16 + lane / 4;
+            const int chunk = (lane & 3) ^ ((row >> 2) & 3);
+            offset[i] = row < valid ? (uint32_t)(row * pitch + chunk * 16) : kOutside;
+        }
+    }
+    // Load i of slice j to `lds` (of the slice's first row); zeros past the last slice.
+    __device__ __forceinline__ void issue(int j, int i, uint32_t lds, int wave) const {
+        load16_lds(lds + (uint32_t)(i * WAVES + wave) * 1024u,
+                   j < slices && offset[i] != kOutside ? offset[i] + (uint32_t)j * kSliceBytes : kOutside, buffer);
+    }
+};
+
+template <int TILE> struct TileShape;
+template <> struct TileShape<256> { static constexpr int kWavesM = 2, kWavesN = 4; };
+template <> struct TileShape<128> { static constexpr int kWavesM = 2, kWavesN = 2; };
+
+// Blocks go to the 8 XCDs round-robin: each XCD gets a contiguous run of tiles.
+__device__ __forceinline__ int xcd_run(int b, int n) {
+    const int q = n >> 3, rem = n & 7, x = b & 7, p = b >> 3;
+    return x * q + (x < rem ? x : rem) + p;
+}
+
+template <int TILE, bool A5, bool B5, bool F32>
+__global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN *kWave) void f8_tile_kernel(F8Matmul f) {
+    using S = TileShape<TILE>;
+    constexpr int kWaves = S::kWavesM * S::kWavesN;
+    constexpr int FM = TILE / S::kWavesM / 32, FN = TILE / S::kWavesN / 32;  // 32 x 32 blocks of a wave
+    constexpr int kOperand = TILE * kSliceBytes, kStage = 2 * kOperand;
+    constexpr int kScaleLds = kStages * kStage, kScaleStage = 2 * TILE * 4;
+    __shared__ __attribute__((aligned(1024))) char lds[kScaleLds + 2 * kScaleStage];
+    const int lane = threadIdx.x & (kWave - 1), wave = first_lane(threadIdx.x / kWave);
+
+    // batch and part of k, then tiles in bands of 8 rows of tiles, down the
+    // band first: the tiles that run at once share operands in L2
+    const int tm = (int)((f.m + TILE - 1) / TILE), tn = (int)((f.n + TILE - 1) / TILE);
+    int t = xcd_run(blockIdx.x, gridDim.x);
+    const int per = tm * tn, unit = t / per;
+    t -= unit * per;
+    const int band = t / (8 * tn), rows_left = tm - band * 8 < 8 ? tm - band * 8 : 8;
+    t -= band * 8 * tn;
+    const int64_t row0 = (int64_t)(band * 8 + t % rows_left) * TILE, col0 = (int64_t)(t / rows_left) * TILE;
+    const int64_t batch = unit / f.splits;
+    const int split = unit % f.splits;
+    const int block0 = split * f.chunk;
+    const int blocks = f.blocks - block0 < f.chunk ? f.blocks - block0 : f.chunk;
+    const int slices = blocks * (kF8Block / kSliceBytes);
+
+    const int valid_m = (int)(f.m - row0 < TILE ? f.m - row0 : TILE), valid_n = (int)(f.n - col0 < TILE ? f.n - col0 : TILE);
+    Slices<TILE, kWaves> la, lb;
+    la.init(f.a + batch * f.a_stride + row0 * f.pitch + (int64_t)block0 * kF8Block, f.pitch, valid_m, slices, wave, lane);
+    lb.init(f.b + batch * f.b_stride + col0 * f.pitch + (int64_t)block0 * kF8Block, f.pitch, valid_n, slices, wave, lane);
+    // scales: wave w loads the dwords of rows 64 w .. of a's rows, then b's
+    static_assert(kWaves * kWave == 2 * TILE, "one scale load per lane");
+    const bool scale_b = wave >= kWaves / 2;
+    const int srow = (scale_b ? wave - kWaves / 2 : wave) * kWave + lane;
+    const int svalid = scale_b ? valid_n : valid_m;
+    const uint8_t *sbase = (scale_b ? f.b_scale + batch * f.bs_stride + col0 * f.scale_pitch
+                                    : f.a_scale + batch * f.as_stride + row0 * f.scale_pitch) + block0;
+    const int dwords = (blocks + 3) / 4;
+    const u32x4 sbuffer = make_buffer(sbase, (svalid - 1) * f.scale_pitch + dwords * 4);
+    const uint32_t soffset = srow < svalid ? (uint32_t)(srow * f.scale_pitch) : kOutside;
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(
+        (__attribute__((address_space(3))) char *)lds);
+    auto load_scales = [&](int g) {
+        load4_lds(lds0 + kScaleLds + (g & 1) * kScaleStage + wave * 256u,
+                  g < dwords && soffset != kOutside ? soffset + (uint32_t)g * 4 : kOutside, sbuffer);
+    };
+
+    constexpr int kLoads = 2 * Slices<TILE, kWaves>::kLoads;
+    auto issue = [&](int j, int i) {  // load i of slice j, of both operands
+        const uint32_t at = lds0 + (uint32_t)(j % kStages) * kStage;
+        if (i < kLoads / 2)
+            la.issue(j, i, at, wave);
+        else
+            lb.issue(j, i - kLoads / 2, at + kOperand, wave);
+    };
+    load_scales(0);
+#pragma unroll
+    for (int j = 0; j < kStages; ++j)
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) issue(j, i);
+
+    const int wm = wave / S::kWavesN * FM * 32, wn = wave % S::kWavesN * FN * 32;
+    const int row = lane & 31, half = lane >> 5;
+    // 32 bytes of a row: the lane's half of the slice
+    auto fragment = [&](const char *operand, int r) {
+        return join(*reinterpret_cast<const u32x4 *>(operand + slice_at(r + row, 2 * half)),
+                    *reinterpret_cast<const u32x4 *>(operand + slice_at(r + row, 2 * half + 1)));
+    };
+    f32x16 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
+    v8i fa[FM], fb[2][FN];
+    int sa[FM], sb[FN];
+
+    wait_loads<(kStages - 1) * kLoads>();  // slice 0 and the first scales
+    barrier();
+#pragma unroll
+    for (int i = 0; i < FM; ++i) fa[i] = fragment(lds, wm + i * 32);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) fb[0][j] = fragment(lds + kOperand, wn + j * 32);
+
+    // Slice j's products, from the registers. Meanwhile slice j + 1 is read
+    // (a's blocks into the registers that their products leave) and slice
+    // j + kStages is loaded to the place that slice j, now in every wave's
+    // registers, leaves in LDS.
+    auto slice = [&](int j, auto parity, int shift) {
+        constexpr int P = decltype(parity)::value;
+        wait_loads<(kStages - 2) * kLoads>();  // slice j + 1 has landed
+        barrier();
+        const char *next = lds + (j + 1) % kStages * kStage;
+        int step = 0;
+        if constexpr (F32) {
+            float xa[FM], xb[FN];
+#pragma unroll
+            for (int i = 0; i < FM; ++i) xa[i] = scale_of(sa[i], shift);
+#pragma unroll
+            for (int n = 0; n < FN; ++n) xb[n] = scale_of(sb[n], shift);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {  // 16 k each: bytes 8 q of both halves
+                bf16x8 wa[FM], wb[FN];
+#pragma unroll
+                for (int n = 0; n < FN; ++n) wb[n] = widen<B5>(fb[P][n], q, xb[n]);
+#pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    wa[i] = widen<A5>(fa[i], q, xa[i]);
+                    if (q == 3) fa[i] = fragment(next, wm + i * 32);
+#pragma unroll
+                    for (int n = 0; n < FN; ++n) {
+                        acc[i][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[n], wa[i], acc[i][n], 0, 0, 0);
+                        if (step < FN) fb[1 - P][step] = fragment(next + kOperand, wn + step * 32);
+                        if (step < kLoads) issue(j + kStages, step);
+                        ++step;
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+#pragma unroll
+            for (int n = 0; n < FN; ++n) {
+                acc[i][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    fb[P][n], fa[i], acc[i][n], B5 ? 1 : 0, A5 ? 1 : 0, 0, sb[n] >> shift, 0, sa[i] >> shift);
+                if (step < FN) fb[1 - P][step] = fragment(next + kOperand, wn + step * 32);
+                if (step < kLoads) issue(j + kStages, step);
+                ++step;
+            }
+            fa[i] = fragment(next, wm + i * 32);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    for (int b = 0; b < blocks; ++b) {
+        if ((b & 3) == 0) {  // the scales of four blocks
+            const char *s = lds + kScaleLds + (b >> 2 & 1) * kScaleStage;
+#pragma unroll
+            for (int i = 0; i < FM; ++i) sa[i] = *reinterpret_cast<const int *>(s + (wm + i * 32 + row) * 4);
+#pragma unroll
+            for (int n = 0; n < FN; ++n) sb[n] = *reinterpret_cast<const int *>(s + (TILE + wn + n * 32 + row) * 4);
+            load_scales((b >> 2) + 1);
+        }
+        slice(2 * b, std::integral_constant<int, 0>{}, (b & 3) * 8);
+        slice(2 * b + 1, std::integral_constant<int, 1>{}, (b & 3) * 8);
+    }
+    wait_loads<0>();  // loads past the end write LDS too
+
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int64_t r = row0 + wm + i * 32 + row;
+        if (r >= f.m) continue;
+#pragma unroll
+        for (int n = 0; n < FN; ++n)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int64_t c = col0 + wn + n * 32 + g * 8 + half * 4;
+                const int have = (int)(f.n - c < 4 ? f.n - c : 4);
+                const float v[4] = {acc[i][n][4 * g], acc[i][n][4 * g + 1], acc[i][n][4 * g + 2], acc[i][n][4 * g + 3]};
+                if (f.splits > 1)
+                    store_n<false>(f.partial, ((split * (int64_t)f.batch + batch) * f.m + r) * f.n + c, have, v);
+                else
+                    store_out(f, (batch * f.m + r) * f.n + c, have, v);
+            }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows
+// ---------------------------------------------------------------------------
+// 16 columns of out and up to 16 MF rows. A wave takes every waves-th group of
+// four blocks of k.
+template <int MF, bool A5, bool B5, bool F32>
+__global__ __launch_bounds__(512) void f8_rows_kernel(F8Matmul f) {
+    extern __shared__ __attribute__((aligned(16))) float sums[];  // [waves][MF][64][4]
+    const int lane = threadIdx.x & (kWave - 1), wave = first_lane(threadIdx.x / kWave);
+    const int tn = (int)((f.n + 15) / 16);
+    const int64_t batch = blockIdx.x / tn, col0 = (int64_t)(blockIdx.x % tn) * 16;
+    const int row = lane & 15, part = lane >> 4;
+    // rows past the last one read the last one: their products are not written
+    const int64_t col = col0 + row < f.n ? col0 + row : f.n - 1;
+    const uint8_t *b = f.b + batch * f.b_stride + col * f.pitch + part * 32;
+    const uint8_t *bs = f.b_scale + batch * f.bs_stride + col * f.scale_pitch;
+    const uint8_t *a[MF], *as[MF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+        const int64_t r = i * 16 + row < f.m ? i * 16 + row : f.m - 1;
+        a[i] = f.a + batch * f.a_stride + r * f.pitch + part * 32;
+        as[i] = f.a_scale + batch * f.as_stride + r * f.scale_pitch;
+    }
+    f32x4 acc[MF] = {};
+    const int groups = (f.blocks + 3) / 4;
+    for (int g = wave; g < groups; g += f.waves) {
+        const int left = f.blocks - g * 4;  // blocks of this group
+        const int sb = *reinterpret_cast<const int *>(bs + g * 4);
+        int sa[MF];
+#pragma unroll
+        for (int i = 0; i < MF; ++i) sa[i] = *reinterpret_cast<const int *>(as[i] + g * 4);
+        v8i fb[4], fa[4][MF];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t at = (int64_t)(g * 4 + (k < left ? k : 0)) * kF8Block;
+            fb[k] = join(*reinterpret_cast<const u32x4 *>(b + at), *reinterpret_cast<const u32x4 *>(b + at + 16));
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+                fa[k][i] = join(*reinterpret_cast<const u32x4 *>(a[i] + at), *reinterpret_cast<const u32x4 *>(a[i] + at + 16));
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < left)
+#pragma unroll
+                for (int i = 0; i < MF; ++i) {
+                    if constexpr (F32) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                widen<B5>(fb[k], q, scale_of(sb, 8 * k)), widen<A5>(fa[k][i], q, scale_of(sa[i], 8 * k)),
+                                acc[i], 0, 0, 0);
+                    } else {
+                        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            fb[k], fa[k][i], acc[i], B5 ? 1 : 0, A5 ? 1 : 0, 0, sb >> (8 * k), 0, sa[i] >> (8 * k));
+                    }
+                }
+    }
+#pragma unroll
+    for (int i = 0; i < MF; ++i) *reinterpret_cast<f32x4 *>(sums + ((wave * MF + i) * kWave + lane) * 4) = acc[i];
+    __syncthreads();
+    for (int t = threadIdx.x; t < MF * kWave; t += f.waves * kWave) {
+        const int l = t & (kWave - 1);
+        f32x4 v = {};
+        for (int w = 0; w < f.waves; ++w) v += *reinterpret_cast<const f32x4 *>(sums + (w * MF * kWave + t) * 4);
+        // lane l: row l % 16 of the block's rows, columns 4 (l / 16) on
+        const int64_t r = t / kWave * 16 + (l & 15), c = col0 + (l >> 4) * 4;
+        const float o[4] = {v[0], v[1], v[2], v[3]};
+        if (r < f.m) store_out(f, (batch * f.m + r) * f.n + c, (int)(f.n - c < 4 ? f.n - c : 4), o);
+    }
+}
+
+// out = the splits' sums, in order; 4 entries a thread of the flat array.
+__global__ __launch_bounds__(256) void f8_sums_kernel(F8Matmul f) {
+    const int64_t total = f.batch * f.m * f.n;
+    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (at >= total) return;
+    const int have = (int)(total - at < 4 ? total - at : 4);
+    float v[4] = {};
+    for (int s = 0; s < f.splits; ++s) {
+        float p[4];
+        load_n<false>(f.partial, s * total + at, have, p);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += p[j];
+    }
+    store_out(f, at, have, v);
+}
+
+template <bool A5, bool B5, bool F32>
+void launch(const F8Matmul &f, hipStream_t s) {
+    if (f.tile == 16) {
+        const dim3 grid((unsigned)(f.batch * ((f.n + 15) / 16)));
+        const int threads = f.waves * kWave;
+        const int mf = f.m <= 16 ? 1 : f.m <= 32 ? 2 : 4;
+        const size_t lds = (size_t)mf * threads * 16;
+        if (mf == 1)
+            f8_rows_kernel<1, A5, B5, F32><<<grid, threads, lds, s>>>(f);
+        else if (mf == 2)
+            f8_rows_kernel<2, A5, B5, F32><<<grid, threads, lds, s>>>(f);
+        else
+            f8_rows_kernel<4, A5, B5, F32><<<grid, threads, lds, s>>>(f);
+        return;
+    }
+    const int64_t tiles = (f.m + f.tile - 1) / f.tile * ((f.n + f.tile - 1) / f.tile);
+    const dim3 grid((unsigned)(tiles * f.batch * f.splits));
+    if (f.tile == 256)
+        f8_tile_kernel<256, A5, B5, F32><<<grid, 512, 0, s>>>(f);
+    else
+        f8_tile_kernel<128, A5, B5, F32><<<grid, 256, 0, s>>>(f);
+}
+
+template <bool F32>
+void launch_out(const F8Matmul &f, hipStream_t s) {
+    if (f.a_e5m2)
+        f.b_e5m2 ? launch<true, true, F32>(f, s) : launch<true, false, F32>(f, s);
+    else
+        f.b_e5m2 ? launch<false, true, F32>(f, s) : launch<false, false, F32>(f, s);
+}
+
+}  // namespace
+
+F8Plan f8_plan(int64_t batch, int64_t m, int64_t n, int64_t k) {
+    const int64_t blocks = f8_pitch(k) / kF8Block, groups = (blocks + 3) / 4;
+    F8Plan p{};
+    p.splits = 1;
+    p.chunk = (int32_t)(groups * 4);
+    if (m <= 64) {
+        p.tile = 16;
+        const int64_t wgs = batch * ((n + 15) / 16);
+        p.waves = 4;
+        while (p.waves < 8 && p.waves < groups && wgs * p.waves < 2048) p.waves *= 2;
+        return p;
+    }
+    auto tiles = [&](int64_t t) { return batch * ((m + t - 1) / t) * ((n + t - 1) / t); };
+    p.tile = tiles(256) >= 192 ? 256 : 128;
+    // parts of k until every compute unit has a workgroup, at least 4 blocks each
+    const int64_t want = p.tile == 256 ? 256 : 512, have = tiles(p.tile);
+    int64_t splits = have >= want ? 1 : want / have;
+    if (splits > groups) splits = groups;
+    p.chunk = (int32_t)((groups + splits - 1) / splits * 4);
+    p.splits = (int32_t)((blocks + p.chunk - 1) / p.chunk);
+    return p;
+}
+
+void launch_f8_matmul(const F8Matmul &f, hipStream_t s) {
+    if (f.out_bf16)
+        launch_out<false>(f, s);
+    else
+        launch_out<true>(f, s);
+}
+
+void launch_f8_sums(const F8Matmul &f, hipStream_t s) {
+    const int64_t total = f.batch * f.m * f.n;
+    f8_sums_kernel<<<dim3((unsigned)((total + 1023) / 1024)), 256, 0, s>>>(f);
+}
+
+}  // namespace sm

@@ -68,6 +68,28 @@ size_t norm_workspace(int32_t workers, int64_t rows, int64_t cols) {
     return parts > 1 ? (size_t)((int64_t)workers * parts * 2 * cols) * sizeof(float) : 0;
 }
 
+// ---------------------------------------------------------------------------
+// 8-bit floating point
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxK = (int64_t)1 << 22;  // a tile's rows of operands lie within 2^31 bytes
+constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;  // of a launch
+
+inline bool f8_ok(int f) { return f == SIGNMUON_E4M3 || f == SIGNMUON_E5M2; }
+
+int check_f8_matmul(int64_t batch, int64_t m, int64_t n, int64_t k) {
+    if (batch < 1 || m < 1 || n < 1 || k < 1) return SIGNMUON_EINVAL;
+    if (batch > kMaxWorkers || m > kMaxTokens || n > kMaxTokens || k > kMaxK) return SIGNMUON_ERANGE;
+    const sm::F8Plan p = sm::f8_plan(batch, m, n, k);
+    if (p.tile == 16) return batch * ((n + 15) / 16) * p.waves * 64 > kMaxThreads ? SIGNMUON_ERANGE : SIGNMUON_OK;
+    const int64_t tiles = ((m + p.tile - 1) / p.tile) * ((n + p.tile - 1) / p.tile);
+    return tiles * batch * p.splits * 2 * p.tile > kMaxThreads ? SIGNMUON_ERANGE : SIGNMUON_OK;
+}
+
+size_t f8_workspace(int64_t batch, int64_t m, int64_t n, int64_t k) {
+    const sm::F8Plan p = sm::f8_plan(batch, m, n, k);
+    return p.splits > 1 ? (size_t)(p.splits * batch * m * n) * sizeof(float) : 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -206,6 +228,94 @@ int signmuon_layer_norm_backward(const void *dy, const void *x, signmuon_dtype x
     if (int rc = sm::launch_status()) return rc;
     if (n.parts == 1 || (!dgamma && !dbeta)) return SIGNMUON_OK;
     sm::launch_layer_norm_sums(n, st);
+    return sm::launch_status();
+}
+
+size_t signmuon_f8_pitch(int64_t k) { return k < 1 ? 0 : (size_t)sm::f8_pitch(k); }
+
+size_t signmuon_f8_scale_pitch(int64_t k) { return k < 1 ? 0 : (size_t)sm::f8_scale_pitch(k); }
+
+int signmuon_f8_quant(const void *x, signmuon_dtype x_dtype, int32_t batch, int64_t rows,
+                      int64_t cols, signmuon_f8 format, void *q, uint8_t *q_scale, void *qt,
+                      uint8_t *qt_scale, signmuon_stream stream) {
+    if (!x || (!q && !qt) || !q != !q_scale || !qt != !qt_scale) return SIGNMUON_EINVAL;
+    if (batch < 1 || rows < 1 || cols < 1) return SIGNMUON_EINVAL;
+    if (batch > kMaxWorkers || rows > kMaxTokens || cols > kMaxTokens) return SIGNMUON_ERANGE;
+    const int64_t row_tiles = (rows + 127) / 128, col_tiles = (cols + 127) / 128;
+    if (batch * row_tiles * col_tiles * 256 > kMaxThreads) return SIGNMUON_ERANGE;
+    if (!dtype_ok(x_dtype) || !f8_ok(format)) return SIGNMUON_EDTYPE;
+    if (!all_aligned(x, q, q_scale, qt, qt_scale)) return SIGNMUON_EALIGN;
+    sm::F8Quant f{};
+    f.x = x;
+    f.q = static_cast<uint8_t *>(q);
+    f.q_scale = q_scale;
+    f.qt = static_cast<uint8_t *>(qt);
+    f.qt_scale = qt_scale;
+    f.rows = rows;
+    f.cols = cols;
+    f.pitch = sm::f8_pitch(cols);
+    f.scale_pitch = sm::f8_scale_pitch(cols);
+    f.tpitch = sm::f8_pitch(rows);
+    f.tscale_pitch = sm::f8_scale_pitch(rows);
+    f.batch = batch;
+    f.row_tiles = (int32_t)row_tiles;
+    f.col_tiles = (int32_t)col_tiles;
+    f.bf16 = x_dtype == SIGNMUON_BF16;
+    f.e5m2 = format == SIGNMUON_E5M2;
+    sm::launch_f8_quant(f, static_cast<hipStream_t>(stream));
+    return sm::launch_status();
+}
+
+size_t signmuon_f8_matmul_workspace_bytes(int32_t batch, int64_t m, int64_t n, int64_t k) {
+    if (check_f8_matmul(batch, m, n, k) != SIGNMUON_OK) return 0;
+    return f8_workspace(batch, m, n, k);
+}
+
+int signmuon_f8_matmul(const void *a, const uint8_t *a_scale, signmuon_f8 a_format, const void *b,
+                       const uint8_t *b_scale, signmuon_f8 b_format, int32_t batch, int64_t m,
+                       int64_t n, int64_t k, int32_t b_shared, void *out, signmuon_dtype out_dtype,
+                       void *workspace, size_t workspace_bytes, signmuon_stream stream) {
+    if (!a || !a_scale || !b || !b_scale || !out || (b_shared != 0 && b_shared != 1)) return SIGNMUON_EINVAL;
+    if (int rc = check_f8_matmul(batch, m, n, k)) return rc;
+    if (!f8_ok(a_format) || !f8_ok(b_format) || !dtype_ok(out_dtype)) return SIGNMUON_EDTYPE;
+    if (!all_aligned(a, a_scale, b, b_scale, out)) return SIGNMUON_EALIGN;
+    // rows of a shared b are one product: fuller tiles
+    if (b_shared && batch > 1 && batch * m <= kMaxTokens && check_f8_matmul(1, batch * m, n, k) == SIGNMUON_OK &&
+        f8_workspace(1, batch * m, n, k) <= f8_workspace(batch, m, n, k)) {
+        m *= batch;
+        batch = 1;
+    }
+    if (int rc = check_workspace(workspace, workspace_bytes, f8_workspace(batch, m, n, k))) return rc;
+    const sm::F8Plan p = sm::f8_plan(batch, m, n, k);
+    sm::F8Matmul f{};
+    f.a = static_cast<const uint8_t *>(a);
+    f.a_scale = a_scale;
+    f.b = static_cast<const uint8_t *>(b);
+    f.b_scale = b_scale;
+    f.out = out;
+    f.partial = static_cast<float *>(workspace);
+    f.m = m;
+    f.n = n;
+    f.pitch = sm::f8_pitch(k);
+    f.scale_pitch = sm::f8_scale_pitch(k);
+    f.a_stride = m * f.pitch;
+    f.as_stride = m * f.scale_pitch;
+    f.b_stride = b_shared ? 0 : n * f.pitch;
+    f.bs_stride = b_shared ? 0 : n * f.scale_pitch;
+    f.batch = batch;
+    f.blocks = (int32_t)(f.pitch / sm::kF8Block);
+    f.splits = p.splits;
+    f.chunk = p.chunk;
+    f.tile = p.tile;
+    f.waves = p.waves;
+    f.a_e5m2 = a_format == SIGNMUON_E5M2;
+    f.b_e5m2 = b_format == SIGNMUON_E5M2;
+    f.out_bf16 = out_dtype == SIGNMUON_BF16;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    sm::launch_f8_matmul(f, st);
+    if (int rc = sm::launch_status()) return rc;
+    if (f.splits == 1) return SIGNMUON_OK;
+    sm::launch_f8_sums(f, st);
     return sm::launch_status();
 }
 

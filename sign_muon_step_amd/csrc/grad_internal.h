@@ -88,6 +88,46 @@ void launch_layer_norm_backward(const NormGrad &n, hipStream_t s);
 void launch_layer_norm_sums(const NormGrad &n, hipStream_t s);
 
 // ---------------------------------------------------------------------------
+// 8-bit floating point.
+// ---------------------------------------------------------------------------
+constexpr int kF8Block = 128;  // values per scale
+constexpr int kF8Zero = 127;   // scale byte of 2^0, and of padding
+inline int64_t f8_pitch(int64_t k) { return (k + kF8Block - 1) / kF8Block * kF8Block; }
+inline int64_t f8_scale_pitch(int64_t k) { return (f8_pitch(k) / kF8Block + 3) / 4 * 4; }
+
+struct F8Quant {
+    const void *x;
+    uint8_t *q, *q_scale, *qt, *qt_scale;  // q or qt may be null
+    int64_t rows, cols;
+    int64_t pitch, scale_pitch;      // of q: a row's bytes
+    int64_t tpitch, tscale_pitch;    // of qt
+    int32_t batch;
+    int32_t row_tiles, col_tiles;    // of 128
+    bool bf16, e5m2;
+};
+void launch_f8_quant(const F8Quant &f, hipStream_t s);
+
+struct F8Matmul {
+    const uint8_t *a, *a_scale, *b, *b_scale;
+    void *out;
+    float *partial;  // [splits][batch][m][n], unused where splits = 1
+    int64_t m, n, pitch, scale_pitch;
+    int64_t a_stride, b_stride, as_stride, bs_stride;  // bytes between batches (b's are 0 where it is shared)
+    int32_t batch, blocks;     // blocks: of 128 along k
+    int32_t splits, chunk;     // chunk: blocks of one split, a multiple of 4
+    int32_t tile;              // rows and columns of a workgroup's tile; 16: few rows
+    int32_t waves;             // tile 16: waves that share a tile's k
+    bool a_e5m2, b_e5m2, out_bf16;
+};
+struct F8Plan {
+    int32_t tile, splits, chunk, waves;
+};
+F8Plan f8_plan(int64_t batch, int64_t m, int64_t n, int64_t k);
+void launch_f8_matmul(const F8Matmul &f, hipStream_t s);
+// Adds the splits' sums (splits > 1).
+void launch_f8_sums(const F8Matmul &f, hipStream_t s);
+
+// ---------------------------------------------------------------------------
 // Device helpers
 // ---------------------------------------------------------------------------
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));

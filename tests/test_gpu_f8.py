@@ -1,0 +1,285 @@
+"""8-bit quantisation and products against plain implementations in 64 bits.
+
+Quantised bytes and scales are compared bit for bit: x times a power of two is
+exact, and the rounding to 8 bits is to nearest even. Products are compared with
+the 64-bit product of the values that the operands stand for."""
+import pytest
+import torch
+
+import sign_muon_step_amd as sm
+from gpu_util import announce
+from grad_util import DEV, HALF_STEP, TINY, Guarded, replays_like_eager, same_bits
+
+pytestmark = pytest.mark.gpu
+E4, E5 = torch.float8_e4m3fn, torch.float8_e5m2
+TOP = {E4: 448.0, E5: 57344.0}
+SMALLEST_NORMAL = {E4: 2.0 ** -6, E5: 2.0 ** -14}
+
+
+@pytest.fixture(autouse=True)
+def _name_the_case(request):
+    announce(f"[gpu-test] {request.node.nodeid}")
+    yield
+    torch.cuda.synchronize()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def up(n, to):
+    return (n + to - 1) // to * to
+
+
+def quantised(x, fmt):
+    """(bytes' values, scale bytes) of x [..., k] by the definition, on the CPU."""
+    k = x.shape[-1]
+    kp = up(k, 128)
+    x = torch.nn.functional.pad(x.double(), (0, kp - k)).unflatten(-1, (-1, 128))
+    size = torch.where(x.isfinite(), x.abs(), 0.0).amax(-1)
+    e = torch.full_like(size, -127)
+    for p in range(-126, 129):  # the least e whose block fits
+        e = torch.where(size > TOP[fmt] * 2.0 ** (p - 1), p, e)
+    e = torch.where(size == 0, 0, e)
+    q = (x * torch.exp2(-e).unsqueeze(-1)).flatten(-2).float().to(fmt)
+    s = torch.full(x.shape[:-2] + (up(kp // 128, 4),), 127, dtype=torch.uint8)
+    s[..., :kp // 128] = (e + 127).to(torch.uint8)
+    return q, s
+
+
+def same_values(a, b):
+    """Equal 8-bit values (signs of zeros too); any NaN equals any NaN."""
+    fa, fb = a.float(), b.float()
+    nan = fa.isnan() & fb.isnan()
+    return bool((nan | (a.view(torch.uint8) == b.view(torch.uint8))).all())
+
+
+def quantise(x, fmt, ways=(True, True)):
+    """The library's (q, scales), (qt, scales)."""
+    lead, (rows, cols) = tuple(x.shape[:-2]), x.shape[-2:]
+    out = []
+    for want, r, c in ((ways[0], rows, cols), (ways[1], cols, rows)):
+        out.append((Guarded(lead + (r, up(c, 128)), fmt), Guarded(lead + (r, up(up(c, 128) // 128, 4)), torch.uint8))
+                   if want else None)
+    args = [g.t for pair in out for g in (pair or ())]
+    if not ways[0]:
+        args = [None, None] + args
+    sm.signmuon_f8_quant(x.to(DEV), *args)
+    torch.cuda.synchronize()
+    for pair in out:
+        for g in pair or ():
+            g.check()
+    return out
+
+
+SIZES = [(1, 1), (1, 128), (2, 129), (3, 500), (127, 7), (128, 128), (129, 130), (200, 1030), (513, 64), (1, 2000),
+         (1700, 1)]
+
+
+@pytest.mark.parametrize("rows,cols", SIZES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("fmt", [E4, E5])
+@pytest.mark.parametrize("ways", [(True, True), (True, False), (False, True)])
+def test_quantisation(rows, cols, dtype, fmt, ways):
+    batch = 1 + rows % 3
+    g = gen(rows + cols)
+    x = torch.randn(batch, rows, cols, generator=g) * torch.exp(4 * torch.randn(batch, rows, cols, generator=g))
+    x = (x * torch.exp(8 * torch.randn(batch, rows, 1, generator=g))).to(dtype)
+    got = quantise(x, fmt, ways)
+    for pair, y in zip(got, (x, x.transpose(1, 2))):
+        if pair is not None:
+            q, s = quantised(y, fmt)
+            assert torch.equal(pair[1].t.cpu(), s)
+            assert same_values(pair[0].t.cpu(), q)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("fmt", [E4, E5])
+def test_quantisation_of_edges(dtype, fmt):
+    """Blocks at the format's border, ties, zeros, the smallest and largest
+    values, NaN and infinities."""
+    inf, nan = float("inf"), float("nan")
+    top = TOP[fmt]
+    rows = []
+    for p in (-130, -126, -60, 0, 1, 60, 110):
+        for t in (top, top * (1 + 2.0 ** -7), top * (1 + 2.0 ** -20), top * (1 - 2.0 ** -7), 1.0, 1.9, 1.75):
+            rows.append([t * 2.0 ** p] + [t * 2.0 ** (p - i / 7) * (-1) ** i for i in range(127)])
+    ties = [v + d for v in (1.0, 1.25, 1.5, 16.0, 2.0 ** -6, 2.0 ** -9, 2.0 ** -14, 2.0 ** -16) for d in
+            (0.0, v / 16, v / 8, 3 * v / 16, 3 * v / 8, v / 4, v / 2)]
+    rows.append([top] + ties + [-t for t in ties] + [0.0] * (127 - 2 * len(ties)))
+    rows += [[0.0] * 128, [-0.0] * 128, [1e-45] * 128, [3e38, -3e38] + [1.0] * 126, [nan] * 128, [inf, -inf] * 64,
+             [nan, inf, -inf, 1.0, -0.0] + [2.0 ** -i for i in range(123)], [2.0 ** -140, -2.0 ** -127] * 64]
+    x = torch.tensor(rows, dtype=torch.float64).to(torch.float32).to(dtype)
+    for y in (x, x.t().contiguous()):
+        got = quantise(y, fmt)
+        for pair, z in zip(got, (y, y.t())):
+            q, s = quantised(z, fmt)
+            assert torch.equal(pair[1].t.cpu(), s)
+            assert same_values(pair[0].t.cpu(), q)
+    assert 255 not in got[0][1].t.cpu()
+
+
+def operand(rows, k, fmt, seed, lead=()):
+    """Quantised random rows of different sizes, on the CPU, and their values."""
+    g = gen(seed)
+    x = torch.randn(lead + (rows, k), generator=g) * torch.exp(1.5 * torch.randn(lead + (rows, 1), generator=g))
+    q, s = quantised(x, fmt)
+    scale = torch.exp2(s[..., :q.shape[-1] // 128].double() - 127)
+    return q, s, (q.double().unflatten(-1, (-1, 128)) * scale.unsqueeze(-1)).flatten(-2), scale
+
+
+def size_of_groups(q, scale, fmt):
+    """A bound of the values' sizes as the 8-bit product sees them: subnormal
+    values count as the smallest normal one."""
+    v = q.double().abs()
+    v = torch.where(v > 0, v.clamp(min=SMALLEST_NORMAL[fmt]), 0.0)
+    return (v.unflatten(-1, (-1, 128)) * scale.unsqueeze(-1)).flatten(-2)
+
+
+def tolerance(out_dtype, a, b, fa, fb):
+    """[..][m][n]. fp32 sums of k products: 2^-23 of the sizes' sum for each of
+    the k additions (adders may cut where they do not round). BF16 results are
+    rounded (half a step), and before that the products of each 8 consecutive k
+    are cut below 2^-13 of their largest: 8 * 2^-13 of it at most."""
+    (qa, _, va, sa), (qb, _, vb, sb) = a, b
+    k = va.shape[-1]
+    size = va.abs() @ vb.abs().transpose(-1, -2)
+    tol = 2.0 ** -23 * k * size
+    if out_dtype == torch.bfloat16:
+        ga, gb = size_of_groups(qa, sa, fa), size_of_groups(qb, sb, fb)
+        for i in range(0, k, 8):
+            x, y = ga[..., i:i + 8], gb[..., i:i + 8]
+            if bool(x.any()):
+                # the largest product of a group is at most the product of the largest values at one k
+                tol = tol + 8 * 2.0 ** -13 * (x.unsqueeze(-2) * y.unsqueeze(-3)).amax(-1)
+    return tol
+
+
+def multiply(a, b, k, out_shape, out_dtype):
+    batch, (m, n) = (out_shape[0] if len(out_shape) == 3 else 1), out_shape[-2:]
+    out = Guarded(out_shape, out_dtype)
+    ws = Guarded((sm.signmuon_f8_matmul_workspace_bytes(batch, m, n, k),), torch.uint8)
+    sm.signmuon_f8_matmul(a[0].to(DEV), a[1].to(DEV), b[0].to(DEV), b[1].to(DEV), k, out.t,
+                          ws.t if ws.nbytes else None)
+    torch.cuda.synchronize()
+    out.check("out")
+    ws.check("workspace")
+    return out.t.cpu()
+
+
+def check_product(got, want, tol):
+    tol = tol + HALF_STEP[got.dtype] * (want.abs() + tol) + TINY
+    assert bool(((got.double() - want).abs() <= tol).all())
+
+
+# one row, few rows, rows around each kernel's border, several tiles, parts of k
+PRODUCTS = [(1, 1, 1), (1, 17, 128), (1, 300, 700), (5, 16, 129), (16, 33, 513), (17, 100, 2000), (33, 64, 640),
+            (64, 129, 1111), (65, 1, 5), (65, 200, 100), (127, 128, 128), (129, 257, 384), (200, 140, 3000),
+            (300, 90, 1537)]
+
+
+@pytest.mark.parametrize("m,n,k", PRODUCTS)
+@pytest.mark.parametrize("fa,fb", [(E4, E4), (E5, E4), (E4, E5), (E5, E5)])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_product(m, n, k, fa, fb, out_dtype):
+    a, b = operand(m, k, fa, m + k), operand(n, k, fb, n + k + 1)
+    got = multiply(a, b, k, (m, n), out_dtype)
+    check_product(got, a[2] @ b[2].t(), tolerance(out_dtype, a, b, fa, fb))
+
+
+@pytest.mark.parametrize("batch,m,n,k", [(3, 1, 40, 300), (2, 70, 130, 257), (5, 130, 200, 600), (2, 20, 19, 30)])
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_batches(batch, m, n, k, shared, out_dtype):
+    a = operand(m, k, E4, 1, (batch,))
+    b = operand(n, k, E4, 2, () if shared else (batch,))
+    got = multiply(a, b, k, (batch, m, n), out_dtype)
+    want = a[2] @ b[2].transpose(-1, -2)
+    b3 = tuple(t.expand((batch,) + t.shape) if t.dim() == 2 else t for t in b)
+    check_product(got, want, tolerance(out_dtype, a, b3, E4, E4))
+    if shared:  # one matrix as a batch of one
+        again = multiply(a, tuple(t.unsqueeze(0) for t in b), k, (batch, m, n), out_dtype)
+        assert same_bits(got, again)
+
+
+@pytest.mark.parametrize("m,n,k", [(3600, 3400, 640), (2047, 7169, 200)])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_large_tiles(m, n, k, out_dtype):
+    a, b = operand(m, k, E4, 5), operand(n, k, E5, 6)
+    got = multiply(a, b, k, (m, n), out_dtype).to(DEV).double()
+    va, vb = a[2].to(DEV), b[2].t().contiguous().to(DEV)
+    want, size = va @ vb, va.abs() @ vb.abs()
+    # of every group of 8, each product is at most the sizes' sum of its group
+    cut = 8 * 2.0 ** -13 if out_dtype == torch.bfloat16 else 0.0
+    ga, gb = size_of_groups(a[0], a[3], E4).to(DEV), size_of_groups(b[0], b[3], E5).t().contiguous().to(DEV)
+    tol = 2.0 ** -23 * k * size + cut * (ga @ gb)
+    tol = tol + HALF_STEP[out_dtype] * (want.abs() + tol) + TINY
+    assert bool(((got - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("m,n", [(1, 64), (40, 64), (200, 300)])
+def test_f32_products_keep_fp32(m, n):
+    """Errors of an F32 result, of random sign, add as their root: 2^-23 of the
+    result for each of about 2 k additions."""
+    k = 4096
+    a, b = operand(m, k, E4, 7), operand(n, k, E4, 8)
+    want = a[2] @ b[2].t()
+    got = multiply(a, b, k, (m, n), torch.float32).double()
+    row = (got - want).norm(dim=-1) / want.norm(dim=-1)
+    assert float(row.max()) <= 2.0 ** -23 * (2 * k) ** 0.5
+
+
+@pytest.mark.parametrize("m", [3, 150])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_nan_infinity_and_far_scales(m, out_dtype):
+    n, k = 70, 400
+    x, w = torch.randn(m, k, generator=gen(9)), torch.randn(n, k, generator=gen(10))
+    x[1, 5], w[3, 399] = float("nan"), float("inf")
+    x[2] *= 2.0 ** 90
+    w[7] *= 2.0 ** -80
+    pairs = []
+    for t, fmt in ((x, E5), (w, E5)):
+        (q, s), _ = quantise(t, fmt, (True, False))
+        pairs.append((q.t, s.t))
+    got = multiply(*pairs, k, (m, n), out_dtype).double()
+    qa, qb = quantised(x, E5), quantised(w, E5)
+    va, vb = ((q.double().unflatten(-1, (-1, 128)) * torch.exp2(s.double() - 127).unsqueeze(-1)).flatten(-2) for q, s in
+              ((qa[0], qa[1][:, :4]), (qb[0], qb[1][:, :4])))
+    want = va @ vb.t()
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.isinf(), want.isinf())
+    fine = want.isfinite()
+    size = torch.nan_to_num(va.abs(), nan=0.0) @ torch.nan_to_num(vb.abs(), nan=0.0, posinf=0.0).t()
+    tol = (2.0 ** -23 * k + 2.0 ** -10) * size + HALF_STEP[out_dtype] * want.abs()
+    assert bool(((got - want).abs()[fine] <= tol[fine]).all())
+
+
+def test_replays_and_streams_give_the_same_bits():
+    batch, rows, cols, outs = 2, 300, 260, 140
+    x = torch.empty(batch, rows, cols, dtype=torch.bfloat16, device=DEV)
+    w = torch.empty(outs, cols, device=DEV)
+    (q, s), (qt, st) = sm.f8_empty((batch, rows, cols), E4, DEV), sm.f8_empty((batch, cols, rows), E4, DEV)
+    qw, sw = sm.f8_empty((outs, cols), E4, DEV)
+    y = torch.empty(batch, rows, outs, dtype=torch.bfloat16, device=DEV)
+    gram = torch.empty(batch, cols, cols, device=DEV)
+    spaces = [sm.bytes_tensor(sm.signmuon_f8_matmul_workspace_bytes(*sizes), DEV) for sizes in
+              ((batch, rows, outs, cols), (batch, cols, cols, rows))]
+
+    def refresh(i):
+        x.copy_(torch.randn(batch, rows, cols, generator=gen(60 + i)))
+        w.copy_(torch.randn(outs, cols, generator=gen(70 + i)))
+
+    def call(stream=None):
+        sm.signmuon_f8_quant(x, q, s, qt, st, stream=stream)
+        sm.signmuon_f8_quant(w, qw, sw, stream=stream)
+        sm.signmuon_f8_matmul(q, s, qw, sw, cols, y, spaces[0], stream=stream)
+        sm.signmuon_f8_matmul(qt, st, qt, st, rows, gram, spaces[1], stream=stream)
+
+    outputs = [q.view(torch.uint8), s, qt.view(torch.uint8), st, y, gram]
+    replays_like_eager(call, outputs, refresh)
+    want = [t.clone() for t in outputs]
+    torch.cuda.synchronize()
+    call(torch.cuda.Stream())
+    torch.cuda.synchronize()
+    for a, b in zip(outputs, want):
+        assert same_bits(a, b)

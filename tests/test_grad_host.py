@@ -144,3 +144,81 @@ def test_layer_norm_binding_refuses_other_tensors():
         back(y, x, gamma, s, s, x, torch.zeros(2, 6), torch.zeros(2, 6).bfloat16(), None, workers=2)
     with pytest.raises(TypeError, match="dy"):
         back(y.bfloat16(), x, gamma, s, s, x, None, None, None)
+
+
+def test_f8_sizes():
+    assert [sm.signmuon_f8_pitch(k) for k in (0, 1, 127, 128, 129, 1000)] == [0, 128, 128, 128, 256, 1024]
+    assert [sm.signmuon_f8_scale_pitch(k) for k in (0, 1, 512, 513, 1024, 1025)] == [0, 4, 4, 8, 8, 12]
+    size = sm.signmuon_f8_matmul_workspace_bytes
+    assert size(0, 1, 1, 1) == size(1, 0, 1, 1) == size(1, 1, 0, 1) == size(1, 1, 1, 0) == 0
+    assert size(1, 8192, 2304, 768) == 0  # enough tiles: k stays whole
+    assert size(1, 128, 128, 8192) > 0    # one tile and a long k: in parts
+
+
+def test_f8_quant_arguments(lib):
+    names = "x x_dtype batch rows cols format q q_scale qt qt_scale stream".split()
+    good = [A, 0, 2, 10, 20, 0, A, A, A, A, None]
+    for change, status in [(dict(x=None), EINVAL), (dict(q=None), EINVAL), (dict(q_scale=None), EINVAL),
+                           (dict(qt=None), EINVAL), (dict(qt_scale=None), EINVAL),
+                           (dict(q=None, q_scale=None, qt=None, qt_scale=None), EINVAL), (dict(batch=0), EINVAL),
+                           (dict(rows=0), EINVAL), (dict(cols=-3), EINVAL), (dict(x_dtype=2), EDTYPE),
+                           (dict(format=2), EDTYPE), (dict(x=A + 2), EALIGN), (dict(q=A + 8), EALIGN),
+                           (dict(q_scale=A + 4), EALIGN), (dict(qt=A + 1), EALIGN), (dict(qt_scale=A + 4), EALIGN),
+                           (dict(batch=256), ERANGE), (dict(rows=(1 << 25) + 1), ERANGE), (dict(cols=1 << 40), ERANGE),
+                           (dict(rows=1 << 25, cols=1 << 14), ERANGE)]:
+        assert calls_with(lib.signmuon_f8_quant, names, good, **change) == status, change
+
+
+def test_f8_matmul_arguments(lib):
+    names = ("a a_scale a_format b b_scale b_format batch m n k b_shared out out_dtype workspace workspace_bytes "
+             "stream").split()
+    good = [A, A, 0, A, A, 1, 1, 128, 128, 8192, 0, A, 0, *WS, None]
+    need = sm.signmuon_f8_matmul_workspace_bytes(1, 128, 128, 8192)
+    for change, status in [(dict(a=None), EINVAL), (dict(a_scale=None), EINVAL), (dict(b=None), EINVAL),
+                           (dict(b_scale=None), EINVAL), (dict(out=None), EINVAL), (dict(batch=0), EINVAL),
+                           (dict(m=0), EINVAL), (dict(n=0), EINVAL), (dict(k=0), EINVAL), (dict(b_shared=2), EINVAL),
+                           (dict(a_format=2), EDTYPE), (dict(b_format=-1), EDTYPE), (dict(out_dtype=2), EDTYPE),
+                           (dict(a=A + 8), EALIGN), (dict(a_scale=A + 4), EALIGN), (dict(b=A + 4), EALIGN),
+                           (dict(b_scale=A + 1), EALIGN), (dict(out=A + 2), EALIGN), (dict(workspace=None), EWORKSPACE),
+                           (dict(workspace_bytes=need - 1), EWORKSPACE), (dict(workspace=WS[0] + 4), EALIGN),
+                           (dict(batch=256), ERANGE), (dict(m=(1 << 25) + 1), ERANGE), (dict(k=(1 << 22) + 1), ERANGE),
+                           (dict(m=1 << 25, n=1 << 25), ERANGE)]:
+        assert calls_with(lib.signmuon_f8_matmul, names, good, **change) == status, change
+
+
+def test_a_shared_operand_needs_no_more_workspace_than_asked():
+    """The rows of a batch with one b may run as one product, but only where the
+    workspace that was asked for the batch is enough."""
+    for batch, m, n, k in [(8, 16, 300, 4096), (3, 70, 128, 8192), (200, 1, 64, 2048), (2, 64, 64, 4096)]:
+        assert sm.signmuon_f8_matmul_workspace_bytes(batch, m, n, k) >= 0
+
+
+def test_f8_binding_refuses_other_tensors():
+    x = torch.zeros(3, 10, 20)
+    q, s = sm.f8_empty((3, 10, 20), torch.float8_e4m3fn, "cpu")
+    qt, st = sm.f8_empty((3, 20, 10), torch.float8_e4m3fn, "cpu")
+    with pytest.raises(ValueError, match="neither"):
+        sm.signmuon_f8_quant(x, None, None)
+    with pytest.raises(ValueError, match="go together"):
+        sm.signmuon_f8_quant(x, q, None)
+    with pytest.raises(TypeError, match="q:"):
+        sm.signmuon_f8_quant(x, q.view(torch.uint8), s)
+    with pytest.raises(ValueError, match="qt: shape"):
+        sm.signmuon_f8_quant(x, q, s, q, s)
+    with pytest.raises(TypeError, match="formats differ"):
+        sm.signmuon_f8_quant(x, q, s, qt.view(torch.float8_e5m2), st)
+    with pytest.raises(TypeError, match="x"):
+        sm.signmuon_f8_quant(x.half(), q, s)
+    with pytest.raises(ValueError, match="GPU memory"):
+        sm.signmuon_f8_quant(x, q, s, qt, st)
+    out = torch.zeros(3, 10, 10)
+    with pytest.raises(ValueError, match="a: shape"):
+        sm.signmuon_f8_matmul(q, s, q, s, 200, out, None)
+    with pytest.raises(ValueError, match="b: shape"):
+        sm.signmuon_f8_matmul(q, s, q[:2].contiguous(), s[:2].contiguous(), 20, out, None)
+    with pytest.raises(TypeError, match="out"):
+        sm.signmuon_f8_matmul(q, s, q, s, 20, out.half(), None)
+    with pytest.raises(TypeError, match="a_scale"):
+        sm.signmuon_f8_matmul(q, s.float(), q, s, 20, out, None)
+    with pytest.raises(ValueError, match="GPU memory"):
+        sm.signmuon_f8_matmul(q, s, q, s, 20, out, None)
