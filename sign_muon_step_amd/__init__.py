@@ -428,23 +428,24 @@ def workspace_tensor(mats: Sequence[Matrix], params: Params, device) -> Optional
 # a call lie on one GPU. The call runs on that GPU, on the given stream or on
 # that GPU's current one.
 # ---------------------------------------------------------------------------
-_ACT = (torch.float32, torch.bfloat16)
+_ACT = {torch.float32: F32, torch.bfloat16: BF16}
 _ITYPE = {torch.int32: 0, torch.int64: 1}
+_FP32 = (torch.float32,)
 
 
-def _operand(t: torch.Tensor, name: str, dtypes, shape) -> int:
+def _operand(t: torch.Tensor, name: str, dtypes, shape: tuple) -> int:
     """The address of a tensor of one of `dtypes` and exactly `shape`. Where it
     lies is for _on."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr()
 
 
-def _optional(t: Optional[torch.Tensor], name: str, dtypes, shape) -> Optional[int]:
+def _optional(t: Optional[torch.Tensor], name: str, dtypes, shape: tuple) -> Optional[int]:
     return None if t is None else _operand(t, name, dtypes, shape)
 
 
@@ -458,30 +459,40 @@ def _space(workspace: Optional[torch.Tensor]):
 
 
 def _on(stream, fn, args, *tensors) -> None:
-    """fn(*args, stream) on the GPU that holds every tensor of the call."""
-    device = None
+    """fn(*args, stream) on the GPU that holds every tensor of the call. The
+    small calls take a few microseconds on the GPU, so the device and its
+    current stream are asked for as plain numbers: torch's objects for them
+    cost about 6 us a call."""
+    index = None
     for t in tensors:
-        if t is None:
-            continue
-        if t.device.type != "cuda":
-            raise ValueError(f"tensors passed to the library must be in GPU memory (device {t.device})")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"tensors of one call must be on one GPU ({device} and {t.device})")
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream on {stream.device}, tensors on {device}")
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
+        if t is not None:
+            at = t.get_device()
+            if at != index:
+                if at < 0:
+                    raise ValueError(f"tensors passed to the library must be in GPU memory (device {t.device})")
+                if index is not None:
+                    raise ValueError(f"tensors of one call must be on one GPU (cuda:{index} and cuda:{at})")
+                index = at
+    if stream is not None:
+        if stream.device.index != index:
+            raise ValueError(f"stream on {stream.device}, tensors on cuda:{index}")
+        raw = stream.cuda_stream
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream)))
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
+    if status:
+        _check(status)
 
 
 def _rank(t: torch.Tensor, name: str, dims) -> tuple:
-    if t.dim() not in dims:
-        raise ValueError(f"{name}: {t.dim()} dimensions, expected {' or '.join(map(str, dims))}")
-    return tuple(t.shape)
+    shape = t.shape
+    if len(shape) not in dims:
+        raise ValueError(f"{name}: {len(shape)} dimensions, expected {' or '.join(map(str, dims))}")
+    return shape
 
 
 def bytes_tensor(nbytes: int, device) -> Optional[torch.Tensor]:
@@ -494,8 +505,8 @@ def signmuon_embedding(ids: torch.Tensor, table: torch.Tensor, scale: float, y: 
     columns. Ids outside the table (padding) give rows of zeros."""
     vocab, cols = _rank(table, "table", (2,))
     args = (_operand(ids, "ids", _ITYPE, ids.shape), _ITYPE[ids.dtype], _operand(table, "table", _ACT, table.shape),
-            _dtype_code(table), ids.numel(), vocab, cols, scale,
-            _operand(y, "y", _ACT, tuple(ids.shape) + (cols,)), _dtype_code(y))
+            _ACT[table.dtype], ids.numel(), vocab, cols, scale,
+            _operand(y, "y", _ACT, ids.shape + (cols,)), _ACT[y.dtype])
     _on(stream, library().signmuon_embedding, args, ids, table, y)
 
 
@@ -511,8 +522,8 @@ def signmuon_embedding_backward(ids: torch.Tensor, dy: torch.Tensor, scale: floa
     workers, tokens = _rank(ids, "ids", (2,))
     vocab, cols = _rank(grad, "grad", (3,))[1:]
     args = (_operand(ids, "ids", _ITYPE, ids.shape), _ITYPE[ids.dtype],
-            _operand(dy, "dy", _ACT, (workers, tokens, cols)), _dtype_code(dy), workers, tokens, vocab, cols, scale,
-            _operand(grad, "grad", _ACT, (workers, vocab, cols)), _dtype_code(grad), int(bool(accumulate)),
+            _operand(dy, "dy", _ACT, (workers, tokens, cols)), _ACT[dy.dtype], workers, tokens, vocab, cols, scale,
+            _operand(grad, "grad", _ACT, (workers, vocab, cols)), _ACT[grad.dtype], int(bool(accumulate)),
             *_space(workspace))
     _on(stream, library().signmuon_embedding_backward, args, ids, dy, grad, workspace)
 
@@ -522,12 +533,11 @@ def signmuon_layer_norm(x: torch.Tensor, gamma: torch.Tensor, beta: Optional[tor
                         stream=None) -> None:
     """Layer norm over x's last dimension; mean and rstd (x's other dimensions,
     fp32) are kept for the backward pass when given."""
-    f32 = (torch.float32,)
     cols = x.shape[-1] if x.dim() else 0
-    args = (_operand(x, "x", _ACT, x.shape), _dtype_code(x), x.numel() // max(cols, 1), cols,
-            _operand(gamma, "gamma", f32, (cols,)), _optional(beta, "beta", f32, (cols,)), eps,
-            _operand(y, "y", (x.dtype,), x.shape), _optional(mean, "mean", f32, x.shape[:-1]),
-            _optional(rstd, "rstd", f32, x.shape[:-1]))
+    args = (_operand(x, "x", _ACT, x.shape), _ACT[x.dtype], x.numel() // max(cols, 1), cols,
+            _operand(gamma, "gamma", _FP32, (cols,)), _optional(beta, "beta", _FP32, (cols,)), eps,
+            _operand(y, "y", (x.dtype,), x.shape), _optional(mean, "mean", _FP32, x.shape[:-1]),
+            _optional(rstd, "rstd", _FP32, x.shape[:-1]))
     _on(stream, library().signmuon_layer_norm, args, x, gamma, beta, y, mean, rstd)
 
 
@@ -542,7 +552,6 @@ def signmuon_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch
     """Gradients of layer norm. x's rows are those of `workers` workers, one
     after the other; dgamma and dbeta are [Mw][C] or [Mw][1][C] (the layout of
     Matrix.grad), one sum for each worker. Each of the three may be None."""
-    f32 = (torch.float32,)
     cols = x.shape[-1] if x.dim() else 0
     rows = x.numel() // max(cols, 1)
     if workers < 1 or rows % workers:
@@ -550,12 +559,12 @@ def signmuon_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch
     sums = [t for t in (dgamma, dbeta) if t is not None]
     grad = sums[0].dtype if sums else torch.float32
     shape = (workers, 1, cols) if sums and sums[0].dim() == 3 else (workers, cols)
-    args = (_operand(dy, "dy", (x.dtype,), x.shape), _operand(x, "x", _ACT, x.shape), _dtype_code(x), workers,
-            rows // workers, cols, _operand(gamma, "gamma", f32, (cols,)),
-            _operand(mean, "mean", f32, x.shape[:-1]), _operand(rstd, "rstd", f32, x.shape[:-1]),
+    args = (_operand(dy, "dy", (x.dtype,), x.shape), _operand(x, "x", _ACT, x.shape), _ACT[x.dtype], workers,
+            rows // workers, cols, _operand(gamma, "gamma", _FP32, (cols,)),
+            _operand(mean, "mean", _FP32, x.shape[:-1]), _operand(rstd, "rstd", _FP32, x.shape[:-1]),
             _optional(dx, "dx", (x.dtype,), x.shape),
-            _optional(dgamma, "dgamma", (grad,), shape), _optional(dbeta, "dbeta", (grad,), shape),
-            _dtype_code(sums[0]) if sums else F32, *_space(workspace))
+            _optional(dgamma, "dgamma", _ACT, shape), _optional(dbeta, "dbeta", (grad,) if grad in _ACT else _ACT, shape),
+            _ACT[grad], *_space(workspace))
     _on(stream, library().signmuon_layer_norm_backward, args, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace)
 
 
@@ -585,8 +594,9 @@ def _f8_operand(q, scale, name: str, lead, k: int):
         return None, None, None
     if q is None or scale is None:
         raise ValueError(f"{name}: values and scales go together")
-    return (_operand(q, name, _F8, lead + (signmuon_f8_pitch(k),)),
-            _operand(scale, name + "_scale", _U8, lead + (signmuon_f8_scale_pitch(k),)), _F8[q.dtype])
+    blocks = (k + 127) // 128
+    return (_operand(q, name, _F8, lead + (blocks * 128,)),
+            _operand(scale, name + "_scale", _U8, lead + ((blocks + 3) // 4 * 4,)), _F8[q.dtype])
 
 
 def signmuon_f8_quant(x: torch.Tensor, q: Optional[torch.Tensor], q_scale: Optional[torch.Tensor],
@@ -601,7 +611,7 @@ def signmuon_f8_quant(x: torch.Tensor, q: Optional[torch.Tensor], q_scale: Optio
     pt, pts, tfmt = _f8_operand(qt, qt_scale, "qt", shape[:-2] + (cols,), rows)
     if fmt is not None and tfmt is not None and fmt != tfmt:
         raise TypeError("q and qt: formats differ")
-    args = (_operand(x, "x", _ACT, x.shape), _dtype_code(x), shape[0] if len(shape) == 3 else 1, rows, cols,
+    args = (_operand(x, "x", _ACT, x.shape), _ACT[x.dtype], shape[0] if len(shape) == 3 else 1, rows, cols,
             tfmt if fmt is None else fmt, pq, ps, pt, pts)
     if args[5] is None:
         raise ValueError("neither q nor qt given")
@@ -623,7 +633,7 @@ def signmuon_f8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, 
     batch = lead[0] if lead else 1
     pa, pas, fa = _f8_operand(a, a_scale, "a", lead + (m,), k)
     one = lead and (b.dim() == 2 or (b.dim() == 3 and b.shape[0] == 1))
-    pb, pbs, fb = _f8_operand(b, b_scale, "b", tuple(b.shape[:-2]) + (n,) if one else lead + (n,), k)
+    pb, pbs, fb = _f8_operand(b, b_scale, "b", b.shape[:-2] + (n,) if one else lead + (n,), k)
     args = (pa, pas, fa, pb, pbs, fb, batch, m, n, k, int(bool(one)), _operand(out, "out", _ACT, shape),
-            _dtype_code(out), *_space(workspace))
+            _ACT[out.dtype], *_space(workspace))
     _on(stream, library().signmuon_f8_matmul, args, a, a_scale, b, b_scale, out, workspace)
