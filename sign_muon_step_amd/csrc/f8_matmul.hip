@@ -86,12 +86,11 @@ __device__ __forceinline__ void store_out(const F8Matmul &f, int64_t at, int hav
 constexpr int kSliceBytes = 64;  // bytes, i.e. values, of k per row and slice
 constexpr int kStages = 4;
 
-// s_waitcnt with vmcnt = N, lgkmcnt = 0, behind every LDS read before it.
+// s_waitcnt with vmcnt = N alone.
 template <int N>
 __device__ __forceinline__ void wait_loads() {
     static_assert(N >= 0 && N < 64, "vmcnt range");
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
 }
 
 // Workgroup barrier that does not wait for the loads into LDS still in flight.
@@ -160,7 +159,7 @@ struct Slices {
 };
 
 template <int TILE> struct TileShape;
-template <> struct TileShape<256> { static constexpr int kWavesM = 2, kWavesN = 4; };
+template <> struct TileShape<256> { static constexpr int kWavesM = 2, kWavesN = 2; };
 template <> struct TileShape<128> { static constexpr int kWavesM = 2, kWavesN = 2; };
 
 // Blocks go to the 8 XCDs round-robin: each XCD gets a contiguous run of tiles.
@@ -198,21 +197,29 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
     Slices<TILE, kWaves> la, lb;
     la.init(f.a + batch * f.a_stride + row0 * f.pitch + (int64_t)block0 * kF8Block, f.pitch, valid_m, slices, wave, lane);
     lb.init(f.b + batch * f.b_stride + col0 * f.pitch + (int64_t)block0 * kF8Block, f.pitch, valid_n, slices, wave, lane);
-    // scales: wave w loads the dwords of rows 64 w .. of a's rows, then b's
-    static_assert(kWaves * kWave == 2 * TILE, "one scale load per lane");
-    const bool scale_b = wave >= kWaves / 2;
-    const int srow = (scale_b ? wave - kWaves / 2 : wave) * kWave + lane;
-    const int svalid = scale_b ? valid_n : valid_m;
-    const uint8_t *sbase = (scale_b ? f.b_scale + batch * f.bs_stride + col0 * f.scale_pitch
-                                    : f.a_scale + batch * f.as_stride + row0 * f.scale_pitch) + block0;
+    // scales: one dword of four blocks for each row of a, then of b, 64 rows a load
+    constexpr int kScaleLoads = 2 * TILE / (kWaves * kWave);
+    static_assert(kScaleLoads * kWaves * kWave == 2 * TILE, "whole scale loads");
     const int dwords = (blocks + 3) / 4;
-    const u32x4 sbuffer = make_buffer(sbase, (svalid - 1) * f.scale_pitch + dwords * 4);
-    const uint32_t soffset = srow < svalid ? (uint32_t)(srow * f.scale_pitch) : kOutside;
+    u32x4 sbuffer[kScaleLoads];
+    uint32_t soffset[kScaleLoads];
+#pragma unroll
+    for (int i = 0; i < kScaleLoads; ++i) {
+        const int first = (i * kWaves + wave) * kWave;
+        const bool of_b = first >= TILE;
+        const int srow = first % TILE + lane, valid = of_b ? valid_n : valid_m;
+        const uint8_t *base = (of_b ? f.b_scale + batch * f.bs_stride + col0 * f.scale_pitch
+                                    : f.a_scale + batch * f.as_stride + row0 * f.scale_pitch) + block0;
+        sbuffer[i] = make_buffer(base, (valid - 1) * f.scale_pitch + dwords * 4);
+        soffset[i] = srow < valid ? (uint32_t)(srow * f.scale_pitch) : kOutside;
+    }
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(
         (__attribute__((address_space(3))) char *)lds);
     auto load_scales = [&](int g) {
-        load4_lds(lds0 + kScaleLds + (g & 1) * kScaleStage + wave * 256u,
-                  g < dwords && soffset != kOutside ? soffset + (uint32_t)g * 4 : kOutside, sbuffer);
+#pragma unroll
+        for (int i = 0; i < kScaleLoads; ++i)
+            load4_lds(lds0 + kScaleLds + (g & 1) * kScaleStage + (i * kWaves + wave) * 256u,
+                      g < dwords && soffset[i] != kOutside ? soffset[i] + (uint32_t)g * 4 : kOutside, sbuffer[i]);
     };
 
     constexpr int kLoads = 2 * Slices<TILE, kWaves>::kLoads;
@@ -225,7 +232,7 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
     };
     load_scales(0);
 #pragma unroll
-    for (int j = 0; j < kStages; ++j)
+    for (int j = 0; j < kStages - 1; ++j)
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) issue(j, i);
 
@@ -244,7 +251,7 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
     v8i fa[FM], fb[2][FN];
     int sa[FM], sb[FN];
 
-    wait_loads<(kStages - 1) * kLoads>();  // slice 0 and the first scales
+    wait_loads<(kStages - 2) * kLoads>();  // slice 0 and the first scales
     barrier();
 #pragma unroll
     for (int i = 0; i < FM; ++i) fa[i] = fragment(lds, wm + i * 32);
@@ -253,11 +260,12 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
 
     // Slice j's products, from the registers. Meanwhile slice j + 1 is read
     // (a's blocks into the registers that their products leave) and slice
-    // j + kStages is loaded to the place that slice j, now in every wave's
-    // registers, leaves in LDS.
+    // j + kStages - 1 is loaded to the place of slice j - 1, which every wave at
+    // the barrier has in its registers (`held`).
+    auto held = [](const v8i &v) { asm volatile("" : : "v"(v)); };
     auto slice = [&](int j, auto parity, int shift) {
         constexpr int P = decltype(parity)::value;
-        wait_loads<(kStages - 2) * kLoads>();  // slice j + 1 has landed
+        wait_loads<(kStages - 3) * kLoads>();  // slice j + 1 has landed
         barrier();
         const char *next = lds + (j + 1) % kStages * kStage;
         int step = 0;
@@ -275,17 +283,22 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
 #pragma unroll
                 for (int i = 0; i < FM; ++i) {
                     wa[i] = widen<A5>(fa[i], q, xa[i]);
-                    if (q == 3) fa[i] = fragment(next, wm + i * 32);
+                    if (q == 3) {
+                        held(fa[i]);
+                        fa[i] = fragment(next, wm + i * 32);
+                    }
 #pragma unroll
                     for (int n = 0; n < FN; ++n) {
                         acc[i][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[n], wa[i], acc[i][n], 0, 0, 0);
                         if (step < FN) fb[1 - P][step] = fragment(next + kOperand, wn + step * 32);
-                        if (step < kLoads) issue(j + kStages, step);
+                        if (step < kLoads) issue(j + kStages - 1, step);
                         ++step;
                     }
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
+#pragma unroll
+            for (int n = 0; n < FN; ++n) held(fb[P][n]);
             return;
         }
 #pragma unroll
@@ -295,12 +308,15 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
                 acc[i][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                     fb[P][n], fa[i], acc[i][n], B5 ? 1 : 0, A5 ? 1 : 0, 0, sb[n] >> shift, 0, sa[i] >> shift);
                 if (step < FN) fb[1 - P][step] = fragment(next + kOperand, wn + step * 32);
-                if (step < kLoads) issue(j + kStages, step);
+                if (step < kLoads) issue(j + kStages - 1, step);
                 ++step;
             }
+            held(fa[i]);
             fa[i] = fragment(next, wm + i * 32);
             __builtin_amdgcn_sched_barrier(0);
         }
+#pragma unroll
+        for (int n = 0; n < FN; ++n) held(fb[P][n]);
     };
     for (int b = 0; b < blocks; ++b) {
         if ((b & 3) == 0) {  // the scales of four blocks
@@ -315,24 +331,67 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
         slice(2 * b + 1, std::integral_constant<int, 1>{}, (b & 3) * 8);
     }
     wait_loads<0>();  // loads past the end write LDS too
+    __syncthreads();
 
+    // 32 rows of a wave at a time through LDS, so that rows are written in
+    // stretches of FN * 32 columns
+    constexpr int kCols = FN * 32;
+    static_assert(kWaves * 32 * (kCols * 4 + 16) <= kScaleLds, "staged rows fit");
+    auto write = [&](auto narrow, void *out, int64_t first) {
+        constexpr bool N = decltype(narrow)::value;  // as BF16
+        constexpr int kPitch = kCols * (N ? 2 : 4) + 16;  // bytes of a staged row
+        constexpr int kLanes = kCols / (N ? 8 : 4);       // 16 bytes each
+        char *mine = lds + wave * 32 * kPitch;
+        const int c = lane % kLanes * (N ? 8 : 4);
+        const int64_t left = f.n - (col0 + wn + c);  // columns from this lane's on
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-        const int64_t r = row0 + wm + i * 32 + row;
-        if (r >= f.m) continue;
+        for (int i = 0; i < FM; ++i) {
 #pragma unroll
-        for (int n = 0; n < FN; ++n)
+            for (int n = 0; n < FN; ++n)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int64_t c = col0 + wn + n * 32 + g * 8 + half * 4;
-                const int have = (int)(f.n - c < 4 ? f.n - c : 4);
-                const float v[4] = {acc[i][n][4 * g], acc[i][n][4 * g + 1], acc[i][n][4 * g + 2], acc[i][n][4 * g + 3]};
-                if (f.splits > 1)
-                    store_n<false>(f.partial, ((split * (int64_t)f.batch + batch) * f.m + r) * f.n + c, have, v);
-                else
-                    store_out(f, (batch * f.m + r) * f.n + c, have, v);
+                for (int g = 0; g < 4; ++g) {
+                    char *at = mine + row * kPitch + (n * 32 + g * 8 + half * 4) * (N ? 2 : 4);
+                    const f32x16 &v = acc[i][n];
+                    if constexpr (N)
+                        *reinterpret_cast<u32x2 *>(at) =
+                            u32x2{to_bf16x2(v[4 * g], v[4 * g + 1]), to_bf16x2(v[4 * g + 2], v[4 * g + 3])};
+                    else
+                        *reinterpret_cast<f32x4 *>(at) = f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+                }
+            // lanes read what others wrote (LDS accesses of a wave keep their order)
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_wave_barrier();
+            u32x4 v[32 * kLanes / kWave];
+#pragma unroll
+            for (int r = 0; r < 32 * kLanes / kWave; ++r)
+                v[r] = *reinterpret_cast<const u32x4 *>(mine + (r * (kWave / kLanes) + lane / kLanes) * kPitch + lane % kLanes * 16);
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_wave_barrier();
+            const int64_t to = row0 + wm + i * 32 + lane / kLanes;
+            char *p = static_cast<char *>(out) + ((first + to) * f.n + col0 + wn + c) * (N ? 2 : 4);
+#pragma unroll
+            for (int r = 0; r < 32 * kLanes / kWave; ++r) {
+                char *q = p + (int64_t)r * (kWave / kLanes) * f.n * (N ? 2 : 4);
+                if (to + r * (kWave / kLanes) >= f.m) continue;
+                if (left >= (N ? 8 : 4)) {
+                    *reinterpret_cast<u32x4_any *>(q) = v[r];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < (N ? 8 : 4); ++j)
+                        if (j < left) {
+                            if constexpr (N)
+                                reinterpret_cast<uint16_t *>(q)[j] = (uint16_t)(v[r][j / 2] >> (j % 2 * 16));
+                            else
+                                reinterpret_cast<uint32_t *>(q)[j] = v[r][j];
+                        }
+                }
             }
-    }
+        }
+    };
+    if (f.splits > 1)
+        write(std::false_type{}, f.partial, (split * (int64_t)f.batch + batch) * f.m);
+    else
+        write(std::integral_constant<bool, !F32>{}, f.out, batch * f.m);
 }
 
 // ---------------------------------------------------------------------------
@@ -440,7 +499,7 @@ void launch(const F8Matmul &f, hipStream_t s) {
     const int64_t tiles = (f.m + f.tile - 1) / f.tile * ((f.n + f.tile - 1) / f.tile);
     const dim3 grid((unsigned)(tiles * f.batch * f.splits));
     if (f.tile == 256)
-        f8_tile_kernel<256, A5, B5, F32><<<grid, 512, 0, s>>>(f);
+        f8_tile_kernel<256, A5, B5, F32><<<grid, 256, 0, s>>>(f);
     else
         f8_tile_kernel<128, A5, B5, F32><<<grid, 256, 0, s>>>(f);
 }
