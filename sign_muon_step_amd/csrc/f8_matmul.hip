@@ -49,10 +49,11 @@ __device__ __forceinline__ v8i join(u32x4 lo, u32x4 hi) {
     return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
-// 2^(byte - 127) of byte `shift / 8` of a dword of scales.
-__device__ __forceinline__ float scale_of(int scales, int shift) {
-    return __int_as_float(((scales >> shift) & 255) << 23);
-}
+// Nothing behind this runs before v is in its registers.
+__device__ __forceinline__ void hold(const v8i &v) { asm volatile("" : : "v"(v) : "memory"); }
+
+// 2^(byte - 127).
+__device__ __forceinline__ float scale_of(int byte) { return __int_as_float(byte << 23); }
 
 // Bytes 8 i .. 8 i + 7 of a fragment as BF16, scaled.
 template <bool E5M2>
@@ -131,19 +132,18 @@ __device__ __forceinline__ uint32_t slice_at(int r, int c) {
 }
 
 // One operand's rows of a tile (ROWS rows of which `valid` exist) on their way
-// into LDS, by WAVES waves. base: the tile's first row at the k of slice 0.
+// into LDS, by WAVES waves. base: the tile's first row at the k of slice 0. A
+// lane's offset stays; the buffer's start moves by a slice (scalar work), and
+// past the last slice the buffer is empty: its loads give zeros.
 template <int ROWS, int WAVES>
 struct Slices {
     static constexpr int kLoads = ROWS * kSliceBytes / 1024 / WAVES;  // per wave and slice
     static_assert(kLoads * WAVES * 1024 == ROWS * kSliceBytes, "whole loads");
     u32x4 buffer;
     uint32_t offset[kLoads];
-    int slices;
 
-    __device__ __forceinline__ void init(const uint8_t *base, int64_t pitch, int valid, int slices_, int wave, int lane) {
-        slices = slices_;
-        // rows past the last one start beyond the buffer's end, which is the end of the last row's slices
-        buffer = make_buffer(base, (valid - 1) * pitch + (int64_t)slices_ * kSliceBytes);
+    __device__ __forceinline__ void init(const uint8_t *base, int64_t pitch, int valid, int wave, int lane) {
+        buffer = make_buffer(base, (valid - 1) * pitch + kSliceBytes);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int row = (i * WAVES + wave) * 16 + lane / 4;
@@ -151,10 +151,16 @@ struct Slices {
             offset[i] = row < valid ? (uint32_t)(row * pitch + chunk * 16) : kOutside;
         }
     }
-    // Load i of slice j to `lds` (of the slice's first row); zeros past the last slice.
-    __device__ __forceinline__ void issue(int j, int i, uint32_t lds, int wave) const {
-        load16_lds(lds + (uint32_t)(i * WAVES + wave) * 1024u,
-                   j < slices && offset[i] != kOutside ? offset[i] + (uint32_t)j * kSliceBytes : kOutside, buffer);
+    // Load i of the current slice to `lds` (of the slice's first row).
+    __device__ __forceinline__ void issue(int i, uint32_t lds, int wave) const {
+        load16_lds(lds + (uint32_t)(i * WAVES + wave) * 1024u, offset[i], buffer);
+    }
+    // On to slice j.
+    __device__ __forceinline__ void advance(int j, int slices) {
+        const uint32_t lo = buffer[0] + kSliceBytes;
+        buffer[1] += lo < (uint32_t)kSliceBytes ? 1u : 0u;
+        buffer[0] = lo;
+        if (j >= slices) buffer[2] = 0;
     }
 };
 
@@ -195,8 +201,8 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
 
     const int valid_m = (int)(f.m - row0 < TILE ? f.m - row0 : TILE), valid_n = (int)(f.n - col0 < TILE ? f.n - col0 : TILE);
     Slices<TILE, kWaves> la, lb;
-    la.init(f.a + batch * f.a_stride + row0 * f.pitch + (int64_t)block0 * kF8Block, f.pitch, valid_m, slices, wave, lane);
-    lb.init(f.b + batch * f.b_stride + col0 * f.pitch + (int64_t)block0 * kF8Block, f.pitch, valid_n, slices, wave, lane);
+    la.init(f.a + batch * f.a_stride + row0 * f.pitch + (int64_t)block0 * kF8Block, f.pitch, valid_m, wave, lane);
+    lb.init(f.b + batch * f.b_stride + col0 * f.pitch + (int64_t)block0 * kF8Block, f.pitch, valid_n, wave, lane);
     // scales: one dword of four blocks for each row of a, then of b, 64 rows a load
     constexpr int kScaleLoads = 2 * TILE / (kWaves * kWave);
     static_assert(kScaleLoads * kWaves * kWave == 2 * TILE, "whole scale loads");
@@ -223,112 +229,110 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
     };
 
     constexpr int kLoads = 2 * Slices<TILE, kWaves>::kLoads;
-    auto issue = [&](int j, int i) {  // load i of slice j, of both operands
+    auto issue = [&](int j, int i) {  // load i of slice j, the current one of both operands
         const uint32_t at = lds0 + (uint32_t)(j % kStages) * kStage;
         if (i < kLoads / 2)
-            la.issue(j, i, at, wave);
+            la.issue(i, at, wave);
         else
-            lb.issue(j, i - kLoads / 2, at + kOperand, wave);
+            lb.issue(i - kLoads / 2, at + kOperand, wave);
+    };
+    auto advance = [&](int j) {
+        la.advance(j, slices);
+        lb.advance(j, slices);
     };
     load_scales(0);
 #pragma unroll
-    for (int j = 0; j < kStages - 1; ++j)
+    for (int j = 0; j < kStages - 1; ++j) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) issue(j, i);
+        advance(j + 1);
+    }
 
+    // A slice's fragments in registers, b's FN then a's FM, 32 bytes a lane (its
+    // half of the slice): read r is 16 bytes of fragment r / 2.
     const int wm = wave / S::kWavesN * FM * 32, wn = wave % S::kWavesN * FN * 32;
     const int row = lane & 31, half = lane >> 5;
-    // 32 bytes of a row: the lane's half of the slice
-    auto fragment = [&](const char *operand, int r) {
-        return join(*reinterpret_cast<const u32x4 *>(operand + slice_at(r + row, 2 * half)),
-                    *reinterpret_cast<const u32x4 *>(operand + slice_at(r + row, 2 * half + 1)));
+    constexpr int kFragments = FM + FN, kReads = 2 * kFragments, kSteps = FM * FN;
+    v8i fr[2][kFragments];
+    auto read = [&](v8i (&to)[kFragments], const char *stage, int r) {
+        const int i = r / 2;
+        const char *p = i < FN ? stage + kOperand + slice_at(wn + i * 32 + row, 2 * half + r % 2)
+                               : stage + slice_at(wm + (i - FN) * 32 + row, 2 * half + r % 2);
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(p);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) to[i][4 * (r % 2) + q] = (int)v[q];
+    };
+    // The scale bytes of block b of k.
+    int sc[kFragments];
+    auto read_scales = [&](int b) {
+        const char *s = lds + kScaleLds + (b >> 2 & 1) * kScaleStage + (b & 3);
+#pragma unroll
+        for (int i = 0; i < kFragments; ++i)
+            sc[i] = (int)*reinterpret_cast<const uint8_t *>(
+                s + 4 * (i < FN ? TILE + wn + i * 32 + row : wm + (i - FN) * 32 + row));
     };
     f32x16 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
-    v8i fa[FM], fb[2][FN];
-    int sa[FM], sb[FN];
 
     wait_loads<(kStages - 2) * kLoads>();  // slice 0 and the first scales
     barrier();
 #pragma unroll
-    for (int i = 0; i < FM; ++i) fa[i] = fragment(lds, wm + i * 32);
-#pragma unroll
-    for (int j = 0; j < FN; ++j) fb[0][j] = fragment(lds + kOperand, wn + j * 32);
+    for (int r = 0; r < kReads; ++r) read(fr[0], lds, r);
 
-    // Slice j's products, from the registers. Meanwhile slice j + 1 is read
-    // (a's blocks into the registers that their products leave) and slice
-    // j + kStages - 1 is loaded to the place of slice j - 1, which every wave at
-    // the barrier has in its registers (`held`).
-    auto held = [](const v8i &v) { asm volatile("" : : "v"(v)); };
-    auto slice = [&](int j, auto parity, int shift) {
+    // Slice j's products, from the registers. Meanwhile slice j + 1 is read and
+    // slice j + kStages - 1 loaded to the place of slice j - 1, which every wave
+    // at the barrier has in its registers (`held`). Reads and loads are spread
+    // over the products, so that the matrix pipe does not wait behind them.
+    auto held = [&](const v8i (&v)[kFragments]) {
+#pragma unroll
+        for (int i = 0; i < kFragments; ++i) hold(v[i]);
+    };
+    auto slice = [&](int j, auto parity) {
         constexpr int P = decltype(parity)::value;
         wait_loads<(kStages - 3) * kLoads>();  // slice j + 1 has landed
         barrier();
         const char *next = lds + (j + 1) % kStages * kStage;
-        int step = 0;
         if constexpr (F32) {
-            float xa[FM], xb[FN];
-#pragma unroll
-            for (int i = 0; i < FM; ++i) xa[i] = scale_of(sa[i], shift);
-#pragma unroll
-            for (int n = 0; n < FN; ++n) xb[n] = scale_of(sb[n], shift);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {  // 16 k each: bytes 8 q of both halves
-                bf16x8 wa[FM], wb[FN];
+                bf16x8 w[kFragments];
 #pragma unroll
-                for (int n = 0; n < FN; ++n) wb[n] = widen<B5>(fb[P][n], q, xb[n]);
+                for (int i = 0; i < kFragments; ++i)
+                    w[i] = i < FN ? widen<B5>(fr[P][i], q, scale_of(sc[i])) : widen<A5>(fr[P][i], q, scale_of(sc[i]));
 #pragma unroll
-                for (int i = 0; i < FM; ++i) {
-                    wa[i] = widen<A5>(fa[i], q, xa[i]);
-                    if (q == 3) {
-                        held(fa[i]);
-                        fa[i] = fragment(next, wm + i * 32);
-                    }
-#pragma unroll
-                    for (int n = 0; n < FN; ++n) {
-                        acc[i][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[n], wa[i], acc[i][n], 0, 0, 0);
-                        if (step < FN) fb[1 - P][step] = fragment(next + kOperand, wn + step * 32);
-                        if (step < kLoads) issue(j + kStages - 1, step);
-                        ++step;
-                    }
+                for (int s = 0; s < kSteps; ++s) {
+                    acc[s / FN][s % FN] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[s % FN], w[FN + s / FN],
+                                                                                 acc[s / FN][s % FN], 0, 0, 0);
+                    const int t = q * kSteps + s;
+                    if (t < kReads) read(fr[1 - P], next, t);
+                    if (t % 4 == 0 && t / 4 < kLoads) issue(j + kStages - 1, t / 4);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
+        } else {
 #pragma unroll
-            for (int n = 0; n < FN; ++n) held(fb[P][n]);
-            return;
-        }
+            for (int s = 0; s < kSteps; ++s) {
+                acc[s / FN][s % FN] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    fr[P][s % FN], fr[P][FN + s / FN], acc[s / FN][s % FN], B5 ? 1 : 0, A5 ? 1 : 0, 0, sc[s % FN], 0,
+                    sc[FN + s / FN]);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
+                for (int r = s * kReads / kSteps; r < (s + 1) * kReads / kSteps; ++r) read(fr[1 - P], next, r);
 #pragma unroll
-            for (int n = 0; n < FN; ++n) {
-                acc[i][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    fb[P][n], fa[i], acc[i][n], B5 ? 1 : 0, A5 ? 1 : 0, 0, sb[n] >> shift, 0, sa[i] >> shift);
-                if (step < FN) fb[1 - P][step] = fragment(next + kOperand, wn + step * 32);
-                if (step < kLoads) issue(j + kStages - 1, step);
-                ++step;
+                for (int i = s * kLoads / kSteps; i < (s + 1) * kLoads / kSteps; ++i) issue(j + kStages - 1, i);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            held(fa[i]);
-            fa[i] = fragment(next, wm + i * 32);
-            __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int n = 0; n < FN; ++n) held(fb[P][n]);
+        held(fr[P]);
+        advance(j + kStages);
     };
     for (int b = 0; b < blocks; ++b) {
-        if ((b & 3) == 0) {  // the scales of four blocks
-            const char *s = lds + kScaleLds + (b >> 2 & 1) * kScaleStage;
-#pragma unroll
-            for (int i = 0; i < FM; ++i) sa[i] = *reinterpret_cast<const int *>(s + (wm + i * 32 + row) * 4);
-#pragma unroll
-            for (int n = 0; n < FN; ++n) sb[n] = *reinterpret_cast<const int *>(s + (TILE + wn + n * 32 + row) * 4);
-            load_scales((b >> 2) + 1);
-        }
-        slice(2 * b, std::integral_constant<int, 0>{}, (b & 3) * 8);
-        slice(2 * b + 1, std::integral_constant<int, 1>{}, (b & 3) * 8);
+        read_scales(b);
+        if ((b & 3) == 0) load_scales((b >> 2) + 1);
+        slice(2 * b, std::integral_constant<int, 0>{});
+        slice(2 * b + 1, std::integral_constant<int, 1>{});
     }
     wait_loads<0>();  // loads past the end write LDS too
     __syncthreads();
@@ -443,7 +447,8 @@ __global__ __launch_bounds__(512) void f8_rows_kernel(F8Matmul f) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
                             acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                widen<B5>(fb[k], q, scale_of(sb, 8 * k)), widen<A5>(fa[k][i], q, scale_of(sa[i], 8 * k)),
+                                widen<B5>(fb[k], q, scale_of(sb >> (8 * k) & 255)),
+                                widen<A5>(fa[k][i], q, scale_of(sa[i] >> (8 * k) & 255)),
                                 acc[i], 0, 0, 0);
                     } else {
                         acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
