@@ -22,9 +22,11 @@
 // so that a lane's accumulators hold four consecutive columns of one row of
 // out.
 //
-// f8_tile_kernel: a workgroup computes a TILE x TILE tile from 64-byte slices
-// of both operands that stream from memory straight into LDS, kStages slices
-// deep. A slice's rows are 64 bytes, their 16-byte chunks XOR-swizzled so that
+// f8_tile_kernel: a workgroup computes a TILE x TILE tile from slices of 128
+// k of both operands that stream from memory straight into LDS, two slices
+// deep. A slice's rows are 128 bytes: whole lines of the caches (rows of 64
+// bytes, four slices deep, fetched each line twice: 650 us where this takes
+// 595, at 16384 x 11008 x 4096). Their 16-byte chunks are XOR-swizzled so that
 // 16 consecutive rows' reads fall on all banks.
 // f8_rows_kernel: up to 64 rows of a. Bound by reading b once: no LDS on the
 // way, each wave reads whole 128-byte lines of b into the instruction's
@@ -55,22 +57,25 @@ __device__ __forceinline__ void hold(const v8i &v) { asm volatile("" : : "v"(v) 
 // 2^(byte - 127).
 __device__ __forceinline__ float scale_of(int byte) { return __int_as_float(byte << 23); }
 
+// Four bytes as BF16, scaled.
+template <bool E5M2>
+__device__ __forceinline__ u32x2 widen4(int bytes, float scale) {
+    bf16x2 lo, hi;
+    if (E5M2) {
+        lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((unsigned)bytes, scale, false);
+        hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((unsigned)bytes, scale, true);
+    } else {
+        lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)bytes, scale, false);
+        hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)bytes, scale, true);
+    }
+    return u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+}
+
 // Bytes 8 i .. 8 i + 7 of a fragment as BF16, scaled.
 template <bool E5M2>
 __device__ __forceinline__ bf16x8 widen(const v8i &f, int i, float scale) {
-    bf16x2 v[4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const unsigned w = (unsigned)f[2 * i + j];
-        if (E5M2) {
-            v[2 * j] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, scale, false);
-            v[2 * j + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, scale, true);
-        } else {
-            v[2 * j] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false);
-            v[2 * j + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true);
-        }
-    }
-    return bf16x8{v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
+    const u32x2 lo = widen4<E5M2>(f[2 * i], scale), hi = widen4<E5M2>(f[2 * i + 1], scale);
+    return __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
 }
 
 // Four consecutive columns of out.
@@ -84,8 +89,8 @@ __device__ __forceinline__ void store_out(const F8Matmul &f, int64_t at, int hav
 // ---------------------------------------------------------------------------
 // Tiles
 // ---------------------------------------------------------------------------
-constexpr int kSliceBytes = 64;  // bytes, i.e. values, of k per row and slice
-constexpr int kStages = 4;
+constexpr int kSliceBytes = kF8Block;  // bytes, i.e. values, of k per row and slice
+constexpr int kStages = 2;
 
 // s_waitcnt with vmcnt = N alone.
 template <int N>
@@ -128,7 +133,7 @@ __device__ __forceinline__ u32x4 make_buffer(const uint8_t *p, int64_t bytes) {
 
 // LDS byte of 16-byte chunk c of a slice's row r.
 __device__ __forceinline__ uint32_t slice_at(int r, int c) {
-    return (uint32_t)(r * kSliceBytes + ((c ^ ((r >> 2) & 3)) << 4));
+    return (uint32_t)(r * kSliceBytes + ((c ^ ((r >> 1) & 7)) << 4));
 }
 
 // One operand's rows of a tile (ROWS rows of which `valid` exist) on their way
@@ -146,8 +151,8 @@ struct Slices {
         buffer = make_buffer(base, (valid - 1) * pitch + kSliceBytes);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int row = (i * WAVES + wave) * 16 + lane / 4;
-            const int chunk = (lane & 3) ^ ((row >> 2) & 3);
+            const int row = (i * WAVES + wave) * 8 + lane / 8;
+            const int chunk = (lane & 7) ^ ((row >> 1) & 7);
             offset[i] = row < valid ? (uint32_t)(row * pitch + chunk * 16) : kOutside;
         }
     }
@@ -161,6 +166,8 @@ struct Slices {
         buffer[1] += lo < (uint32_t)kSliceBytes ? 1u : 0u;
         buffer[0] = lo;
         if (j >= slices) buffer[2] = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) buffer[i] = (uint32_t)first_lane((int)buffer[i]);  // it stays in scalar registers
     }
 };
 
@@ -197,7 +204,6 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
     const int split = unit % f.splits;
     const int block0 = split * f.chunk;
     const int blocks = f.blocks - block0 < f.chunk ? f.blocks - block0 : f.chunk;
-    const int slices = blocks * (kF8Block / kSliceBytes);
 
     const int valid_m = (int)(f.m - row0 < TILE ? f.m - row0 : TILE), valid_n = (int)(f.n - col0 < TILE ? f.n - col0 : TILE);
     Slices<TILE, kWaves> la, lb;
@@ -237,38 +243,40 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
             lb.issue(i - kLoads / 2, at + kOperand, wave);
     };
     auto advance = [&](int j) {
-        la.advance(j, slices);
-        lb.advance(j, slices);
+        la.advance(j, blocks);
+        lb.advance(j, blocks);
     };
     load_scales(0);
 #pragma unroll
-    for (int j = 0; j < kStages - 1; ++j) {
+    for (int j = 0; j < kStages; ++j) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) issue(j, i);
         advance(j + 1);
     }
 
-    // A slice's fragments in registers, b's FN then a's FM, 32 bytes a lane (its
-    // half of the slice): read r is 16 bytes of fragment r / 2.
+    // The fragments of half a slice (64 k) in registers: b's FN, then a's FM, 32
+    // bytes a lane (lanes 32 on have the upper 32 k). Read r is 16 bytes of
+    // fragment r / 2.
     const int wm = wave / S::kWavesN * FM * 32, wn = wave % S::kWavesN * FN * 32;
     const int row = lane & 31, half = lane >> 5;
-    constexpr int kFragments = FM + FN, kReads = 2 * kFragments, kSteps = FM * FN;
+    constexpr int kFragments = FM + FN, kReads = 2 * kFragments, kTiles = FM * FN;
     v8i fr[2][kFragments];
-    auto read = [&](v8i (&to)[kFragments], const char *stage, int r) {
-        const int i = r / 2;
-        const char *p = i < FN ? stage + kOperand + slice_at(wn + i * 32 + row, 2 * half + r % 2)
-                               : stage + slice_at(wm + (i - FN) * 32 + row, 2 * half + r % 2);
-        const u32x4 v = *reinterpret_cast<const u32x4 *>(p);
+    auto read = [&](auto h, int j, int r) {  // of half h of slice j
+        constexpr int H = decltype(h)::value;
+        const char *stage = lds + j % kStages * kStage;
+        const int i = r / 2, chunk = 4 * H + 2 * half + r % 2;
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(i < FN ? stage + kOperand + slice_at(wn + i * 32 + row, chunk)
+                                                                : stage + slice_at(wm + (i - FN) * 32 + row, chunk));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) to[i][4 * (r % 2) + q] = (int)v[q];
+        for (int q = 0; q < 4; ++q) fr[H][i][4 * (r % 2) + q] = (int)v[q];
     };
-    // The scale bytes of block b of k.
-    int sc[kFragments];
-    auto read_scales = [&](int b) {
-        const char *s = lds + kScaleLds + (b >> 2 & 1) * kScaleStage + (b & 3);
+    // The scale bytes of slice j.
+    int sc[kFragments], sc_next[kFragments];
+    auto read_scales = [&](int j) {
+        const char *s = lds + kScaleLds + (j >> 2 & 1) * kScaleStage + (j & 3);
 #pragma unroll
         for (int i = 0; i < kFragments; ++i)
-            sc[i] = (int)*reinterpret_cast<const uint8_t *>(
+            sc_next[i] = (int)*reinterpret_cast<const uint8_t *>(
                 s + 4 * (i < FN ? TILE + wn + i * 32 + row : wm + (i - FN) * 32 + row));
     };
     f32x16 acc[FM][FN];
@@ -277,62 +285,101 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
 
-    wait_loads<(kStages - 2) * kLoads>();  // slice 0 and the first scales
+    constexpr std::integral_constant<int, 0> kLow{};
+    constexpr std::integral_constant<int, 1> kHigh{};
+    wait_loads<kLoads>();  // slice 0 and the first scales
     barrier();
+    read_scales(0);
 #pragma unroll
-    for (int r = 0; r < kReads; ++r) read(fr[0], lds, r);
+    for (int r = 0; r < kReads; ++r) read(kLow, 0, r);
 
-    // Slice j's products, from the registers. Meanwhile slice j + 1 is read and
-    // slice j + kStages - 1 loaded to the place of slice j - 1, which every wave
-    // at the barrier has in its registers (`held`). Reads and loads are spread
-    // over the products, so that the matrix pipe does not wait behind them.
-    auto held = [&](const v8i (&v)[kFragments]) {
-#pragma unroll
-        for (int i = 0; i < kFragments; ++i) hold(v[i]);
+    // F32: 16 k of the fragments as BF16 (bytes 8 q of both lane halves), one set
+    // for the products and one that is filled meanwhile: part p is four bytes of
+    // fragment p / 2.
+    u32x4 wide[2][F32 ? kFragments : 1];
+    auto widen_part = [&](auto h, int q, int p, const int *scales) {
+        constexpr int H = decltype(h)::value;
+        const int i = p / 2, d = p % 2;
+        const float x = scale_of(scales[i]);
+        const u32x2 v = i < FN ? widen4<B5>(fr[H][i][2 * q + d], x) : widen4<A5>(fr[H][i][2 * q + d], x);
+        wide[q & 1][i][2 * d] = v[0];
+        wide[q & 1][i][2 * d + 1] = v[1];
     };
-    auto slice = [&](int j, auto parity) {
-        constexpr int P = decltype(parity)::value;
-        wait_loads<(kStages - 3) * kLoads>();  // slice j + 1 has landed
-        barrier();
-        const char *next = lds + (j + 1) % kStages * kStage;
+    if constexpr (F32)
+#pragma unroll
+        for (int p = 0; p < kReads; ++p) widen_part(kLow, 0, p, sc_next);
+
+    // The products of half h of slice j, from the registers, a step for each;
+    // extra(step) is what else the step issues, so that the matrix pipe does not
+    // wait behind a run of reads, loads or conversions.
+    auto products = [&](auto h, auto extra) {
+        constexpr int H = decltype(h)::value;
         if constexpr (F32) {
+            constexpr int kParts = kReads / kTiles;  // a step
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {  // 16 k each: bytes 8 q of both halves
-                bf16x8 w[kFragments];
+            for (int t = 0; t < 4 * kTiles; ++t) {
+                const int q = t / kTiles, s = t % kTiles;
+                extra(t);
 #pragma unroll
-                for (int i = 0; i < kFragments; ++i)
-                    w[i] = i < FN ? widen<B5>(fr[P][i], q, scale_of(sc[i])) : widen<A5>(fr[P][i], q, scale_of(sc[i]));
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                    acc[s / FN][s % FN] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[s % FN], w[FN + s / FN],
-                                                                                 acc[s / FN][s % FN], 0, 0, 0);
-                    const int t = q * kSteps + s;
-                    if (t < kReads) read(fr[1 - P], next, t);
-                    if (t % 4 == 0 && t / 4 < kLoads) issue(j + kStages - 1, t / 4);
+                for (int p = s * kParts; p < (s + 1) * kParts; ++p) {
+                    if (q < 3)
+                        widen_part(h, q + 1, p, sc);
+                    else if (H == 0)
+                        widen_part(kHigh, 0, p, sc);
+                    else
+                        widen_part(kLow, 0, p, sc_next);
                 }
+                acc[s / FN][s % FN] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    __builtin_bit_cast(bf16x8, wide[q & 1][s % FN]), __builtin_bit_cast(bf16x8, wide[q & 1][FN + s / FN]),
+                    acc[s / FN][s % FN], 0, 0, 0);
                 __builtin_amdgcn_sched_barrier(0);
             }
         } else {
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
+            for (int s = 0; s < kTiles; ++s) {
+                extra(s);
                 acc[s / FN][s % FN] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    fr[P][s % FN], fr[P][FN + s / FN], acc[s / FN][s % FN], B5 ? 1 : 0, A5 ? 1 : 0, 0, sc[s % FN], 0,
+                    fr[H][s % FN], fr[H][FN + s / FN], acc[s / FN][s % FN], B5 ? 1 : 0, A5 ? 1 : 0, 0, sc[s % FN], 0,
                     sc[FN + s / FN]);
-#pragma unroll
-                for (int r = s * kReads / kSteps; r < (s + 1) * kReads / kSteps; ++r) read(fr[1 - P], next, r);
-#pragma unroll
-                for (int i = s * kLoads / kSteps; i < (s + 1) * kLoads / kSteps; ++i) issue(j + kStages - 1, i);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-        held(fr[P]);
-        advance(j + kStages);
     };
-    for (int b = 0; b < blocks; ++b) {
-        read_scales(b);
-        if ((b & 3) == 0) load_scales((b >> 2) + 1);
-        slice(2 * b, std::integral_constant<int, 0>{});
-        slice(2 * b + 1, std::integral_constant<int, 1>{});
+    // Steps of the low half: the reads of the high half in the first half of
+    // them, then at step kMeet all waves have read slice j and slice j + 1 has
+    // landed, so that slice j + 2 is loaded to slice j's place from there on, two
+    // (TILE 128: four) loads a step, and slice j + 1 may be read.
+    constexpr int kMeet = (kTiles * 5 + 7) / 8, kPerRead = kReads * 2 / kTiles, kPerLoad = kLoads * 2 / kTiles;
+    static_assert(kPerRead * kTiles == 2 * kReads && kPerLoad * kTiles == 2 * kLoads, "whole steps");
+    auto load_step = [&](int j, int s) {  // s: steps from kMeet on
+#pragma unroll
+        for (int i = s * kPerLoad; i < (s + 1) * kPerLoad; ++i)
+            if (i < kLoads) issue(j + kStages, i);
+    };
+    for (int j = 0; j < blocks; ++j) {
+#pragma unroll
+        for (int i = 0; i < kFragments; ++i) sc[i] = sc_next[i];
+        if ((j & 3) == 0) load_scales((j >> 2) + 1);
+        products(kLow, [&](int s) {
+#pragma unroll
+            for (int r = s * kPerRead; r < (s + 1) * kPerRead; ++r)
+                if (r < kReads) read(kHigh, j, r);
+            if (s == kMeet) {
+#pragma unroll
+                for (int i = 0; i < kFragments; ++i) hold(fr[1][i]);
+                wait_loads<0>();
+                barrier();
+            }
+            if (s >= kMeet) load_step(j, s - kMeet);
+        });
+        products(kHigh, [&](int s) {
+            if (s == 0) read_scales(j + 1);
+#pragma unroll
+            for (int r = s * kReads / kTiles; r < (s + 1) * kReads / kTiles; ++r)
+                if (r < kReads) read(kLow, j + 1, r);
+            if (!F32) load_step(j, kTiles - kMeet + s);
+        });
+        advance(j + kStages + 1);
     }
     wait_loads<0>();  // loads past the end write LDS too
     __syncthreads();
