@@ -54,6 +54,17 @@ __device__ __forceinline__ v8i join(u32x4 lo, u32x4 hi) {
 // Nothing behind this runs before v is in its registers.
 __device__ __forceinline__ void hold(const v8i &v) { asm volatile("" : : "v"(v) : "memory"); }
 
+// v is computed here, not behind a later branch.
+__device__ __forceinline__ void pin(f32x16 &v) { asm volatile("" : "+a"(v)); }
+
+// Zeros written straight to where they are kept (one zero for all of them would
+// take sixteen registers of its own).
+__device__ __forceinline__ f32x16 zeros() {
+    float z = 0.0f;
+    asm volatile("" : "+v"(z));
+    return f32x16{z, z, z, z, z, z, z, z, z, z, z, z, z, z, z, z};
+}
+
 // 2^(byte - 127).
 __device__ __forceinline__ float scale_of(int byte) { return __int_as_float(byte << 23); }
 
@@ -96,6 +107,7 @@ constexpr int kStages = 2;
 template <int N>
 __device__ __forceinline__ void wait_loads() {
     static_assert(N >= 0 && N < 64, "vmcnt range");
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
 }
 
@@ -136,122 +148,168 @@ __device__ __forceinline__ uint32_t slice_at(int r, int c) {
     return (uint32_t)(r * kSliceBytes + ((c ^ ((r >> 1) & 7)) << 4));
 }
 
-// One operand's rows of a tile (ROWS rows of which `valid` exist) on their way
-// into LDS, by WAVES waves. base: the tile's first row at the k of slice 0. A
-// lane's offset stays; the buffer's start moves by a slice (scalar work), and
-// past the last slice the buffer is empty: its loads give zeros.
-template <int ROWS, int WAVES>
-struct Slices {
-    static constexpr int kLoads = ROWS * kSliceBytes / 1024 / WAVES;  // per wave and slice
-    static_assert(kLoads * WAVES * 1024 == ROWS * kSliceBytes, "whole loads");
-    u32x4 buffer;
-    uint32_t offset[kLoads];
-
-    __device__ __forceinline__ void init(const uint8_t *base, int64_t pitch, int valid, int wave, int lane) {
-        buffer = make_buffer(base, (valid - 1) * pitch + kSliceBytes);
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int row = (i * WAVES + wave) * 8 + lane / 8;
-            const int chunk = (lane & 7) ^ ((row >> 1) & 7);
-            offset[i] = row < valid ? (uint32_t)(row * pitch + chunk * 16) : kOutside;
-        }
-    }
-    // Load i of the current slice to `lds` (of the slice's first row).
-    __device__ __forceinline__ void issue(int i, uint32_t lds, int wave) const {
-        load16_lds(lds + (uint32_t)(i * WAVES + wave) * 1024u, offset[i], buffer);
-    }
-    // On to slice j.
-    __device__ __forceinline__ void advance(int j, int slices) {
-        const uint32_t lo = buffer[0] + kSliceBytes;
-        buffer[1] += lo < (uint32_t)kSliceBytes ? 1u : 0u;
-        buffer[0] = lo;
-        if (j >= slices) buffer[2] = 0;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) buffer[i] = (uint32_t)first_lane((int)buffer[i]);  // it stays in scalar registers
-    }
-};
-
-template <int TILE> struct TileShape;
-template <> struct TileShape<256> { static constexpr int kWavesM = 2, kWavesN = 2; };
-template <> struct TileShape<128> { static constexpr int kWavesM = 2, kWavesN = 2; };
-
 // Blocks go to the 8 XCDs round-robin: each XCD gets a contiguous run of tiles.
 __device__ __forceinline__ int xcd_run(int b, int n) {
     const int q = n >> 3, rem = n & 7, x = b & 7, p = b >> 3;
     return x * q + (x < rem ? x : rem) + p;
 }
 
-template <int TILE, bool A5, bool B5, bool F32>
-__global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN *kWave) void f8_tile_kernel(F8Matmul f) {
+// A tile of one batch entry and one part of k.
+struct Tile {
+    int64_t row0, col0, batch;
+    int split, block0, blocks;
+};
+
+template <int TILE> struct TileShape;
+template <> struct TileShape<256> { static constexpr int kWavesM = 2, kWavesN = 2; };
+template <> struct TileShape<128> { static constexpr int kWavesM = 2, kWavesN = 2; };
+
+template <int TILE>
+__device__ __forceinline__ Tile tile_at(const F8Matmul &f, int v, int total) {
+    // batch and part of k, then tiles in bands of 8 rows of tiles, down the
+    // band first: the tiles that run at once share operands in L2
+    // (quotients come from vector code: first_lane brings them back to scalar)
+    const int tm = (int)((f.m + TILE - 1) / TILE), tn = (int)((f.n + TILE - 1) / TILE);
+    int t = xcd_run(v, total);
+    const int per = tm * tn, unit = first_lane(t / per);
+    t -= unit * per;
+    const int band = first_lane(t / (8 * tn)), rows = tm - band * 8 < 8 ? tm - band * 8 : 8;
+    t -= band * 8 * tn;
+    const int col = first_lane(t / rows);
+    Tile o;
+    o.row0 = (int64_t)(band * 8 + t - col * rows) * TILE;
+    o.col0 = (int64_t)col * TILE;
+    const int batch = first_lane(unit / f.splits);
+    o.batch = batch;
+    o.split = unit - batch * f.splits;
+    o.block0 = o.split * f.chunk;
+    o.blocks = f.blocks - o.block0 < f.chunk ? f.blocks - o.block0 : f.chunk;
+    return o;
+}
+
+// The slices of a workgroup's tiles, one after the other, on their way into
+// LDS: both operands' rows and their scales (a row's dword of four blocks). A
+// lane's offsets stay: a tile and a slice are a buffer's start and length, and
+// rows past the operand's last one, like slices past the last tile's, lie
+// beyond the length and give zeros.
+template <int TILE, int WAVES>
+struct Loader {
+    static constexpr int kRowLoads = TILE * kSliceBytes / 1024 / WAVES;  // per wave, slice and operand
+    static constexpr int kScaleLoads = 2 * TILE / (WAVES * kWave);
+    static constexpr int kLoads = 2 * kRowLoads;
+    static constexpr int kOperand = TILE * kSliceBytes, kStage = 2 * kOperand;
+    // scales lie apart, a stage for each four blocks of a tile: those that a wave
+    // may still read, two slices' that are there or under way, and the next one's
+    static constexpr int kScales = kStages * kStage, kScaleStages = 4, kScaleStage = 2 * TILE * 4;
+    static_assert(kRowLoads * WAVES * 1024 == kOperand && kScaleLoads * WAVES * kWave == 2 * TILE, "whole loads");
+    u32x4 rows[2], scales[kScaleLoads];
+    uint32_t row_at[kRowLoads], scale_at;
+    int v, blocks, block;  // the tile, the end of its blocks and the next one to load
+    unsigned group;        // groups of scales so far
+
+    __device__ __forceinline__ void start(const F8Matmul &f, int v_, int total, int wave, int lane) {
+#pragma unroll
+        for (int i = 0; i < kRowLoads; ++i) {
+            const int row = (i * WAVES + wave) * 8 + lane / 8;
+            row_at[i] = (uint32_t)(row * f.pitch + (((lane & 7) ^ ((row >> 1) & 7)) << 4));
+        }
+        static_assert(TILE == 128 || TILE % (WAVES * kWave) == 0, "a wave's scale loads are of the same rows");
+        scale_at = (uint32_t)((wave * kWave % TILE + lane) * f.scale_pitch);
+        v = v_;
+        group = 0;
+        tile(f, total, wave);
+    }
+    __device__ __forceinline__ void tile(const F8Matmul &f, int total, int wave) {
+        const bool there = v < total;
+        const Tile t = tile_at<TILE>(f, there ? v : 0, total);
+        block = t.block0;
+        blocks = t.block0 + t.blocks;
+        const int64_t valid[2] = {f.m - t.row0 < TILE ? f.m - t.row0 : TILE, f.n - t.col0 < TILE ? f.n - t.col0 : TILE};
+        const uint8_t *base[2] = {f.a + t.batch * f.a_stride + t.row0 * f.pitch,
+                                  f.b + t.batch * f.b_stride + t.col0 * f.pitch};
+        const uint8_t *sbase[2] = {f.a_scale + t.batch * f.as_stride + t.row0 * f.scale_pitch,
+                                   f.b_scale + t.batch * f.bs_stride + t.col0 * f.scale_pitch};
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+            rows[o] = make_buffer(base[o] + (int64_t)block * kSliceBytes,
+                                  there ? (valid[o] - 1) * f.pitch + kSliceBytes : 0);
+#pragma unroll
+        for (int i = 0; i < kScaleLoads; ++i) {
+            const bool of_b = (i * WAVES + wave) * kWave >= TILE;
+            scales[i] = make_buffer((of_b ? sbase[1] : sbase[0]) + block,
+                                    there ? ((of_b ? valid[1] : valid[0]) - 1) * f.scale_pitch + 4 : 0);
+        }
+    }
+    // Load i of the current slice to LDS; `to`: the wave's place in the slice's stage.
+    __device__ __forceinline__ void issue(int i, uint32_t to) const {
+        const int o = i / kRowLoads, r = i % kRowLoads;
+        load16_lds(to + (uint32_t)(o * kOperand + r * WAVES * 1024), row_at[r], rows[o]);
+    }
+    // The scales of the current slice's four blocks.
+    __device__ __forceinline__ void issue_scales(uint32_t lds, int wave) {
+        const uint32_t to = lds + kScales + group++ % kScaleStages * kScaleStage + (uint32_t)wave * 256u;
+#pragma unroll
+        for (int i = 0; i < kScaleLoads; ++i) load4_lds(to + (uint32_t)(i * WAVES * 256), scale_at, scales[i]);
+    }
+    __device__ __forceinline__ void move(u32x4 &buffer, uint32_t by) {
+        const uint32_t lo = buffer[0] + by;
+        buffer[1] += lo < by ? 1u : 0u;
+        buffer[0] = lo;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) buffer[i] = (uint32_t)first_lane((int)buffer[i]);  // it stays in scalar registers
+    }
+    // On to the next slice, and its scales where they are the first of four.
+    __device__ __forceinline__ void advance(const F8Matmul &f, int total, uint32_t lds, int wave) {
+        if (++block == blocks) {
+            v += gridDim.x;
+            tile(f, total, wave);
+        } else {
+            move(rows[0], kSliceBytes);
+            move(rows[1], kSliceBytes);
+            if (block & 3) return;
+#pragma unroll
+            for (int i = 0; i < kScaleLoads; ++i) move(scales[i], 4);
+        }
+        issue_scales(lds, wave);
+    }
+};
+
+// A workgroup takes every gridDim-th tile. The loads run two slices ahead of
+// the products, on into the next tile, so that a tile's first slices are there
+// when the one before it is done, and a tile's results are on their way to
+// memory during the next one's products.
+// F32: the widened form. WIDE: results in fp32 (F32, and the parts of k of BF16 results).
+template <int TILE, bool A5, bool B5, bool F32, bool WIDE>
+__global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN *kWave) void f8_tile_kernel(F8Matmul f,
+                                                                                                         int total) {
     using S = TileShape<TILE>;
     constexpr int kWaves = S::kWavesM * S::kWavesN;
     constexpr int FM = TILE / S::kWavesM / 32, FN = TILE / S::kWavesN / 32;  // 32 x 32 blocks of a wave
-    constexpr int kOperand = TILE * kSliceBytes, kStage = 2 * kOperand;
-    constexpr int kScaleLds = kStages * kStage, kScaleStage = 2 * TILE * 4;
-    __shared__ __attribute__((aligned(1024))) char lds[kScaleLds + 2 * kScaleStage];
+    using L = Loader<TILE, kWaves>;
+    constexpr int kLoads = L::kLoads;
+    // results on their way: 32 rows of kOutBytes a wave
+    constexpr int kOutBytes = TILE / 2, kOutPitch = kOutBytes + 16;
+    constexpr int kOut = L::kScales + L::kScaleStages * L::kScaleStage;
+    __shared__ __attribute__((aligned(1024))) char lds[kOut + kWaves * 32 * kOutPitch];
     const int lane = threadIdx.x & (kWave - 1), wave = first_lane(threadIdx.x / kWave);
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char *)lds);
 
-    // batch and part of k, then tiles in bands of 8 rows of tiles, down the
-    // band first: the tiles that run at once share operands in L2
-    const int tm = (int)((f.m + TILE - 1) / TILE), tn = (int)((f.n + TILE - 1) / TILE);
-    int t = xcd_run(blockIdx.x, gridDim.x);
-    const int per = tm * tn, unit = t / per;
-    t -= unit * per;
-    const int band = t / (8 * tn), rows_left = tm - band * 8 < 8 ? tm - band * 8 : 8;
-    t -= band * 8 * tn;
-    const int64_t row0 = (int64_t)(band * 8 + t % rows_left) * TILE, col0 = (int64_t)(t / rows_left) * TILE;
-    const int64_t batch = unit / f.splits;
-    const int split = unit % f.splits;
-    const int block0 = split * f.chunk;
-    const int blocks = f.blocks - block0 < f.chunk ? f.blocks - block0 : f.chunk;
-
-    const int valid_m = (int)(f.m - row0 < TILE ? f.m - row0 : TILE), valid_n = (int)(f.n - col0 < TILE ? f.n - col0 : TILE);
-    Slices<TILE, kWaves> la, lb;
-    la.init(f.a + batch * f.a_stride + row0 * f.pitch + (int64_t)block0 * kF8Block, f.pitch, valid_m, wave, lane);
-    lb.init(f.b + batch * f.b_stride + col0 * f.pitch + (int64_t)block0 * kF8Block, f.pitch, valid_n, wave, lane);
-    // scales: one dword of four blocks for each row of a, then of b, 64 rows a load
-    constexpr int kScaleLoads = 2 * TILE / (kWaves * kWave);
-    static_assert(kScaleLoads * kWaves * kWave == 2 * TILE, "whole scale loads");
-    const int dwords = (blocks + 3) / 4;
-    u32x4 sbuffer[kScaleLoads];
-    uint32_t soffset[kScaleLoads];
-#pragma unroll
-    for (int i = 0; i < kScaleLoads; ++i) {
-        const int first = (i * kWaves + wave) * kWave;
-        const bool of_b = first >= TILE;
-        const int srow = first % TILE + lane, valid = of_b ? valid_n : valid_m;
-        const uint8_t *base = (of_b ? f.b_scale + batch * f.bs_stride + col0 * f.scale_pitch
-                                    : f.a_scale + batch * f.as_stride + row0 * f.scale_pitch) + block0;
-        sbuffer[i] = make_buffer(base, (valid - 1) * f.scale_pitch + dwords * 4);
-        soffset[i] = srow < valid ? (uint32_t)(srow * f.scale_pitch) : kOutside;
-    }
-    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>(
-        (__attribute__((address_space(3))) char *)lds);
-    auto load_scales = [&](int g) {
-#pragma unroll
-        for (int i = 0; i < kScaleLoads; ++i)
-            load4_lds(lds0 + kScaleLds + (g & 1) * kScaleStage + (i * kWaves + wave) * 256u,
-                      g < dwords && soffset[i] != kOutside ? soffset[i] + (uint32_t)g * 4 : kOutside, sbuffer[i]);
+    L loader;
+    loader.start(f, blockIdx.x, total, wave, lane);
+    auto place = [&](unsigned c) {
+        uint32_t to = lds0 + c % kStages * L::kStage + (uint32_t)wave * 1024u;
+        // opaque: each load adds its constant to this, where the compiler would
+        // keep every sum in a scalar register of its own and run out of them
+        asm volatile("" : "+s"(to));
+        return to;
     };
-
-    constexpr int kLoads = 2 * Slices<TILE, kWaves>::kLoads;
-    auto issue = [&](int j, int i) {  // load i of slice j, the current one of both operands
-        const uint32_t at = lds0 + (uint32_t)(j % kStages) * kStage;
-        if (i < kLoads / 2)
-            la.issue(i, at, wave);
-        else
-            lb.issue(i - kLoads / 2, at + kOperand, wave);
-    };
-    auto advance = [&](int j) {
-        la.advance(j, blocks);
-        lb.advance(j, blocks);
-    };
-    load_scales(0);
+    loader.issue_scales(lds0, wave);
+#pragma unroll 1
+    for (unsigned c = 0; c < kStages; ++c) {
+        const uint32_t to = place(c);
 #pragma unroll
-    for (int j = 0; j < kStages; ++j) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) issue(j, i);
-        advance(j + 1);
+        for (int i = 0; i < kLoads; ++i) loader.issue(i, to);
+        loader.advance(f, total, lds0, wave);
     }
 
     // The fragments of half a slice (64 k) in registers: b's FN, then a's FM, 32
@@ -261,19 +319,20 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
     const int row = lane & 31, half = lane >> 5;
     constexpr int kFragments = FM + FN, kReads = 2 * kFragments, kTiles = FM * FN;
     v8i fr[2][kFragments];
-    auto read = [&](auto h, int j, int r) {  // of half h of slice j
+    auto read = [&](auto h, unsigned c, int r) {  // of half h of slice c
         constexpr int H = decltype(h)::value;
-        const char *stage = lds + j % kStages * kStage;
+        const char *stage = lds + c % kStages * L::kStage;
         const int i = r / 2, chunk = 4 * H + 2 * half + r % 2;
-        const u32x4 v = *reinterpret_cast<const u32x4 *>(i < FN ? stage + kOperand + slice_at(wn + i * 32 + row, chunk)
-                                                                : stage + slice_at(wm + (i - FN) * 32 + row, chunk));
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(
+            i < FN ? stage + L::kOperand + slice_at(wn + i * 32 + row, chunk) : stage + slice_at(wm + (i - FN) * 32 + row, chunk));
 #pragma unroll
         for (int q = 0; q < 4; ++q) fr[H][i][4 * (r % 2) + q] = (int)v[q];
     };
-    // The scale bytes of slice j.
+    // The scale bytes of block b of a tile, in group g so far (tiles begin at
+    // every fourth block of k, as the scales' dwords do).
     int sc[kFragments], sc_next[kFragments];
-    auto read_scales = [&](int j) {
-        const char *s = lds + kScaleLds + (j >> 2 & 1) * kScaleStage + (j & 3);
+    auto read_scales = [&](unsigned g, int b) {
+        const char *s = lds + L::kScales + g % L::kScaleStages * L::kScaleStage + (b & 3);
 #pragma unroll
         for (int i = 0; i < kFragments; ++i)
             sc_next[i] = (int)*reinterpret_cast<const uint8_t *>(
@@ -281,15 +340,14 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
     };
     f32x16 acc[FM][FN];
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
+    for (int i = 0; i < kTiles; ++i) acc[i / FN][i % FN] = zeros();
 
     constexpr std::integral_constant<int, 0> kLow{};
     constexpr std::integral_constant<int, 1> kHigh{};
-    wait_loads<kLoads>();  // slice 0 and the first scales
+    wait_loads<kLoads>();  // slice 0 and its scales
     barrier();
-    read_scales(0);
+    Tile t = tile_at<TILE>(f, blockIdx.x, total);
+    read_scales(0, 0);
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(kLow, 0, r);
 
@@ -309,7 +367,7 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
 #pragma unroll
         for (int p = 0; p < kReads; ++p) widen_part(kLow, 0, p, sc_next);
 
-    // The products of half h of slice j, from the registers, a step for each;
+    // The products of half a slice, from the registers, a step for each;
     // extra(step) is what else the step issues, so that the matrix pipe does not
     // wait behind a run of reads, loads or conversions.
     auto products = [&](auto h, auto extra) {
@@ -346,103 +404,142 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
         }
     };
     // Steps of the low half: the reads of the high half in the first half of
-    // them, then at step kMeet all waves have read slice j and slice j + 1 has
-    // landed, so that slice j + 2 is loaded to slice j's place from there on, two
-    // (TILE 128: four) loads a step, and slice j + 1 may be read.
-    constexpr int kMeet = (kTiles * 5 + 7) / 8, kPerRead = kReads * 2 / kTiles, kPerLoad = kLoads * 2 / kTiles;
+    // them, then at step kMeet all waves have read slice c and slice c + 1 has
+    // landed, so that slice c + 2 is loaded to slice c's place from there on, and
+    // slice c + 1 may be read.
+    constexpr int kMeet = (kTiles * 5 + 7) / 8, kPerRead = kReads * 2 / kTiles;
+    constexpr int kPerLoad = kLoads * 2 / kTiles;
     static_assert(kPerRead * kTiles == 2 * kReads && kPerLoad * kTiles == 2 * kLoads, "whole steps");
-    auto load_step = [&](int j, int s) {  // s: steps from kMeet on
+    auto load_step = [&](uint32_t to, int s) {  // s: steps from kMeet on
 #pragma unroll
         for (int i = s * kPerLoad; i < (s + 1) * kPerLoad; ++i)
-            if (i < kLoads) issue(j + kStages, i);
+            if (i < kLoads) loader.issue(i, to);
     };
-    for (int j = 0; j < blocks; ++j) {
+
+    // Results as BF16 (N) or fp32, through LDS so that whole lines are written.
+    // n a multiple of the 16 bytes' columns (`even`): buffer stores, which are
+    // always issued (what lies outside is dropped), so that their number is
+    // known; otherwise plain stores.
+    const bool even = f.n % (WIDE ? 4 : 8) == 0;
+    auto write = [&](void *out, int64_t first) {
+        constexpr bool N = !WIDE;
+        constexpr int E = N ? 2 : 4, W = 16 / E;              // bytes of a value, values of a store
+        constexpr int kCols = kOutBytes / E;                      // columns at a time
+        constexpr int kLanes = kOutBytes / 16, kRows = kWave / kLanes;  // lanes of a row, rows of a store
+        static_assert(kCols % 8 == 0 && FN * 32 % kCols == 0, "whole passes");
+        char *mine = lds + kOut + wave * 32 * kOutPitch;
+        // made anew for each tile, so that no address is kept in registers meanwhile
+        int lane_ = lane;
+        asm volatile("" : "+v"(lane_));
+        const int r0 = lane_ / kLanes, c16 = lane_ % kLanes, row = lane_ & 31, half = lane_ >> 5;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int n0 = 0; n0 < FN * 32; n0 += kCols) {
+                // no accumulator leaves its register before its turn
+#pragma unroll
+                for (int n = n0 / 32; n < (n0 + kCols + 31) / 32; ++n) pin(acc[i][n]);
+#pragma unroll
+                for (int n = n0; n < n0 + kCols; n += 8) {
+                    char *at = mine + row * kOutPitch + (n - n0 + half * 4) * E;
+                    const f32x16 &v = acc[i][n / 32];
+                    const int g = n % 32 / 2;  // of the four groups of 8 columns, 4 values each
+                    if constexpr (N)
+                        *reinterpret_cast<u32x2 *>(at) = u32x2{to_bf16x2(v[g], v[g + 1]), to_bf16x2(v[g + 2], v[g + 3])};
+                    else
+                        *reinterpret_cast<f32x4 *>(at) = f32x4{v[g], v[g + 1], v[g + 2], v[g + 3]};
+                }
+                if (n0 + kCols == FN * 32)
+#pragma unroll
+                    for (int n = 0; n < FN; ++n) acc[i][n] = zeros();
+                // lanes read what others wrote (LDS accesses of a wave keep their order)
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_wave_barrier();
+                auto staged = [&](int r) { return *reinterpret_cast<const u32x4 *>(mine + (r * kRows + r0) * kOutPitch + c16 * 16); };
+                const int64_t to = t.row0 + wm + i * 32, c0 = t.col0 + wn + n0;
+                const int rows = (int)(f.m - to < 0 ? 0 : f.m - to < 32 ? f.m - to : 32);
+                const int cols = (int)(f.n - c0 < 0 ? 0 : f.n - c0 < kCols ? f.n - c0 : kCols);
+                char *p = static_cast<char *>(out) + ((first + to) * f.n + c0) * E;
+                if (even) {
+                    const __amdgpu_buffer_rsrc_t buffer = __builtin_amdgcn_make_buffer_rsrc(
+                        p, 0, rows > 0 && cols > 0 ? ((rows - 1) * (int)f.n + cols) * E : 0, 0x00020000);
+                    const uint32_t at = c16 * W < cols ? (uint32_t)(r0 * (int)f.n + c16 * W) * E : kOutside;
+#pragma unroll
+                    for (int r = 0; r < 32 / kRows; ++r)
+                        __builtin_amdgcn_raw_buffer_store_b128(staged(r), buffer, (int)(at + (uint32_t)(r * kRows * (int)f.n * E)), 0, 0);
+                } else {
+#pragma unroll 1
+                    for (int r = 0; r < 32 / kRows; ++r)
+                        if (r * kRows + r0 < rows && c16 * W + W <= cols)
+                            *reinterpret_cast<u32x4_any *>(p + ((int64_t)(r * kRows + r0) * f.n + c16 * W) * E) = staged(r);
+                    // the last columns of a row, one by one
+                    const int last = cols / W * W;
+                    if (lane_ < rows)
+#pragma unroll 1
+                        for (int c = last; c < cols; ++c) {
+                            char *q = p + ((int64_t)lane_ * f.n + c) * E;
+                            const char *from = mine + lane_ * kOutPitch + c * E;
+                            if constexpr (N)
+                                *reinterpret_cast<uint16_t *>(q) = *reinterpret_cast<const uint16_t *>(from);
+                            else
+                                *reinterpret_cast<uint32_t *>(q) = *reinterpret_cast<const uint32_t *>(from);
+                        }
+                }
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    };
+    // stores of one tile and wave
+    constexpr int kStores = FM * FN * 32 * 32 * (WIDE ? 4 : 2) / 1024, kBehind = kStores < 63 ? kStores : 63;
+    bool behind = false;
+
+    // Slice c, block j of tile t; `newer` operations may be under way behind the
+    // loads of slice c + 1 and its scales.
+    unsigned group = 0;  // of the scales of the next slice
+    auto slice = [&](unsigned c, int j, auto newer) {
+        const uint32_t to = place(c);
+        const int next = j + 1 == t.blocks ? 0 : j + 1;
+        if ((next & 3) == 0) ++group;
 #pragma unroll
         for (int i = 0; i < kFragments; ++i) sc[i] = sc_next[i];
-        if ((j & 3) == 0) load_scales((j >> 2) + 1);
         products(kLow, [&](int s) {
 #pragma unroll
             for (int r = s * kPerRead; r < (s + 1) * kPerRead; ++r)
-                if (r < kReads) read(kHigh, j, r);
+                if (r < kReads) read(kHigh, c, r);
             if (s == kMeet) {
 #pragma unroll
                 for (int i = 0; i < kFragments; ++i) hold(fr[1][i]);
-                wait_loads<0>();
+                wait_loads<decltype(newer)::value>();
                 barrier();
             }
-            if (s >= kMeet) load_step(j, s - kMeet);
+            if (s >= kMeet) load_step(to, s - kMeet);
         });
         products(kHigh, [&](int s) {
-            if (s == 0) read_scales(j + 1);
+            if (s == 0) read_scales(group, next);
 #pragma unroll
             for (int r = s * kReads / kTiles; r < (s + 1) * kReads / kTiles; ++r)
-                if (r < kReads) read(kLow, j + 1, r);
-            if (!F32) load_step(j, kTiles - kMeet + s);
+                if (r < kReads) read(kLow, c + 1, r);
+            if (!F32) load_step(to, kTiles - kMeet + s);
         });
-        advance(j + kStages + 1);
-    }
-    wait_loads<0>();  // loads past the end write LDS too
-    __syncthreads();
-
-    // 32 rows of a wave at a time through LDS, so that rows are written in
-    // stretches of FN * 32 columns
-    constexpr int kCols = FN * 32;
-    static_assert(kWaves * 32 * (kCols * 4 + 16) <= kScaleLds, "staged rows fit");
-    auto write = [&](auto narrow, void *out, int64_t first) {
-        constexpr bool N = decltype(narrow)::value;  // as BF16
-        constexpr int kPitch = kCols * (N ? 2 : 4) + 16;  // bytes of a staged row
-        constexpr int kLanes = kCols / (N ? 8 : 4);       // 16 bytes each
-        char *mine = lds + wave * 32 * kPitch;
-        const int c = lane % kLanes * (N ? 8 : 4);
-        const int64_t left = f.n - (col0 + wn + c);  // columns from this lane's on
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-#pragma unroll
-            for (int n = 0; n < FN; ++n)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    char *at = mine + row * kPitch + (n * 32 + g * 8 + half * 4) * (N ? 2 : 4);
-                    const f32x16 &v = acc[i][n];
-                    if constexpr (N)
-                        *reinterpret_cast<u32x2 *>(at) =
-                            u32x2{to_bf16x2(v[4 * g], v[4 * g + 1]), to_bf16x2(v[4 * g + 2], v[4 * g + 3])};
-                    else
-                        *reinterpret_cast<f32x4 *>(at) = f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
-                }
-            // lanes read what others wrote (LDS accesses of a wave keep their order)
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_wave_barrier();
-            u32x4 v[32 * kLanes / kWave];
-#pragma unroll
-            for (int r = 0; r < 32 * kLanes / kWave; ++r)
-                v[r] = *reinterpret_cast<const u32x4 *>(mine + (r * (kWave / kLanes) + lane / kLanes) * kPitch + lane % kLanes * 16);
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_wave_barrier();
-            const int64_t to = row0 + wm + i * 32 + lane / kLanes;
-            char *p = static_cast<char *>(out) + ((first + to) * f.n + col0 + wn + c) * (N ? 2 : 4);
-#pragma unroll
-            for (int r = 0; r < 32 * kLanes / kWave; ++r) {
-                char *q = p + (int64_t)r * (kWave / kLanes) * f.n * (N ? 2 : 4);
-                if (to + r * (kWave / kLanes) >= f.m) continue;
-                if (left >= (N ? 8 : 4)) {
-                    *reinterpret_cast<u32x4_any *>(q) = v[r];
-                } else {
-#pragma unroll
-                    for (int j = 0; j < (N ? 8 : 4); ++j)
-                        if (j < left) {
-                            if constexpr (N)
-                                reinterpret_cast<uint16_t *>(q)[j] = (uint16_t)(v[r][j / 2] >> (j % 2 * 16));
-                            else
-                                reinterpret_cast<uint32_t *>(q)[j] = v[r][j];
-                        }
-                }
-            }
-        }
+        for (int i = 0; i < kTiles; ++i) pin(acc[i / FN][i % FN]);
+        loader.advance(f, total, lds0, wave);
     };
-    if (f.splits > 1)
-        write(std::false_type{}, f.partial, (split * (int64_t)f.batch + batch) * f.m);
-    else
-        write(std::integral_constant<bool, !F32>{}, f.out, batch * f.m);
+    unsigned c = 0;  // slices so far
+    for (int v = blockIdx.x; v < total; v += gridDim.x) {
+        int j = 0;
+        if (behind) slice(c++, j++, std::integral_constant<int, kBehind>{});
+#pragma unroll 1
+        for (; j < t.blocks; ++j, ++c) slice(c, j, kLow);
+        if constexpr (WIDE)
+            write(f.splits > 1 ? f.partial : f.out, (f.splits > 1 ? t.split * (int64_t)f.batch + t.batch : t.batch) * f.m);
+        else
+            write(f.out, t.batch * f.m);
+        behind = even;
+        if (v + (int)gridDim.x < total) t = tile_at<TILE>(f, v + gridDim.x, total);
+    }
+    wait_loads<0>();  // loads past the last tile write LDS too
 }
 
 // ---------------------------------------------------------------------------
@@ -548,12 +645,16 @@ void launch(const F8Matmul &f, hipStream_t s) {
             f8_rows_kernel<4, A5, B5, F32><<<grid, threads, lds, s>>>(f);
         return;
     }
-    const int64_t tiles = (f.m + f.tile - 1) / f.tile * ((f.n + f.tile - 1) / f.tile);
-    const dim3 grid((unsigned)(tiles * f.batch * f.splits));
+    const int total = (int)((f.m + f.tile - 1) / f.tile * ((f.n + f.tile - 1) / f.tile)) * f.batch * f.splits;
+    // one workgroup a compute unit (TILE 128: two), a multiple of the XCDs
+    const int most = device_cus() / 8 * 8 * (f.tile == 256 ? 1 : 2);
+    const dim3 grid((unsigned)(total < most ? total : most));
     if (f.tile == 256)
-        f8_tile_kernel<256, A5, B5, F32><<<grid, 256, 0, s>>>(f);
+        f.splits > 1 ? f8_tile_kernel<256, A5, B5, F32, true><<<grid, 256, 0, s>>>(f, total)
+                     : f8_tile_kernel<256, A5, B5, F32, F32><<<grid, 256, 0, s>>>(f, total);
     else
-        f8_tile_kernel<128, A5, B5, F32><<<grid, 256, 0, s>>>(f);
+        f.splits > 1 ? f8_tile_kernel<128, A5, B5, F32, true><<<grid, 256, 0, s>>>(f, total)
+                     : f8_tile_kernel<128, A5, B5, F32, F32><<<grid, 256, 0, s>>>(f, total);
 }
 
 template <bool F32>
