@@ -432,6 +432,18 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
         int lane_ = lane;
         asm volatile("" : "+v"(lane_));
         const int r0 = lane_ / kLanes, c16 = lane_ % kLanes, row = lane_ & 31, half = lane_ >> 5;
+        // the wave's part of the tile: what exists of it, and a buffer over that
+        const int64_t row1 = t.row0 + wm, col1 = t.col0 + wn;
+        const int rows = (int)(f.m - row1 < 0 ? 0 : f.m - row1 < FM * 32 ? f.m - row1 : FM * 32);
+        const int cols = (int)(f.n - col1 < 0 ? 0 : f.n - col1 < FN * 32 ? f.n - col1 : FN * 32);
+        const int pitch = (int)f.n * E;
+        char *p = static_cast<char *>(out) + ((first + row1) * f.n + col1) * E;
+        const __amdgpu_buffer_rsrc_t buffer =
+            __builtin_amdgcn_make_buffer_rsrc(p, 0, rows > 0 && cols > 0 ? (rows - 1) * pitch + cols * E : 0, 0x00020000);
+        uint32_t at[FN * 32 / kCols];  // of the lane's columns of each pass, in row r0
+#pragma unroll
+        for (int n0 = 0; n0 < FN * 32; n0 += kCols)
+            at[n0 / kCols] = n0 + c16 * W < cols ? (uint32_t)(r0 * pitch + (n0 + c16 * W) * E) : kOutside;
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -441,13 +453,13 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
                 for (int n = n0 / 32; n < (n0 + kCols + 31) / 32; ++n) pin(acc[i][n]);
 #pragma unroll
                 for (int n = n0; n < n0 + kCols; n += 8) {
-                    char *at = mine + row * kOutPitch + (n - n0 + half * 4) * E;
+                    char *to = mine + row * kOutPitch + (n - n0 + half * 4) * E;
                     const f32x16 &v = acc[i][n / 32];
                     const int g = n % 32 / 2;  // of the four groups of 8 columns, 4 values each
                     if constexpr (N)
-                        *reinterpret_cast<u32x2 *>(at) = u32x2{to_bf16x2(v[g], v[g + 1]), to_bf16x2(v[g + 2], v[g + 3])};
+                        *reinterpret_cast<u32x2 *>(to) = u32x2{to_bf16x2(v[g], v[g + 1]), to_bf16x2(v[g + 2], v[g + 3])};
                     else
-                        *reinterpret_cast<f32x4 *>(at) = f32x4{v[g], v[g + 1], v[g + 2], v[g + 3]};
+                        *reinterpret_cast<f32x4 *>(to) = f32x4{v[g], v[g + 1], v[g + 2], v[g + 3]};
                 }
                 if (n0 + kCols == FN * 32)
 #pragma unroll
@@ -456,29 +468,27 @@ __global__ __launch_bounds__(TileShape<TILE>::kWavesM *TileShape<TILE>::kWavesN 
                 asm volatile("" ::: "memory");
                 __builtin_amdgcn_wave_barrier();
                 auto staged = [&](int r) { return *reinterpret_cast<const u32x4 *>(mine + (r * kRows + r0) * kOutPitch + c16 * 16); };
-                const int64_t to = t.row0 + wm + i * 32, c0 = t.col0 + wn + n0;
-                const int rows = (int)(f.m - to < 0 ? 0 : f.m - to < 32 ? f.m - to : 32);
-                const int cols = (int)(f.n - c0 < 0 ? 0 : f.n - c0 < kCols ? f.n - c0 : kCols);
-                char *p = static_cast<char *>(out) + ((first + to) * f.n + c0) * E;
                 if (even) {
-                    const __amdgpu_buffer_rsrc_t buffer = __builtin_amdgcn_make_buffer_rsrc(
-                        p, 0, rows > 0 && cols > 0 ? ((rows - 1) * (int)f.n + cols) * E : 0, 0x00020000);
-                    const uint32_t at = c16 * W < cols ? (uint32_t)(r0 * (int)f.n + c16 * W) * E : kOutside;
+                    u32x4 v[32 / kRows];
+#pragma unroll
+                    for (int r = 0; r < 32 / kRows; ++r) v[r] = staged(r);
 #pragma unroll
                     for (int r = 0; r < 32 / kRows; ++r)
-                        __builtin_amdgcn_raw_buffer_store_b128(staged(r), buffer, (int)(at + (uint32_t)(r * kRows * (int)f.n * E)), 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            v[r], buffer, (int)(at[n0 / kCols] + (uint32_t)((i * 32 + r * kRows) * pitch)), 0, 0);
                 } else {
+                    const int here = cols - n0;  // columns from this pass's first on
 #pragma unroll 1
                     for (int r = 0; r < 32 / kRows; ++r)
-                        if (r * kRows + r0 < rows && c16 * W + W <= cols)
-                            *reinterpret_cast<u32x4_any *>(p + ((int64_t)(r * kRows + r0) * f.n + c16 * W) * E) = staged(r);
+                        if (i * 32 + r * kRows + r0 < rows && c16 * W + W <= here)
+                            *reinterpret_cast<u32x4_any *>(p + (int64_t)(i * 32 + r * kRows + r0) * pitch + (n0 + c16 * W) * E) =
+                                staged(r);
                     // the last columns of a row, one by one
-                    const int last = cols / W * W;
-                    if (lane_ < rows)
+                    if (here > 0 && here < kCols && i * 32 + row < rows && half == 0)
 #pragma unroll 1
-                        for (int c = last; c < cols; ++c) {
-                            char *q = p + ((int64_t)lane_ * f.n + c) * E;
-                            const char *from = mine + lane_ * kOutPitch + c * E;
+                        for (int c = here / W * W; c < here; ++c) {
+                            char *q = p + (int64_t)(i * 32 + row) * pitch + (n0 + c) * E;
+                            const char *from = mine + row * kOutPitch + c * E;
                             if constexpr (N)
                                 *reinterpret_cast<uint16_t *>(q) = *reinterpret_cast<const uint16_t *>(from);
                             else

@@ -71,14 +71,15 @@ size_t norm_workspace(int32_t workers, int64_t rows, int64_t cols) {
 // ---------------------------------------------------------------------------
 // 8-bit floating point
 // ---------------------------------------------------------------------------
-constexpr int64_t kMaxK = (int64_t)1 << 22;  // k and n: a tile's rows of operands and of out lie within 2^31 bytes
+constexpr int64_t kMaxK = (int64_t)1 << 22;     // a tile's rows of an operand lie within 2^31 bytes
+constexpr int64_t kMaxF8Cols = (int64_t)1 << 21;  // and so do a wave's rows of out
 constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;  // of a launch
 
 inline bool f8_ok(int f) { return f == SIGNMUON_E4M3 || f == SIGNMUON_E5M2; }
 
 int check_f8_matmul(int64_t batch, int64_t m, int64_t n, int64_t k) {
     if (batch < 1 || m < 1 || n < 1 || k < 1) return SIGNMUON_EINVAL;
-    if (batch > kMaxWorkers || m > kMaxTokens || n > kMaxK || k > kMaxK) return SIGNMUON_ERANGE;
+    if (batch > kMaxWorkers || m > kMaxTokens || n > kMaxF8Cols || k > kMaxK) return SIGNMUON_ERANGE;
     const sm::F8Plan p = sm::f8_plan(batch, m, n, k);
     if (p.tile == 16) return batch * ((n + 15) / 16) * p.waves * 64 > kMaxThreads ? SIGNMUON_ERANGE : SIGNMUON_OK;
     const int64_t tiles = ((m + p.tile - 1) / p.tile) * ((n + p.tile - 1) / p.tile);
