@@ -28,7 +28,7 @@
 // bytes, four slices deep, fetched each line twice: 650 us where this takes
 // 595, at 16384 x 11008 x 4096). Their 16-byte chunks are XOR-swizzled so that
 // 16 consecutive rows' reads fall on all banks.
-// f8_rows_kernel: up to 64 rows of a. Bound by reading b once: no LDS on the
+// f8_rows_kernel: up to 32 rows of a. Bound by reading b once: no LDS on the
 // way, each wave reads whole 128-byte lines of b into the instruction's
 // layout, and the waves of a workgroup share k.
 // f8_sums_kernel: adds the parts of k that several workgroups computed.
@@ -575,40 +575,54 @@ __global__ __launch_bounds__(512) void f8_rows_kernel(F8Matmul f) {
         a[i] = f.a + batch * f.a_stride + r * f.pitch + part * 32;
         as[i] = f.a_scale + batch * f.as_stride + r * f.scale_pitch;
     }
-    f32x4 acc[MF] = {};
-    const int groups = (f.blocks + 3) / 4;
-    for (int g = wave; g < groups; g += f.waves) {
-        const int left = f.blocks - g * 4;  // blocks of this group
-        const int sb = *reinterpret_cast<const int *>(bs + g * 4);
-        int sa[MF];
+    // Four blocks of both operands and their scales. Blocks past the last one
+    // read the group's first: their products are not taken.
+    struct Group {
+        v8i b[4], a[4][MF];
+        int sb, sa[MF];
+    };
+    auto load = [&](Group &o, int g) {
+        o.sb = *reinterpret_cast<const int *>(bs + g * 4);
 #pragma unroll
-        for (int i = 0; i < MF; ++i) sa[i] = *reinterpret_cast<const int *>(as[i] + g * 4);
-        v8i fb[4], fa[4][MF];
+        for (int i = 0; i < MF; ++i) o.sa[i] = *reinterpret_cast<const int *>(as[i] + g * 4);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int64_t at = (int64_t)(g * 4 + (k < left ? k : 0)) * kF8Block;
-            fb[k] = join(*reinterpret_cast<const u32x4 *>(b + at), *reinterpret_cast<const u32x4 *>(b + at + 16));
+            const int64_t at = (int64_t)(g * 4 + (g * 4 + k < f.blocks ? k : 0)) * kF8Block;
+            o.b[k] = join(*reinterpret_cast<const u32x4 *>(b + at), *reinterpret_cast<const u32x4 *>(b + at + 16));
 #pragma unroll
             for (int i = 0; i < MF; ++i)
-                fa[k][i] = join(*reinterpret_cast<const u32x4 *>(a[i] + at), *reinterpret_cast<const u32x4 *>(a[i] + at + 16));
+                o.a[k][i] = join(*reinterpret_cast<const u32x4 *>(a[i] + at), *reinterpret_cast<const u32x4 *>(a[i] + at + 16));
         }
+    };
+    f32x4 acc[MF] = {};
+    auto products = [&](const Group &o, int g) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (k < left)
+            if (g * 4 + k < f.blocks)
 #pragma unroll
                 for (int i = 0; i < MF; ++i) {
                     if constexpr (F32) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
                             acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                widen<B5>(fb[k], q, scale_of(sb >> (8 * k) & 255)),
-                                widen<A5>(fa[k][i], q, scale_of(sa[i] >> (8 * k) & 255)),
-                                acc[i], 0, 0, 0);
+                                widen<B5>(o.b[k], q, scale_of(o.sb >> (8 * k) & 255)),
+                                widen<A5>(o.a[k][i], q, scale_of(o.sa[i] >> (8 * k) & 255)), acc[i], 0, 0, 0);
                     } else {
                         acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            fb[k], fa[k][i], acc[i], B5 ? 1 : 0, A5 ? 1 : 0, 0, sb >> (8 * k), 0, sa[i] >> (8 * k));
+                            o.b[k], o.a[k][i], acc[i], B5 ? 1 : 0, A5 ? 1 : 0, 0, o.sb >> (8 * k), 0, o.sa[i] >> (8 * k));
                     }
                 }
+    };
+    // the next group is on its way while one is multiplied
+    const int groups = (f.blocks + 3) / 4;
+    Group even, odd;
+    if (wave < groups) load(even, wave);
+    for (int g = wave; g < groups; g += 2 * f.waves) {
+        if (g + f.waves < groups) load(odd, g + f.waves);
+        products(even, g);
+        if (g + f.waves >= groups) break;
+        if (g + 2 * f.waves < groups) load(even, g + 2 * f.waves);
+        products(odd, g + f.waves);
     }
 #pragma unroll
     for (int i = 0; i < MF; ++i) *reinterpret_cast<f32x4 *>(sums + ((wave * MF + i) * kWave + lane) * 4) = acc[i];
@@ -645,14 +659,12 @@ void launch(const F8Matmul &f, hipStream_t s) {
     if (f.tile == 16) {
         const dim3 grid((unsigned)(f.batch * ((f.n + 15) / 16)));
         const int threads = f.waves * kWave;
-        const int mf = f.m <= 16 ? 1 : f.m <= 32 ? 2 : 4;
+        const int mf = f.m <= 16 ? 1 : 2;
         const size_t lds = (size_t)mf * threads * 16;
         if (mf == 1)
             f8_rows_kernel<1, A5, B5, F32><<<grid, threads, lds, s>>>(f);
-        else if (mf == 2)
-            f8_rows_kernel<2, A5, B5, F32><<<grid, threads, lds, s>>>(f);
         else
-            f8_rows_kernel<4, A5, B5, F32><<<grid, threads, lds, s>>>(f);
+            f8_rows_kernel<2, A5, B5, F32><<<grid, threads, lds, s>>>(f);
         return;
     }
     const int total = (int)((f.m + f.tile - 1) / f.tile * ((f.n + f.tile - 1) / f.tile)) * f.batch * f.splits;
@@ -682,21 +694,46 @@ F8Plan f8_plan(int64_t batch, int64_t m, int64_t n, int64_t k) {
     F8Plan p{};
     p.splits = 1;
     p.chunk = (int32_t)(groups * 4);
-    if (m <= 64) {
+    // Few rows: each tile of 16 columns reads all of a, which costs more than b
+    // from about 32 rows on (n = 11008, k = 4096: 22.6 us at 32 rows and 30 at 48,
+    // where tiles of 128 take 20 and 21; n = k = 4096: 9.2 and 11.8 against 12.1 and 12.6).
+    if (m <= 32) {
         p.tile = 16;
+        // waves that share a tile's k: 2 to 8, until each has one group of four
+        // blocks or the device is full
         const int64_t wgs = batch * ((n + 15) / 16);
-        p.waves = 4;
+        p.waves = 2;
         while (p.waves < 8 && p.waves < groups && wgs * p.waves < 2048) p.waves *= 2;
         return p;
     }
-    auto tiles = [&](int64_t t) { return batch * ((m + t - 1) / t) * ((n + t - 1) / t); };
-    p.tile = tiles(256) >= 192 ? 256 : 128;
-    // parts of k until every compute unit has a workgroup, at least 4 blocks each
-    const int64_t want = p.tile == 256 ? 256 : 512, have = tiles(p.tile);
-    int64_t splits = have >= want ? 1 : want / have;
-    if (splits > groups) splits = groups;
-    p.chunk = (int32_t)((groups + splits - 1) / splits * 4);
-    p.splits = (int32_t)((blocks + p.chunk - 1) / p.chunk);
+    // The tile and the parts of k (at least 4 blocks each) of the least time by
+    // this model, in units of about half a microsecond, fitted to both tiles at
+    // 8 to 11008 tiles and 6 to 64 blocks: a round of tiles (one of 256 or two of
+    // 128 a compute unit) takes 3 units a block and 10 more, or 2 and 4 more;
+    // adding the parts takes 10 and 2 MB of partial sums written or read a unit.
+    // E.g. 8192 x 2304 x 768 to bf16: 288 tiles of 256 in two rounds, 30.7 us, 1152 of
+    // 128 in three short ones, 25 us; 8 x 768 x 2304 x 2000 to fp32: 216 tiles in one
+    // round, 62 us, 864 in two, 66 us.
+    double best = 0.0;
+    for (const int32_t tile : {256, 128}) {
+        const int64_t tiles = batch * ((m + tile - 1) / tile) * ((n + tile - 1) / tile);
+        const int64_t slots = tile == 256 ? 256 : 512;
+        int32_t last = 0;
+        for (int64_t splits = 1; splits <= groups && splits <= 32; ++splits) {
+            const int64_t chunk = (groups + splits - 1) / splits * 4, parts = (blocks + chunk - 1) / chunk;
+            if (chunk == last) continue;
+            last = (int32_t)chunk;
+            const double rounds = (double)((tiles * parts + slots - 1) / slots);
+            double time = rounds * (tile == 256 ? 3.0 * chunk + 10.0 : 2.0 * chunk + 4.0);
+            if (parts > 1) time += 10.0 + 8.0 * (double)(parts * batch) * (double)m * (double)n / 2e6;
+            if (p.tile == 0 || time < best) {
+                best = time;
+                p.tile = tile;
+                p.chunk = (int32_t)chunk;
+                p.splits = (int32_t)parts;
+            }
+        }
+    }
     return p;
 }
 

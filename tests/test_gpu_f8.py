@@ -173,8 +173,8 @@ def check_product(got, want, tol):
 
 
 # one row, few rows, rows around each kernel's border, several tiles, parts of k
-PRODUCTS = [(1, 1, 1), (1, 17, 128), (1, 300, 700), (5, 16, 129), (16, 33, 513), (17, 100, 2000), (33, 64, 640),
-            (64, 129, 1111), (65, 1, 5), (65, 200, 100), (127, 128, 128), (129, 257, 384), (200, 140, 3000),
+PRODUCTS = [(1, 1, 1), (1, 17, 128), (1, 300, 700), (5, 16, 129), (16, 33, 513), (17, 100, 2000), (32, 50, 3500),
+            (33, 64, 640), (64, 129, 1111), (65, 1, 5), (65, 200, 100), (127, 128, 128), (129, 257, 384), (200, 140, 3000),
             (300, 90, 1537)]
 
 
@@ -227,6 +227,36 @@ def test_f32_products_keep_fp32(m, n):
     got = multiply(a, b, k, (m, n), torch.float32).double()
     row = (got - want).norm(dim=-1) / want.norm(dim=-1)
     assert float(row.max()) <= 2.0 ** -23 * (2 * k) ** 0.5
+
+
+@pytest.mark.parametrize("m,n,k", [(4096, 2048, 22100), (4090, 2046, 22100)])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_a_long_sum_in_parts(m, n, k, out_dtype):
+    """Many tokens of a weight's gradient: large tiles, k in parts, with and
+    without a ragged edge. The operands are quantised on the GPU (compared bit
+    for bit above)."""
+    assert sm.signmuon_f8_matmul_workspace_bytes(1, m, n, k) == 2 * m * n * 4
+    g = torch.Generator(device=DEV).manual_seed(12)
+    values, pairs = [], []
+    for rows in (m, n):
+        x = torch.randn(rows, k, generator=g, device=DEV)
+        q, s = sm.f8_empty((rows, k), E4, DEV)
+        sm.signmuon_f8_quant(x, q, s)
+        blocks = up(k, 128) // 128
+        values.append((q.double().unflatten(-1, (blocks, 128)) * torch.exp2(s[:, :blocks].double() - 127)[..., None]).flatten(-2))
+        pairs.append((q, s))
+    got = multiply(*pairs, k, (m, n), out_dtype).to(DEV).double()
+    va, vb = values[0], values[1].t().contiguous()
+    want = va @ vb
+    # F32: errors of random sign add as their root. BF16: half a step, and a cut of at most 8 * 2^-13 of the
+    # largest of 8 products, which is at most their sizes' sum
+    norm = float((got - want).norm() / want.norm())
+    if out_dtype == torch.float32:
+        assert norm <= 2.0 ** -23 * (2 * k) ** 0.5
+    else:
+        assert norm <= 2.0 ** -8
+        size = va.abs() @ vb.abs()
+        assert bool(((got - want).abs() <= 2.0 ** -10 * size + 2.0 ** -8 * want.abs()).all())
 
 
 @pytest.mark.parametrize("m", [3, 150])
