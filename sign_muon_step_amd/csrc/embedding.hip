@@ -27,6 +27,7 @@ namespace sm {
 namespace {
 
 constexpr int kWave = 64;
+static_assert(kSortChunk == 4 * 1024, "sorted by 1024 threads, 4 keys each");
 
 // The id of token t, or vocab where it lies outside [0, vocab).
 __device__ __forceinline__ uint32_t token_id(const void *ids, bool id64, int64_t t, uint32_t vocab) {
@@ -47,14 +48,11 @@ __global__ __launch_bounds__(256) void embed_kernel(Embed e, int lg) {
     const uint32_t id = token_id(e.ids, e.id64, t, (uint32_t)e.vocab);
     const bool there = id < (uint32_t)e.vocab;
     for (int64_t c = (int64_t)(threadIdx.x & ((1 << lg) - 1)) * 8; c < e.cols; c += step) {
-        const int n = (int)(e.cols - c < 8 ? e.cols - c : 8);
-        float v[8] = {};
-        if (there) {
-            load_n<TB>(e.table, (int64_t)id * e.cols + c, n, v);
+        float v[8];
+        unpack(load_raw<TB, 8>(e.table, there ? (int64_t)id * e.cols : 0, c, e.cols), c, e.cols, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= e.scale;
-        }
-        store_n<YB>(e.y, t * e.cols + c, n, v);
+        for (int j = 0; j < 8; ++j) v[j] = there ? v[j] * e.scale : 0.0f;
+        store_n<YB>(e.y, t * e.cols + c, (int)(e.cols - c < 8 ? e.cols - c : 8), v);
     }
 }
 
@@ -63,41 +61,45 @@ __global__ __launch_bounds__(256) void embed_kernel(Embed e, int lg) {
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / kWave;
-constexpr int kSortRounds = kSortChunk / kSortThreads;  // keys a thread
 
-// Keys id << 32 | token of one chunk, sorted. Wave w holds places 256 w ..
-// 256 w + 255 of the current order, 64 a round, so that a key's rank among its
-// digit is: those of earlier waves + those of earlier rounds of its wave +
-// those of lower lanes of its round.
-__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedGrad e, int chunks, int bits) {
-    __shared__ uint64_t keys[kSortChunk];
+// Keys id << 32 | token of one chunk of up to 1024 R, sorted by `passes` digits
+// of `width` bits (at most 8). Wave w holds places 64 R w .. of the current
+// order, 64 a round, so that a key's rank among its digit is: those of earlier
+// waves + those of earlier rounds of its wave + those of lower lanes of its
+// round. Latency counts here (a workgroup for each worker's 4096 tokens), so a
+// digit's counts of the sixteen waves are read at once and added in registers.
+template <int R>
+__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedGrad e, int chunks, int passes, int width) {
+    __shared__ uint64_t keys[kSortThreads * R];
     __shared__ uint32_t count[kSortWaves][256];
     __shared__ uint32_t wave_total[4];
     const int worker = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
     const int64_t first = (int64_t)chunk * kSortChunk;
     const int n = (int)(e.tokens - first < kSortChunk ? e.tokens - first : kSortChunk);
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int place = wave * (kWave * kSortRounds) + lane;
+    const int place = wave * (kWave * R) + lane;
+    const uint32_t mask = (1u << width) - 1;
 
-    uint64_t key[kSortRounds];
+    uint64_t key[R];
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
+    for (int r = 0; r < R; ++r) {
         const int i = place + r * kWave;
         // places past the chunk: behind every token, as their place is
         const uint32_t id =
             i < n ? token_id(e.ids, e.id64, worker * e.tokens + first + i, (uint32_t)e.vocab) : (uint32_t)e.vocab;
         key[r] = (uint64_t)id << 32 | (uint32_t)(first + i);
     }
-    for (int shift = 32; shift < 32 + bits; shift += 8) {
+    for (int p = 0; p < passes; ++p) {
+        const int shift = 32 + p * width;
         for (int i = threadIdx.x; i < kSortWaves * 256; i += kSortThreads) (&count[0][0])[i] = 0;
         __syncthreads();
-        uint32_t rank[kSortRounds];
+        uint32_t rank[R];
 #pragma unroll
-        for (int r = 0; r < kSortRounds; ++r) {
-            const uint32_t digit = (uint32_t)(key[r] >> shift) & 255u;
+        for (int r = 0; r < R; ++r) {
+            const uint32_t digit = (uint32_t)(key[r] >> shift) & mask;
             uint64_t same = ~0ull;
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
+            for (int b = 0; b < 8; ++b) {  // bits past the width are 0 in every lane
                 const bool bit = (digit >> b) & 1u;
                 const uint64_t m = __ballot(bit);
                 same &= bit ? m : ~m;
@@ -115,13 +117,12 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedGrad e, i
         }
         __syncthreads();
         // exclusive sums over digits, then waves
-        uint32_t total = 0, inclusive = 0;
+        uint32_t own[kSortWaves], total = 0, inclusive = 0;
         if (threadIdx.x < 256) {
-            for (int w = 0; w < kSortWaves; ++w) {
-                const uint32_t c = count[w][threadIdx.x];
-                count[w][threadIdx.x] = total;
-                total += c;
-            }
+#pragma unroll
+            for (int w = 0; w < kSortWaves; ++w) own[w] = count[w][threadIdx.x];
+#pragma unroll
+            for (int w = 0; w < kSortWaves; ++w) total += own[w];
             inclusive = total;
 #pragma unroll
             for (int d = 1; d < kWave; d <<= 1) {
@@ -133,20 +134,25 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedGrad e, i
         __syncthreads();
         if (threadIdx.x < 256) {
             uint32_t base = inclusive - total;
-            for (int w = 0; w < wave; ++w) base += wave_total[w];
-            for (int w = 0; w < kSortWaves; ++w) count[w][threadIdx.x] += base;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                if (w < wave) base += wave_total[w];
+#pragma unroll
+            for (int w = 0; w < kSortWaves; ++w) {
+                count[w][threadIdx.x] = base;
+                base += own[w];
+            }
         }
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < kSortRounds; ++r)
-            keys[count[wave][(uint32_t)(key[r] >> shift) & 255u] + rank[r]] = key[r];
+        for (int r = 0; r < R; ++r) keys[count[wave][(uint32_t)(key[r] >> shift) & mask] + rank[r]] = key[r];
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < kSortRounds; ++r) key[r] = keys[place + r * kWave];
+        for (int r = 0; r < R; ++r) key[r] = keys[place + r * kWave];
     }
     uint64_t *out = e.keys[0] + worker * e.tokens + first;
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r)
+    for (int r = 0; r < R; ++r)
         if (place + r * kWave < n) out[place + r * kWave] = key[r];
 }
 
@@ -163,6 +169,21 @@ __device__ __forceinline__ int64_t lower_bound(const uint64_t *keys, int64_t n, 
         }
     }
     return lo;
+}
+
+// The same by a whole wave: 64 probes at a time, so two dependent loads for 4096
+// keys where one lane's search takes twelve.
+__device__ __forceinline__ int64_t wave_lower_bound(const uint64_t *keys, int64_t n, uint64_t key, int lane) {
+    int64_t lo = 0, len = n;
+    while (len > kWave) {
+        const int64_t step = (len + kWave - 1) / kWave;  // probe i: the last key of its step
+        const int64_t at = (lane + 1) * step - 1;
+        const int64_t below = __popcll(__ballot(keys[lo + (at < len ? at : len - 1)] < key)) * step;
+        if (below >= len) return lo + len;
+        lo += below;
+        len = len - below < step ? len - below : step;
+    }
+    return lo + __popcll(__ballot(lane < len && keys[lo + (lane < len ? lane : 0)] < key));
 }
 
 // Runs of `run` sorted keys into runs of 2 * run. Keys differ (a token is in
@@ -186,21 +207,20 @@ __global__ __launch_bounds__(256) void embed_merge_kernel(const uint64_t *from, 
 // ---------------------------------------------------------------------------
 // Sums
 // ---------------------------------------------------------------------------
-template <bool GB>
+// The gradient of a row's columns from their sum; `old`: what is there, to add to.
+template <bool GB, bool ADD>
 __device__ __forceinline__ void write_row(const EmbedGrad &e, int64_t worker, uint32_t id, int64_t c, int n,
-                                          const float (&sum)[4]) {
+                                          const float (&sum)[4], const Raw<GB, 4> &old) {
     float v[4];
-    const int64_t at = (worker * e.vocab + id) * e.cols + c;
-    if (n <= 0) return;
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = e.scale * sum[j];
-    if (e.accumulate) {
-        float old[4];
-        load_n<GB>(e.grad, at, n, old);
+    if constexpr (ADD) {
+        float o[4];
+        unpack(old, c, e.cols, o);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] += old[j];
+        for (int j = 0; j < 4; ++j) v[j] += o[j];
     }
-    store_n<GB>(e.grad, at, n, v);
+    if (n > 0) store_n<GB>(e.grad, (worker * e.vocab + id) * e.cols + c, n, v);
 }
 
 __device__ __forceinline__ void write_partial(const EmbedGrad &e, int64_t worker, int seg, int which, int64_t c,
@@ -208,30 +228,41 @@ __device__ __forceinline__ void write_partial(const EmbedGrad &e, int64_t worker
     if (n > 0) store_n<false>(e.partial, ((worker * e.segments + seg) * 2 + which) * e.cols + c, n, sum);
 }
 
-// Zeros in the rows of 64 ids that no token has. Rows that follow each other
-// are one stretch of memory.
+// Zeros in the rows of kZeroRows ids that no token has. Rows that follow each
+// other are one stretch of memory. (Few ids a wave: the search in the keys is a
+// chain of loads, which other waves' stores hide.)
+constexpr int kZeroRows = 16;
 template <bool GB>
 __device__ void zero_rows(const EmbedGrad &e, const uint64_t *keys, int64_t worker, int64_t v0, int lane) {
-    const int64_t v = v0 + lane;
-    bool empty = false;
-    if (v < e.vocab) {
-        const int64_t at = lower_bound(keys, e.tokens, (uint64_t)v << 32);
-        empty = at >= e.tokens || (int64_t)(keys[at] >> 32) != v;
+    // the ids that there are: from the keys behind the first of them, and again
+    // behind the last one seen where 64 keys do not reach past the group
+    const int64_t v1 = v0 + kZeroRows < e.vocab ? v0 + kZeroRows : e.vocab;
+    uint64_t mask = ~0ull >> (kWave - (int)(v1 - v0));
+    for (int64_t v = v0; v < v1;) {
+        const int64_t at = wave_lower_bound(keys, e.tokens, (uint64_t)v << 32, lane) + lane;
+        const int64_t id = at < e.tokens ? (int64_t)(keys[at] >> 32) : e.vocab;
+        uint32_t seen = id < v1 ? 1u << (int)(id - v0) : 0u;
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) seen |= __shfl_xor(seen, d);
+        mask &= ~(uint64_t)seen;
+        v = (int64_t)__shfl((unsigned long long)id, kWave - 1) + 1;
     }
-    uint64_t mask = __ballot(empty);
-    const float zero[8] = {};
+    constexpr int W = GB ? 8 : 4;  // 16 bytes a lane, side by side
+    const float zero[W] = {};
     while (mask) {
         const int first = __builtin_ctzll(mask);
         const uint64_t rest = ~(mask >> first);
         const int count = rest ? __builtin_ctzll(rest) : kWave - first;  // rows of this stretch
         const int64_t at = (worker * e.vocab + v0 + first) * e.cols, len = count * e.cols;
-        for (int64_t i = (int64_t)lane * 8; i < len; i += kWave * 8)
-            store_n<GB>(e.grad, at + i, (int)(len - i < 8 ? len - i : 8), zero);
+        for (int64_t i = (int64_t)lane * W; i < len; i += kWave * W)
+            store_n<GB>(e.grad, at + i, (int)(len - i < W ? len - i : W), zero);
         mask = first + count >= kWave ? 0 : mask >> (first + count) << (first + count);
     }
 }
 
-template <bool DB, bool GB>
+constexpr int kInFlight = 16;  // rows that a wave has under way
+
+template <bool DB, bool GB, bool ADD>
 __global__ __launch_bounds__(256) void embed_sums_kernel(EmbedGrad e, const uint64_t *keys, int64_t sum_waves,
                                                          int64_t waves) {
     const int lane = threadIdx.x & (kWave - 1);
@@ -239,9 +270,9 @@ __global__ __launch_bounds__(256) void embed_sums_kernel(EmbedGrad e, const uint
     if (w >= waves) return;
     if (w >= sum_waves) {  // rows that no token has
         w -= sum_waves;
-        const int64_t groups = (e.vocab + kWave - 1) / kWave;
+        const int64_t groups = (e.vocab + kZeroRows - 1) / kZeroRows;
         const int64_t worker = w / groups;
-        zero_rows<GB>(e, keys + worker * e.tokens, worker, (w % groups) * kWave, lane);
+        zero_rows<GB>(e, keys + worker * e.tokens, worker, (w % groups) * kZeroRows, lane);
         return;
     }
     const int blocks = (int)((e.cols + kEmbedCols - 1) / kEmbedCols);
@@ -252,57 +283,57 @@ __global__ __launch_bounds__(256) void embed_sums_kernel(EmbedGrad e, const uint
     keys += worker * e.tokens;
     const int64_t begin = (int64_t)seg * e.seg;
     const int64_t end = begin + e.seg < e.tokens ? begin + e.seg : e.tokens;
-    const uint32_t before = begin > 0 ? (uint32_t)(keys[begin - 1] >> 32) : (uint32_t)e.vocab;
-    const uint32_t after = end < e.tokens ? (uint32_t)(keys[end] >> 32) : (uint32_t)e.vocab;
-    uint32_t cur = (uint32_t)e.vocab;  // the row being summed
-    bool first = true;                 // cur is the segment's first row
-    float sum[4] = {};
+    const uint32_t none = (uint32_t)e.vocab;  // padding: sorted behind every row
+    const uint32_t before = begin > 0 ? (uint32_t)(keys[begin - 1] >> 32) : none;
     const int64_t base = worker * e.tokens;
+    uint32_t cur = none;  // a row that goes on
+    bool first = true;    // none has ended in this segment
+    float sum[4] = {};
     for (int64_t g = begin; g < end; g += kWave) {
         const int have = (int)(end - g < kWave ? end - g : kWave);
-        const uint64_t key = lane < have ? keys[g + lane] : (uint64_t)e.vocab << 32;
+        const uint64_t key = lane < have ? keys[g + lane] : (uint64_t)none << 32;
         const uint32_t key_id = (uint32_t)(key >> 32), key_at = (uint32_t)key;
-        for (int i0 = 0; i0 < have; i0 += 8) {
-            float v[8][4];
+        // the next token's id: a row ends where it differs
+        const uint32_t key_next = lane < have && g + lane + 1 < e.tokens ? (uint32_t)(keys[g + lane + 1] >> 32) : none;
+        for (int i0 = 0; i0 < have; i0 += kInFlight) {
+            Raw<DB, 4> v[kInFlight];
+            Raw<GB, 4> old[ADD ? kInFlight : 1];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {  // eight rows in flight
-                const uint32_t t = __builtin_amdgcn_readlane(key_at, i0 + i);
-                const bool there = i0 + i < have && __builtin_amdgcn_readlane(key_id, i0 + i) < (uint32_t)e.vocab;
-                load_n<DB>(e.dy, (base + (there ? t : 0)) * e.cols + c, there ? n : 0, v[i]);
+            for (int i = 0; i < kInFlight; ++i) {
+                const uint32_t id = __builtin_amdgcn_readlane(key_id, i0 + i);
+                const uint32_t t = id == none ? 0 : __builtin_amdgcn_readlane(key_at, i0 + i);
+                v[i] = load_raw<DB, 4>(e.dy, (base + t) * e.cols, c, e.cols);
+                if constexpr (ADD)
+                    old[i] = load_raw<GB, 4>(e.grad, (worker * e.vocab + (id == none ? 0 : id)) * e.cols, c, e.cols);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t id = i0 + i < have ? __builtin_amdgcn_readlane(key_id, i0 + i) : (uint32_t)e.vocab;
-                if (id == (uint32_t)e.vocab) continue;  // padding is sorted behind every row
-                if (id != cur) {
-                    if (cur != (uint32_t)e.vocab) {
-                        if (first && cur == before)
-                            write_partial(e, worker, seg, 0, c, n, sum);
-                        else
-                            write_row<GB>(e, worker, cur, c, n, sum);
-                        first = false;
-                    }
-                    cur = id;
+            for (int i = 0; i < kInFlight; ++i) {
+                const uint32_t id = __builtin_amdgcn_readlane(key_id, i0 + i);
+                if (id == none) continue;
+                float x[4];
+                unpack(v[i], c, e.cols, x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum[j] += x[j];
+                cur = id;
+                if (id != __builtin_amdgcn_readlane(key_next, i0 + i)) {
+                    if (first && id == before)
+                        write_partial(e, worker, seg, 0, c, n, sum);
+                    else
+                        write_row<GB, ADD>(e, worker, id, c, n, sum, old[ADD ? i : 0]);
+                    first = false;
+                    cur = none;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) sum[j] = 0.0f;
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sum[j] += v[i][j];
             }
         }
     }
-    if (cur == (uint32_t)e.vocab) return;
-    if (first && cur == before)
-        write_partial(e, worker, seg, 0, c, n, sum);
-    else if (cur == after)
-        write_partial(e, worker, seg, 1, c, n, sum);
-    else
-        write_row<GB>(e, worker, cur, c, n, sum);
+    if (cur != none) write_partial(e, worker, seg, first && cur == before ? 0 : 1, c, n, sum);
 }
 
 // A row that begins in segment `seg` and goes on in the next ones: its last
 // partial there, then the first partials of the segments that it reaches.
-template <bool GB>
+template <bool GB, bool ADD>
 __global__ __launch_bounds__(256) void embed_join_kernel(EmbedGrad e, const uint64_t *keys, int64_t waves) {
     const int lane = threadIdx.x & (kWave - 1);
     const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -318,25 +349,46 @@ __global__ __launch_bounds__(256) void embed_join_kernel(EmbedGrad e, const uint
     // one that began in an earlier segment is joined there
     if (begin > 0 && (uint32_t)(keys[begin - 1] >> 32) == id) return;
     const int n = (int)(e.cols - c < 4 ? e.cols - c : 4);
-    if (n <= 0) return;
+    Raw<GB, 4> old;
+    if constexpr (ADD) old = load_raw<GB, 4>(e.grad, (worker * e.vocab + id) * e.cols, c, e.cols);
     // the last token of the row, and its segment
-    const int64_t stop = end + lower_bound(keys + end, e.tokens - end, (uint64_t)(id + 1) << 32);
+    const int64_t stop = end + wave_lower_bound(keys + end, e.tokens - end, (uint64_t)(id + 1) << 32, lane);
     const int last = (int)((stop - 1) / e.seg);
-    const int64_t at = (worker * e.segments + seg) * 2 * e.cols + c;
+    const int64_t at = (worker * e.segments + seg) * 2 * e.cols;
     float sum[4];
-    load_n<false>(e.partial, at + e.cols, n, sum);
-    for (int i = 1; i <= last - seg; i += 4) {
-        float v[4][4];
+    unpack(load_raw<false, 4>(e.partial, at + e.cols, c, e.cols), c, e.cols, sum);
+    for (int i = 1; i <= last - seg; i += 8) {
+        Raw<false, 4> v[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            load_n<false>(e.partial, at + (int64_t)(i + k <= last - seg ? i + k : i) * 2 * e.cols,
-                          i + k <= last - seg ? n : 0, v[k]);
+        for (int k = 0; k < 8; ++k)
+            v[k] = load_raw<false, 4>(e.partial, at + (int64_t)(i + k <= last - seg ? i + k : i) * 2 * e.cols, c, e.cols);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k) {
+            float x[4];
+            unpack(v[k], c, e.cols, x);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sum[j] += v[k][j];
+            for (int j = 0; j < 4; ++j) sum[j] += i + k <= last - seg ? x[j] : 0.0f;
+        }
     }
-    write_row<GB>(e, worker, id, c, n, sum);
+    write_row<GB, ADD>(e, worker, id, c, n, sum, old);
+}
+
+template <bool DB, bool GB>
+void launch_sums(const EmbedGrad &e, const uint64_t *keys, int64_t sums, int64_t waves, hipStream_t s) {
+    const dim3 grid((unsigned)((waves + 3) / 4));
+    if (e.accumulate)
+        embed_sums_kernel<DB, GB, true><<<grid, 256, 0, s>>>(e, keys, sums, waves);
+    else
+        embed_sums_kernel<DB, GB, false><<<grid, 256, 0, s>>>(e, keys, sums, waves);
+}
+
+template <bool GB>
+void launch_join(const EmbedGrad &e, const uint64_t *keys, int64_t waves, hipStream_t s) {
+    const dim3 grid((unsigned)((waves + 3) / 4));
+    if (e.accumulate)
+        embed_join_kernel<GB, true><<<grid, 256, 0, s>>>(e, keys, waves);
+    else
+        embed_join_kernel<GB, false><<<grid, 256, 0, s>>>(e, keys, waves);
 }
 
 int64_t sum_waves(const EmbedGrad &e) {
@@ -369,10 +421,10 @@ int embed_merge_passes(int64_t tokens) {
     return passes;
 }
 
-// At least 16 tokens a segment, and more where that gives over 16384 waves.
+// At least 32 tokens a segment, and more where that gives over 16384 waves.
 int32_t embed_segment(int32_t workers, int64_t tokens, int64_t cols) {
     const int64_t blocks = (cols + kEmbedCols - 1) / kEmbedCols;
-    int64_t seg = 16;
+    int64_t seg = 32;
     while (seg < tokens && workers * ((tokens + seg - 1) / seg) * blocks > 16384) seg *= 2;
     return (int32_t)seg;
 }
@@ -381,7 +433,14 @@ void launch_embedding_sort(const EmbedGrad &e, hipStream_t s) {
     const int chunks = (int)((e.tokens + kSortChunk - 1) / kSortChunk);
     int bits = 0;  // of the largest key, vocab (padding)
     while (bits < 32 && (e.vocab >> bits) != 0) ++bits;
-    embed_sort_kernel<<<dim3((unsigned)(e.workers * chunks)), kSortThreads, 0, s>>>(e, chunks, bits);
+    const int passes = (bits + 7) / 8, width = (bits + passes - 1) / passes;
+    const dim3 grid((unsigned)(e.workers * chunks));
+    if (e.tokens <= kSortThreads)
+        embed_sort_kernel<1><<<grid, kSortThreads, 0, s>>>(e, chunks, passes, width);
+    else if (e.tokens <= 2 * kSortThreads)
+        embed_sort_kernel<2><<<grid, kSortThreads, 0, s>>>(e, chunks, passes, width);
+    else
+        embed_sort_kernel<4><<<grid, kSortThreads, 0, s>>>(e, chunks, passes, width);
 }
 
 void launch_embedding_merge(const EmbedGrad &e, int pass, hipStream_t s) {
@@ -393,29 +452,20 @@ void launch_embedding_merge(const EmbedGrad &e, int pass, hipStream_t s) {
 void launch_embedding_sums(const EmbedGrad &e, hipStream_t s) {
     const uint64_t *keys = e.keys[embed_merge_passes(e.tokens) & 1];
     const int64_t sums = sum_waves(e);
-    const int64_t waves = sums + (e.accumulate ? 0 : e.workers * ((e.vocab + kWave - 1) / kWave));
-    const dim3 grid((unsigned)((waves + 3) / 4));
-    if (e.dy_bf16) {
-        if (e.grad_bf16)
-            embed_sums_kernel<true, true><<<grid, 256, 0, s>>>(e, keys, sums, waves);
-        else
-            embed_sums_kernel<true, false><<<grid, 256, 0, s>>>(e, keys, sums, waves);
-    } else {
-        if (e.grad_bf16)
-            embed_sums_kernel<false, true><<<grid, 256, 0, s>>>(e, keys, sums, waves);
-        else
-            embed_sums_kernel<false, false><<<grid, 256, 0, s>>>(e, keys, sums, waves);
-    }
+    const int64_t waves = sums + (e.accumulate ? 0 : e.workers * ((e.vocab + kZeroRows - 1) / kZeroRows));
+    if (e.dy_bf16)
+        e.grad_bf16 ? launch_sums<true, true>(e, keys, sums, waves, s) : launch_sums<true, false>(e, keys, sums, waves, s);
+    else
+        e.grad_bf16 ? launch_sums<false, true>(e, keys, sums, waves, s) : launch_sums<false, false>(e, keys, sums, waves, s);
 }
 
 void launch_embedding_join(const EmbedGrad &e, hipStream_t s) {
     const uint64_t *keys = e.keys[embed_merge_passes(e.tokens) & 1];
     const int64_t waves = sum_waves(e) / e.segments * (e.segments - 1);
-    const dim3 grid((unsigned)((waves + 3) / 4));
     if (e.grad_bf16)
-        embed_join_kernel<true><<<grid, 256, 0, s>>>(e, keys, waves);
+        launch_join<true>(e, keys, waves, s);
     else
-        embed_join_kernel<false><<<grid, 256, 0, s>>>(e, keys, waves);
+        launch_join<false>(e, keys, waves, s);
 }
 
 }  // namespace sm

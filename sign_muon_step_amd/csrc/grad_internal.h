@@ -226,4 +226,75 @@ __device__ __forceinline__ void store_n(void *p, int64_t i, int count, const flo
     }
 }
 
+// N values of a row from column c on, as they lie in memory. Columns past the
+// row's end are not there: the vector then starts at the row's last N values,
+// and unpack moves what exists to the front. So every lane loads in the same
+// instruction, whatever the width, and several loads can be under way before
+// the first is unpacked (a branch around each load, with the conversion inside,
+// waits for one after the other).
+template <bool BF16, int N>
+struct Raw {
+    uint32_t w[BF16 ? N / 2 : N];
+};
+
+template <bool BF16, int N>
+__device__ __forceinline__ Raw<BF16, N> load_raw(const void *p, int64_t row, int64_t c, int64_t cols) {
+    Raw<BF16, N> o;
+    if (cols >= N) {
+        const int64_t at = row + (c <= cols - N ? c : cols - N);
+        if constexpr (BF16 && N == 4) {
+            const u32x2 t = *reinterpret_cast<const u32x2_any *>(static_cast<const uint16_t *>(p) + at);
+            o.w[0] = t[0];
+            o.w[1] = t[1];
+        } else {
+            const char *q = static_cast<const char *>(p) + at * (BF16 ? 2 : 4);
+#pragma unroll
+            for (int h = 0; h < (BF16 ? N / 8 : N / 4); ++h) {
+                const u32x4 t = *reinterpret_cast<const u32x4_any *>(q + 16 * h);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o.w[4 * h + j] = t[j];
+            }
+        }
+    } else {
+        // shorter than a vector: value by value, the last one again behind the end
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int64_t at = row + (c + j < cols ? c + j : cols - 1);
+            if constexpr (BF16) {
+                const uint32_t h = static_cast<const uint16_t *>(p)[at];
+                o.w[j / 2] = j % 2 ? o.w[j / 2] | h << 16 : h;
+            } else {
+                o.w[j] = static_cast<const uint32_t *>(p)[at];
+            }
+        }
+    }
+    return o;
+}
+
+// The values, 0 past the row's end.
+template <bool BF16, int N>
+__device__ __forceinline__ void unpack(const Raw<BF16, N> &o, int64_t c, int64_t cols, float (&v)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        v[j] = BF16 ? __uint_as_float(j % 2 ? o.w[j / 2] & 0xffff0000u : o.w[j / 2] << 16)
+                    : __uint_as_float(o.w[BF16 ? 0 : j]);
+    if (cols % N == 0) {
+        const bool there = c < cols;
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = there ? v[j] : 0.0f;
+    } else if (cols >= N) {
+        const int64_t by = c - (cols - N);
+        const int d = by <= 0 ? 0 : by < N ? (int)by : N;
+#pragma unroll
+        for (int s = N; s >= 1; s >>= 1) {
+            const bool move = d & s;
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = move ? (j + s < N ? v[j + s < N ? j + s : 0] : 0.0f) : v[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = c + j < cols ? v[j] : 0.0f;
+    }
+}
+
 }  // namespace sm
