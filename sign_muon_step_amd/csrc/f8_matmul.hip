@@ -148,12 +148,6 @@ __device__ __forceinline__ uint32_t slice_at(int r, int c) {
     return (uint32_t)(r * kSliceBytes + ((c ^ ((r >> 1) & 7)) << 4));
 }
 
-// Blocks go to the 8 XCDs round-robin: each XCD gets a contiguous run of tiles.
-__device__ __forceinline__ int xcd_run(int b, int n) {
-    const int q = n >> 3, rem = n & 7, x = b & 7, p = b >> 3;
-    return x * q + (x < rem ? x : rem) + p;
-}
-
 // A tile of one batch entry and one part of k.
 struct Tile {
     int64_t row0, col0, batch;

@@ -139,6 +139,13 @@ typedef u32x2 u32x2_any __attribute__((aligned(2)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
+// Blocks go to the 8 XCDs round-robin: each XCD gets a contiguous run of n
+// pieces of work.
+__device__ __forceinline__ int xcd_run(int b, int n) {
+    const int q = n >> 3, rem = n & 7, x = b & 7, p = b >> 3;
+    return x * q + (x < rem ? x : rem) + p;
+}
+
 __device__ __forceinline__ float from_bf16(uint32_t h) { return __uint_as_float(h << 16); }
 
 // Two fp32 values rounded to nearest even, as bf16 pairs (one v_cvt_pk_bf16_f32).
@@ -238,16 +245,16 @@ struct Raw {
 };
 
 template <bool BF16, int N>
-__device__ __forceinline__ Raw<BF16, N> load_raw(const void *p, int64_t row, int64_t c, int64_t cols) {
+__device__ __forceinline__ Raw<BF16, N> load_raw(const void *p, int64_t row, int c, int cols) {
     Raw<BF16, N> o;
+    const char *base = static_cast<const char *>(p) + row * (BF16 ? 2 : 4);
     if (cols >= N) {
-        const int64_t at = row + (c <= cols - N ? c : cols - N);
+        const char *q = base + (uint32_t)(c <= cols - N ? c : cols - N) * (BF16 ? 2u : 4u);
         if constexpr (BF16 && N == 4) {
-            const u32x2 t = *reinterpret_cast<const u32x2_any *>(static_cast<const uint16_t *>(p) + at);
+            const u32x2 t = *reinterpret_cast<const u32x2_any *>(q);
             o.w[0] = t[0];
             o.w[1] = t[1];
         } else {
-            const char *q = static_cast<const char *>(p) + at * (BF16 ? 2 : 4);
 #pragma unroll
             for (int h = 0; h < (BF16 ? N / 8 : N / 4); ++h) {
                 const u32x4 t = *reinterpret_cast<const u32x4_any *>(q + 16 * h);
@@ -259,32 +266,32 @@ __device__ __forceinline__ Raw<BF16, N> load_raw(const void *p, int64_t row, int
         // shorter than a vector: value by value, the last one again behind the end
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int64_t at = row + (c + j < cols ? c + j : cols - 1);
+            const int at = c + j < cols ? c + j : cols - 1;
             if constexpr (BF16) {
-                const uint32_t h = static_cast<const uint16_t *>(p)[at];
+                const uint32_t h = reinterpret_cast<const uint16_t *>(base)[at];
                 o.w[j / 2] = j % 2 ? o.w[j / 2] | h << 16 : h;
             } else {
-                o.w[j] = static_cast<const uint32_t *>(p)[at];
+                o.w[j] = reinterpret_cast<const uint32_t *>(base)[at];
             }
         }
     }
     return o;
 }
 
-// The values, 0 past the row's end.
+// The values, 0 past the row's end. whole: every lane's are there.
 template <bool BF16, int N>
-__device__ __forceinline__ void unpack(const Raw<BF16, N> &o, int64_t c, int64_t cols, float (&v)[N]) {
+__device__ __forceinline__ void unpack(const Raw<BF16, N> &o, int c, int cols, float (&v)[N], bool whole = false) {
 #pragma unroll
     for (int j = 0; j < N; ++j)
         v[j] = BF16 ? __uint_as_float(j % 2 ? o.w[j / 2] & 0xffff0000u : o.w[j / 2] << 16)
                     : __uint_as_float(o.w[BF16 ? 0 : j]);
+    if (whole) return;
     if (cols % N == 0) {
         const bool there = c < cols;
 #pragma unroll
         for (int j = 0; j < N; ++j) v[j] = there ? v[j] : 0.0f;
     } else if (cols >= N) {
-        const int64_t by = c - (cols - N);
-        const int d = by <= 0 ? 0 : by < N ? (int)by : N;
+        const int by = c - (cols - N), d = by <= 0 ? 0 : by < N ? by : N;
 #pragma unroll
         for (int s = N; s >= 1; s >>= 1) {
             const bool move = d & s;
