@@ -7,9 +7,12 @@
 // Both passes are bound by memory: the forward reads x and writes y, the
 // backward reads x and dy and writes dx. Each row is read once and held in
 // registers by a team of lanes (8 values a lane and chunk): 8 to 64 lanes of a
-// wave for up to 2048 columns, a workgroup of 256, 512 or 1024 for up to
-// 16384; longer rows are read again from the caches. The variance is summed
-// from the differences to the mean.
+// wave for up to 1024 columns, a workgroup of 128 to 512 for up to 8192; longer
+// rows are read again from the caches. The variance is summed from the differences
+// to the mean. Backward, BF16 with F32 sums: 16384 x 4096 85 us (4.7 TB/s of the
+// least traffic, the rate of a large copy), 1 worker x 8192 x 1024 17 us, 8 workers
+// x 1024 x 768 13.1 us, of which about 5 us are the launch of the second kernel and
+// its pass over the partial rows.
 //
 // The weight's gradients are sums down the columns, over rows that many teams
 // hold. A lane keeps the same columns for every row of its team and adds them
@@ -60,8 +63,8 @@ struct Team {
     }
 };
 
-__device__ __forceinline__ int left(int64_t cols, int64_t c) {  // values of a chunk at column c
-    return (int)(cols - c < 0 ? 0 : cols - c < 8 ? cols - c : 8);
+__device__ __forceinline__ int left(int cols, int c) {  // values of a chunk at column c
+    return cols - c < 0 ? 0 : cols - c < 8 ? cols - c : 8;
 }
 
 // One team per row, `teams` of the grid taking every teams-th row.
@@ -69,33 +72,33 @@ template <bool BF16, int TS, int NIT, int THREADS>
 __global__ __launch_bounds__(THREADS) void norm_kernel(Norm n) {
     __shared__ float lds[TS > kWave ? 4 * TS / kWave : 1];
     Team<TS> team{lds};
-    const int tl = threadIdx.x % TS;
+    const int tl = threadIdx.x % TS, cols = (int)n.cols;
     const int64_t teams = (int64_t)gridDim.x * (THREADS / TS);
     const float inv = 1.0f / (float)n.cols;
     float g[NIT][8], b[NIT][8];
 #pragma unroll
     for (int i = 0; i < NIT; ++i) {
-        const int64_t c = (int64_t)(i * TS + tl) * 8;
-        load_n<false>(n.gamma, c, left(n.cols, c), g[i]);
-        load_n<false>(n.beta, c, n.beta ? left(n.cols, c) : 0, b[i]);
+        const int c = (i * TS + tl) * 8;
+        load_n<false>(n.gamma, c, left(cols, c), g[i]);
+        load_n<false>(n.beta, c, n.beta ? left(cols, c) : 0, b[i]);
     }
     for (int64_t row = (int64_t)blockIdx.x * (THREADS / TS) + threadIdx.x / TS; row < n.rows; row += teams) {
+        Raw<BF16, 8> raw[NIT];
         float v[NIT][8];
         float total = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NIT; ++i) {
-            const int64_t c = (int64_t)(i * TS + tl) * 8;
-            load_n<BF16>(n.x, row * n.cols + c, left(n.cols, c), v[i]);
-        }
+        for (int i = 0; i < NIT; ++i) raw[i] = load_raw<BF16, 8>(n.x, row * n.cols, (i * TS + tl) * 8, cols);
 #pragma unroll
-        for (int i = 0; i < NIT; ++i)
+        for (int i = 0; i < NIT; ++i) {
+            unpack(raw[i], (i * TS + tl) * 8, cols, v[i], (i + 1) * TS * 8 <= cols);
 #pragma unroll
             for (int j = 0; j < 8; ++j) total += v[i][j];
+        }
         const float mean = team.sum(total) * inv;
         float square = 0.0f;
 #pragma unroll
         for (int i = 0; i < NIT; ++i) {
-            const int have = left(n.cols, (int64_t)(i * TS + tl) * 8);
+            const int have = left(cols, (i * TS + tl) * 8);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[i][j] -= mean;
@@ -105,10 +108,10 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(Norm n) {
         const float rstd = 1.0f / sqrtf(team.sum(square) * inv + n.eps);
 #pragma unroll
         for (int i = 0; i < NIT; ++i) {
-            const int64_t c = (int64_t)(i * TS + tl) * 8;
+            const int c = (i * TS + tl) * 8;
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = fmaf(v[i][j] * rstd, g[i][j], b[i][j]);
-            store_n<BF16>(n.y, row * n.cols + c, left(n.cols, c), v[i]);
+            store_n<BF16>(n.y, row * n.cols + c, left(cols, c), v[i]);
         }
         if (tl == 0) {
             if (n.mean) n.mean[row] = mean;
@@ -186,7 +189,7 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGrad n) {
     __shared__ float sums[kTeams > 1 ? kTeams * NIT * TS * 8 : 1];
     __shared__ float lds[TS > kWave ? 4 * TS / kWave : 1];
     Team<TS> team{lds};
-    const int tl = threadIdx.x % TS, tm = threadIdx.x / TS;
+    const int tl = threadIdx.x % TS, tm = threadIdx.x / TS, cols = (int)n.cols;
     const int64_t worker = blockIdx.x / n.parts, part = blockIdx.x % n.parts;
     const int64_t begin = part * rows_per_part(n);
     const int64_t end = begin + rows_per_part(n) < n.rows ? begin + rows_per_part(n) : n.rows;
@@ -194,23 +197,42 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGrad n) {
     float g[NIT][8], dg[NIT][8] = {}, db[NIT][8] = {};
 #pragma unroll
     for (int i = 0; i < NIT; ++i) {
-        const int64_t c = (int64_t)(i * TS + tl) * 8;
-        load_n<false>(n.gamma, c, left(n.cols, c), g[i]);
+        const int c = (i * TS + tl) * 8;
+        load_n<false>(n.gamma, c, left(cols, c), g[i]);
     }
+    Raw<BF16, 8> rx[NIT], rd[NIT];
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    auto fetch = [&](int64_t r) {
+        const int64_t row = worker * n.rows + r;
+#pragma unroll
+        for (int i = 0; i < NIT; ++i) {
+            const int c = (i * TS + tl) * 8;
+            rx[i] = load_raw<BF16, 8>(n.x, row * n.cols, c, cols);
+            rd[i] = load_raw<BF16, 8>(n.dy, row * n.cols, c, cols);
+        }
+        next_mean = n.mean[row];
+        next_rstd = n.rstd[row];
+    };
+    // a wave with up to 1024 columns has room for the next row while it works on
+    // one; for more columns other waves fill the wait
+    constexpr bool kAhead = TS <= kWave && NIT <= 2;
+    if (kAhead && begin + tm < end) fetch(begin + tm);
     for (int64_t r = begin + tm; r < end; r += kTeams) {
         const int64_t row = worker * n.rows + r;
-        const float mean = n.mean[row], rstd = n.rstd[row];
+        if (!kAhead) fetch(r);
         float x[NIT][8], d[NIT][8];
 #pragma unroll
         for (int i = 0; i < NIT; ++i) {
-            const int64_t c = (int64_t)(i * TS + tl) * 8;
-            load_n<BF16>(n.x, row * n.cols + c, left(n.cols, c), x[i]);
-            load_n<BF16>(n.dy, row * n.cols + c, left(n.cols, c), d[i]);
+            const int c = (i * TS + tl) * 8;
+            unpack(rx[i], c, cols, x[i], (i + 1) * TS * 8 <= cols);
+            unpack(rd[i], c, cols, d[i], (i + 1) * TS * 8 <= cols);
         }
+        const float mean = next_mean, rstd = next_rstd;
+        if (kAhead && r + kTeams < end) fetch(r + kTeams);
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < NIT; ++i) {
-            const int have = left(n.cols, (int64_t)(i * TS + tl) * 8);
+            const int have = left(cols, (i * TS + tl) * 8);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float xh = j < have ? (x[i][j] - mean) * rstd : 0.0f;
@@ -228,10 +250,10 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGrad n) {
         s2 *= inv;
 #pragma unroll
         for (int i = 0; i < NIT; ++i) {
-            const int64_t c = (int64_t)(i * TS + tl) * 8;
+            const int c = (i * TS + tl) * 8;
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[i][j] = rstd * (d[i][j] - s1 - x[i][j] * s2);
-            store_n<BF16>(n.dx, row * n.cols + c, left(n.cols, c), x[i]);
+            store_n<BF16>(n.dx, row * n.cols + c, left(cols, c), x[i]);
         }
     }
 #pragma unroll
@@ -240,8 +262,8 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGrad n) {
         if constexpr (kTeams == 1) {
 #pragma unroll
             for (int i = 0; i < NIT; ++i) {
-                const int64_t c = (int64_t)(i * TS + tl) * 8;
-                write_sum(n, worker, part, which, c, left(n.cols, c), which ? db[i] : dg[i]);
+                const int c = (i * TS + tl) * 8;
+                write_sum(n, worker, part, which, c, left(cols, c), which ? db[i] : dg[i]);
             }
         } else {
             __syncthreads();
@@ -325,11 +347,11 @@ __global__ __launch_bounds__(64) void norm_grad_columns_kernel(NormGrad n, int b
     if (n.dbeta) write_sum(n, worker, part, 1, c, have, db);
 }
 
-// 64 columns of one sum of one worker: four waves add a quarter of the parts
-// each, in order, and the first adds the four.
+// 64 columns of one sum of one worker: eight waves add an eighth of the parts
+// each, in order, and the first adds the eight.
 template <bool GB>
-__global__ __launch_bounds__(256) void norm_sums_kernel(NormGrad n, int blocks) {
-    __shared__ float lds[4][kWave];
+__global__ __launch_bounds__(512) void norm_sums_kernel(NormGrad n, int blocks) {
+    __shared__ float lds[8][kWave];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int64_t c = (int64_t)(blockIdx.x % blocks) * kWave + lane;
     const int which = blockIdx.x / blocks & 1;
@@ -338,22 +360,26 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(NormGrad n, int blocks) 
     if (!out) return;
     float total = 0.0f;
     if (c < n.cols) {
-        const int quarter = (n.parts + 3) / 4;
-        const int end = (wave + 1) * quarter < n.parts ? (wave + 1) * quarter : n.parts;
+        const int each = (n.parts + 7) / 8;
+        const int end = (wave + 1) * each < n.parts ? (wave + 1) * each : n.parts;
         const float *p = n.partial + (worker * n.parts * 2 + which) * n.cols + c;
 #pragma unroll 8
-        for (int i = wave * quarter; i < end; ++i) total += p[(int64_t)i * 2 * n.cols];
+        for (int i = wave * each; i < end; ++i) total += p[(int64_t)i * 2 * n.cols];
     }
     lds[wave][lane] = total;
     __syncthreads();
     if (wave == 0 && c < n.cols)
-        store1<GB>(out, worker * n.cols + c, (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]));
+        store1<GB>(out, worker * n.cols + c,
+                   ((lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane])) +
+                       ((lds[4][lane] + lds[5][lane]) + (lds[6][lane] + lds[7][lane])));
 }
 
-// A team's lanes, chunks a lane, and a workgroup's threads.
+// A team's lanes, chunks a lane, and a workgroup's threads (those of one team
+// where it is more than a wave: its sums meet at barriers).
 template <int TS_, int NIT_, int THREADS_>
 struct Width {
     static constexpr int TS = TS_, NIT = NIT_, THREADS = THREADS_;
+    static_assert(TS <= kWave || THREADS == TS, "teams of a workgroup do not meet");
 };
 
 // f(Width) for a row of `cols` values.
@@ -369,25 +395,16 @@ void by_width(int64_t cols, F &&f) {
         f(Width<64, 1, 256>{});
     else if (cols <= 1024)
         f(Width<64, 2, 256>{});
-    else if (cols <= 1536)
-        f(Width<64, 3, 256>{});
     else if (cols <= 2048)
-        f(Width<64, 4, 256>{});
+        f(Width<128, 2, 128>{});
     else if (cols <= 4096)
         f(Width<256, 2, 256>{});
-    else if (cols <= 8192)
-        f(Width<512, 2, 512>{});
     else
-        f(Width<1024, 2, 1024>{});
+        f(Width<512, 2, 512>{});
 }
-constexpr int64_t kLongRow = 16384;  // columns that a workgroup's registers hold
-
-int teams_of(int64_t cols) {
-    int teams = 1;
-    auto f = [&](auto w) { teams = w.THREADS / w.TS; };
-    by_width(cols, f);
-    return teams;
-}
+// Columns that a workgroup's registers hold without spilling in the backward pass:
+// with four chunks a lane, 700 x 12000 takes 109 us there and 43 us reading twice.
+constexpr int64_t kLongRow = 8192;
 
 }  // namespace
 
@@ -412,11 +429,23 @@ void launch_layer_norm(const Norm &n, hipStream_t s) {
     by_width(n.cols, f);
 }
 
+// Two rows a team at least, and at most 4096 waves in all (4 on each SIMD), or 2048
+// where a lane holds two chunks and its registers leave room for half as many: all
+// the waves run at once, and there are fewer partial sums to join. 8 workers x 1024 x
+// 768 16.2 -> 13.8 us with 2048, 8 x 4096 x 300 22.6 -> 26.3 us.
 int32_t norm_parts(int32_t workers, int64_t rows, int64_t cols) {
-    const int64_t teams = cols > kLongRow ? 8 : teams_of(cols);
-    const int64_t most = 1024 / workers > 1 ? 1024 / workers : 1;
+    int64_t teams = 8, waves = 4, most = 4096;
+    if (cols <= kLongRow) {
+        auto f = [&](auto w) {
+            teams = w.THREADS / w.TS;
+            waves = w.THREADS / kWave;
+            most = w.NIT > 1 ? 2048 : 4096;
+        };
+        by_width(cols, f);
+    }
+    const int64_t each = most / waves / workers > 1 ? most / waves / workers : 1;
     const int64_t parts = (rows + teams * 2 - 1) / (teams * 2);
-    return (int32_t)(parts < most ? parts : most);
+    return (int32_t)(parts < each ? parts : each);
 }
 
 void launch_layer_norm_backward(const NormGrad &n, hipStream_t s) {
@@ -449,9 +478,9 @@ void launch_layer_norm_sums(const NormGrad &n, hipStream_t s) {
     const int blocks = (int)((n.cols + kWave - 1) / kWave);
     const dim3 grid((unsigned)(n.workers * 2 * blocks));
     if (n.grad_bf16)
-        norm_sums_kernel<true><<<grid, 256, 0, s>>>(n, blocks);
+        norm_sums_kernel<true><<<grid, 512, 0, s>>>(n, blocks);
     else
-        norm_sums_kernel<false><<<grid, 256, 0, s>>>(n, blocks);
+        norm_sums_kernel<false><<<grid, 512, 0, s>>>(n, blocks);
 }
 
 }  // namespace sm
