@@ -313,3 +313,26 @@ def test_replays_and_streams_give_the_same_bits():
     torch.cuda.synchronize()
     for a, b in zip(outputs, want):
         assert same_bits(a, b)
+
+
+@pytest.mark.parametrize("m,n", [(3, 20), (40, 64), (300, 260)])
+@pytest.mark.parametrize("fmt", [E4, E5])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_the_smallest_and_largest_scales(m, n, fmt, out_dtype):
+    """Blocks of scale byte 0 (2^-127) times blocks of large scales. A block's values
+    lie within a factor of 2, so no 8-bit value is subnormal, and none stands for
+    less than 2^-126."""
+    k = 300
+    g = gen(41)
+    tiny = (1 + torch.rand(m, k, generator=g)) * 2.0 ** (-122 if fmt == E4 else -115) * 2.0 ** (-(torch.arange(m) % 3))[:, None]
+    large = torch.randn(n, k, generator=g).sign() * (1 + torch.rand(n, k, generator=g)) * 2.0 ** 100
+    pairs = []
+    for x in (tiny, large):
+        q, s = quantised(x, fmt)
+        blocks = torch.exp2(s[:, :q.shape[-1] // 128].double() - 127)
+        pairs.append((q, s, (q.double().unflatten(-1, (-1, 128)) * blocks.unsqueeze(-1)).flatten(-2), blocks))
+    a, b = pairs
+    assert int(a[1][:, :3].max()) == 0 and float(a[2][:, :k].abs().min()) >= 2.0 ** -126
+    want, tol = a[2] @ b[2].t(), tolerance(out_dtype, a, b, fmt, fmt)
+    check_product(multiply(a, b, k, (m, n), out_dtype), want, tol)
+    check_product(multiply(b, a, k, (n, m), out_dtype), want.t(), tol.t())
