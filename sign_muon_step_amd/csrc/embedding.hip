@@ -22,7 +22,7 @@
 //                       that no token has.
 //   embed_join_kernel   adds the partial sums of each row, in their order
 //
-// 8 workers x 4096 tokens, 32000 x 768, F32 from BF16: 160 us, of which 119 us are
+// 8 workers x 4096 tokens, 32000 x 768, F32 from BF16: 155 us, of which 119 us are
 // what the stack's zeros alone take to store; 3 x 1501 tokens, 5003 x 515: 22 us,
 // three launches that wait for one another.
 #include "grad_internal.h"
@@ -72,11 +72,37 @@ constexpr int kSortWaves = kSortThreads / kWave;
 // waves + those of earlier rounds of its wave + those of lower lanes of its
 // round. Latency counts here (a workgroup for each worker's 4096 tokens), so a
 // digit's counts of the sixteen waves are read at once and added in registers.
+// Workgroups behind the sorting ones write zeros to each worker's rows from
+// `beside` on, before embed_sums_kernel writes those of them that have tokens: the
+// sort keeps few compute units busy, and memory not at all. 8 workers x 4096
+// tokens, 32000 x 768, F32: 165 us without, 162 us with 48 MB of zeros here, 156 us
+// with 96 MB, 157 to 158 us with more, up to all of them (which would write every
+// row twice where each has a token).
+constexpr int kZeroPiece = 32768;  // bytes of a workgroup
+constexpr int64_t kZeroBeside = (int64_t)96 << 20;  // bytes of all of them
+
 template <int R>
-__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedGrad e, int chunks, int passes, int width) {
+__global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(EmbedGrad e, int chunks, int passes, int width,
+                                                                 int64_t beside, int pieces) {
     __shared__ uint64_t keys[kSortThreads * R];
     __shared__ uint32_t count[kSortWaves][256];
     __shared__ uint32_t wave_total[4];
+    const int sorting = e.workers * chunks;
+    if ((int)blockIdx.x >= sorting) {
+        const int b = xcd_run(blockIdx.x - sorting, gridDim.x - sorting);
+        const int64_t size = e.grad_bf16 ? 2 : 4, from = (int64_t)(b % pieces) * kZeroPiece;
+        const int64_t left = (e.vocab - beside) * e.cols * size - from;
+        char *p = static_cast<char *>(e.grad) + ((b / pieces + 1) * e.vocab * e.cols * size - left);
+        const int bytes = (int)(left < kZeroPiece ? left : kZeroPiece);
+#pragma unroll
+        for (int i = threadIdx.x * 16; i < kZeroPiece; i += kSortThreads * 16) {
+            if (i + 16 <= bytes)
+                *reinterpret_cast<u32x4_any *>(p + i) = u32x4{0, 0, 0, 0};
+            else
+                for (int j = i; j < bytes; j += 2) *reinterpret_cast<uint16_t *>(p + j) = 0;
+        }
+        return;
+    }
     const int worker = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
     const int64_t first = (int64_t)chunk * kSortChunk;
     const int n = (int)(e.tokens - first < kSortChunk ? e.tokens - first : kSortChunk);
@@ -240,12 +266,12 @@ __device__ __forceinline__ void write_partial(const EmbedGrad &e, int64_t worker
 constexpr int kMaxZeroRows = 32;
 constexpr int64_t kZeroBytes = 12288;
 template <bool GB>
-__device__ void zero_rows(const EmbedGrad &e, const uint64_t *keys, int64_t worker, int64_t v0, int rows) {
+__device__ void zero_rows(const EmbedGrad &e, const uint64_t *keys, int64_t worker, int64_t v0, int rows, int64_t most) {
     const int lane = threadIdx.x & (kWave - 1);
     // the ids that there are (each wave for itself): from the keys behind the
     // first of them, and again behind the last one seen where 64 keys do not
     // reach past the group
-    const int64_t v1 = v0 + rows < e.vocab ? v0 + rows : e.vocab;
+    const int64_t v1 = v0 + rows < most ? v0 + rows : most;
     uint32_t mask = ~0u >> (kMaxZeroRows - (int)(v1 - v0));
     for (int64_t v = v0; v < v1;) {
         const int64_t at = wave_lower_bound(keys, e.tokens, (uint64_t)v << 32, lane) + lane;
@@ -273,13 +299,13 @@ constexpr int kInFlight = 16;  // rows that a wave has under way
 
 template <bool DB, bool GB, bool ADD>
 __global__ __launch_bounds__(256) void embed_sums_kernel(EmbedGrad e, const uint64_t *keys, int64_t sum_waves,
-                                                         int sum_blocks, int zero_rows_each) {
+                                                         int sum_blocks, int zero_rows_each, int64_t beside) {
     const int lane = threadIdx.x & (kWave - 1);
-    if ((int)blockIdx.x >= sum_blocks) {  // rows that no token has
+    if ((int)blockIdx.x >= sum_blocks) {  // rows below `beside` that no token has
         const int b = xcd_run(blockIdx.x - sum_blocks, gridDim.x - sum_blocks);
-        const int groups = (int)((e.vocab + zero_rows_each - 1) / zero_rows_each);
+        const int groups = (int)((beside + zero_rows_each - 1) / zero_rows_each);
         const int64_t worker = b / groups;
-        zero_rows<GB>(e, keys + worker * e.tokens, worker, (int64_t)(b % groups) * zero_rows_each, zero_rows_each);
+        zero_rows<GB>(e, keys + worker * e.tokens, worker, (int64_t)(b % groups) * zero_rows_each, zero_rows_each, beside);
         return;
     }
     const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -383,6 +409,12 @@ __global__ __launch_bounds__(256) void embed_join_kernel(EmbedGrad e, const uint
     write_row<GB, ADD>(e, worker, id, c, n, sum, old);
 }
 
+// The first of the rows that get their zeros beside the sort.
+int64_t first_beside(const EmbedGrad &e) {
+    const int64_t rows = kZeroBeside / (e.workers * e.cols * (e.grad_bf16 ? 2 : 4));
+    return e.accumulate || rows <= 0 ? e.vocab : rows < e.vocab ? e.vocab - rows : 0;
+}
+
 template <bool DB, bool GB>
 void launch_sums(const EmbedGrad &e, const uint64_t *keys, int64_t waves, hipStream_t s) {
     const int blocks = (int)((waves + 31) / 32 * 8);  // a multiple of the XCDs
@@ -391,12 +423,12 @@ void launch_sums(const EmbedGrad &e, const uint64_t *keys, int64_t waves, hipStr
     int64_t rows = kZeroBytes / bytes, least = (e.workers * e.vocab + (1 << 23) - 1) >> 23;
     rows = rows < least ? least : rows;
     rows = rows < 1 ? 1 : rows > kMaxZeroRows ? kMaxZeroRows : rows;
-    const int64_t zeros = e.accumulate ? 0 : e.workers * ((e.vocab + rows - 1) / rows);
+    const int64_t beside = first_beside(e), zeros = e.accumulate ? 0 : e.workers * ((beside + rows - 1) / rows);
     const dim3 grid((unsigned)(blocks + zeros));
     if (e.accumulate)
-        embed_sums_kernel<DB, GB, true><<<grid, 256, 0, s>>>(e, keys, waves, blocks, (int)rows);
+        embed_sums_kernel<DB, GB, true><<<grid, 256, 0, s>>>(e, keys, waves, blocks, (int)rows, beside);
     else
-        embed_sums_kernel<DB, GB, false><<<grid, 256, 0, s>>>(e, keys, waves, blocks, (int)rows);
+        embed_sums_kernel<DB, GB, false><<<grid, 256, 0, s>>>(e, keys, waves, blocks, (int)rows, beside);
 }
 
 template <bool GB>
@@ -451,13 +483,15 @@ void launch_embedding_sort(const EmbedGrad &e, hipStream_t s) {
     int bits = 0;  // of the largest key, vocab (padding)
     while (bits < 32 && (e.vocab >> bits) != 0) ++bits;
     const int passes = (bits + 7) / 8, width = (bits + passes - 1) / passes;
-    const dim3 grid((unsigned)(e.workers * chunks));
+    const int64_t beside = first_beside(e), bytes = (e.vocab - beside) * e.cols * (e.grad_bf16 ? 2 : 4);
+    const int pieces = (int)((bytes + kZeroPiece - 1) / kZeroPiece);
+    const dim3 grid((unsigned)(e.workers * (chunks + pieces)));
     if (e.tokens <= kSortThreads)
-        embed_sort_kernel<1><<<grid, kSortThreads, 0, s>>>(e, chunks, passes, width);
+        embed_sort_kernel<1><<<grid, kSortThreads, 0, s>>>(e, chunks, passes, width, beside, pieces);
     else if (e.tokens <= 2 * kSortThreads)
-        embed_sort_kernel<2><<<grid, kSortThreads, 0, s>>>(e, chunks, passes, width);
+        embed_sort_kernel<2><<<grid, kSortThreads, 0, s>>>(e, chunks, passes, width, beside, pieces);
     else
-        embed_sort_kernel<4><<<grid, kSortThreads, 0, s>>>(e, chunks, passes, width);
+        embed_sort_kernel<4><<<grid, kSortThreads, 0, s>>>(e, chunks, passes, width, beside, pieces);
 }
 
 void launch_embedding_merge(const EmbedGrad &e, int pass, hipStream_t s) {
