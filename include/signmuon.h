@@ -318,7 +318,10 @@ size_t signmuon_workspace_bytes(const signmuon_matrix *mats, int32_t n_mats,
  * that may be replayed at once, take one each. Every result is the same on
  * every run: no sum depends on the order in which the hardware runs it.
  * Activations and weight gradients are F32 or BF16; sums and statistics are
- * fp32, and each result is rounded once to its storage type.
+ * fp32, and each result is rounded once to its storage type. Sizes below 1 are
+ * refused (SIGNMUON_EINVAL), and larger ones than the kernels index
+ * (SIGNMUON_ERANGE): 255 workers, 2^25 tokens or rows of all workers, 2^20
+ * columns, tables of 2^20 rows and 2^31 - 1 entries.
  * ---------------------------------------------------------------------- */
 
 /* Element type of token numbers. */
@@ -412,19 +415,24 @@ size_t signmuon_layer_norm_workspace_bytes(int32_t workers, int64_t rows, int64_
  * block (0 for a block with no finite nonzero value), the scale byte e + 127,
  * and q = x * 2^-e rounded to nearest even. NaN gives NaN; an infinity gives
  * NaN in E4M3 and itself in E5M2. Padding bytes of q and qt are written as
- * zeros, padding scale bytes as 127.
+ * zeros, padding scale bytes as 127. batch is at most 255, rows and cols 2^25.
  */
 int signmuon_f8_quant(const void *x, signmuon_dtype x_dtype, int32_t batch, int64_t rows,
                       int64_t cols, signmuon_f8 format, void *q, uint8_t *q_scale, void *qt,
                       uint8_t *qt_scale, signmuon_stream stream);
 
+/* Bytes of an operand's row and of its scales (0 unless 1 <= k <= 2^25). */
 size_t signmuon_f8_pitch(int64_t k);
 size_t signmuon_f8_scale_pitch(int64_t k);
 
 /*
  * signmuon_f8_matmul -- out[i][r][c] = sum over k of a[i][r][k] * b[i][c][k]
  * of the values that the operands stand for, accumulated in fp32 on the matrix
- * cores and rounded once to out_dtype. a is [batch][m] rows of k values, b
+ * cores and rounded once to out_dtype. For a BF16 out the matrix cores multiply
+ * the bytes themselves and cut the products of each 8 consecutive k below 2^-13
+ * of the largest one's power of two (1.4e-5 of a sum of random products); for an
+ * F32 out they multiply the bytes widened to BF16, at half the rate, and add as
+ * fp32 does (values below 2^-126 count as BF16 holds them). a is [batch][m] rows of k values, b
  * [batch][n] rows, or [n] rows shared by every i (b_shared = 1), both laid out
  * and padded as signmuon_f8_quant writes them (the bytes past k must be zero);
  * out is [batch][m][n]. For a linear layer y = x w^T with w [n][k]: the output
@@ -432,6 +440,7 @@ size_t signmuon_f8_scale_pitch(int64_t k);
  * weight's gradient of each worker dy and x by columns, batch = workers, which
  * fills signmuon_matrix.grad. workspace:
  * signmuon_f8_matmul_workspace_bytes(batch, m, n, k) bytes (may be 0, then NULL).
+ * batch is at most 255, m 2^25, n 2^21 and k 2^22.
  */
 int signmuon_f8_matmul(const void *a, const uint8_t *a_scale, signmuon_f8 a_format, const void *b,
                        const uint8_t *b_scale, signmuon_f8 b_format, int32_t batch, int64_t m,

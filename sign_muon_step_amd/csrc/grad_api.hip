@@ -232,9 +232,11 @@ int signmuon_layer_norm_backward(const void *dy, const void *x, signmuon_dtype x
     return sm::launch_status();
 }
 
-size_t signmuon_f8_pitch(int64_t k) { return k < 1 ? 0 : (size_t)sm::f8_pitch(k); }
+size_t signmuon_f8_pitch(int64_t k) { return k < 1 || k > kMaxTokens ? 0 : (size_t)sm::f8_pitch(k); }
 
-size_t signmuon_f8_scale_pitch(int64_t k) { return k < 1 ? 0 : (size_t)sm::f8_scale_pitch(k); }
+size_t signmuon_f8_scale_pitch(int64_t k) {
+    return k < 1 || k > kMaxTokens ? 0 : (size_t)sm::f8_scale_pitch(k);
+}
 
 int signmuon_f8_quant(const void *x, signmuon_dtype x_dtype, int32_t batch, int64_t rows,
                       int64_t cols, signmuon_f8 format, void *q, uint8_t *q_scale, void *qt,

@@ -336,3 +336,13 @@ def test_the_smallest_and_largest_scales(m, n, fmt, out_dtype):
     want, tol = a[2] @ b[2].t(), tolerance(out_dtype, a, b, fmt, fmt)
     check_product(multiply(a, b, k, (m, n), out_dtype), want, tol)
     check_product(multiply(b, a, k, (n, m), out_dtype), want.t(), tol.t())
+
+
+@pytest.mark.parametrize("batch,m,n,k", [(8, 16, 300, 4096), (3, 70, 128, 8192), (200, 1, 64, 2048), (2, 64, 64, 4096)])
+def test_a_shared_operand_in_the_workspace_of_its_batch(batch, m, n, k):
+    """The rows of a batch with one b may run as one product, which may want another
+    workspace: the one of the batch, between guard bytes, has to do."""
+    a, b = operand(m, k, E4, 1, (batch,)), operand(n, k, E5, 2)
+    b3 = tuple(t.expand((batch,) + t.shape) for t in b)
+    got = multiply(a, b, k, (batch, m, n), torch.float32)
+    check_product(got, a[2] @ b[2].t(), tolerance(torch.float32, a, b3, E4, E5))

@@ -186,11 +186,11 @@ def test_f8_matmul_arguments(lib):
         assert calls_with(lib.signmuon_f8_matmul, names, good, **change) == status, change
 
 
-def test_a_shared_operand_needs_no_more_workspace_than_asked():
-    """The rows of a batch with one b may run as one product, but only where the
-    workspace that was asked for the batch is enough."""
-    for batch, m, n, k in [(8, 16, 300, 4096), (3, 70, 128, 8192), (200, 1, 64, 2048), (2, 64, 64, 4096)]:
-        assert sm.signmuon_f8_matmul_workspace_bytes(batch, m, n, k) >= 0
+def test_workspace_of_a_batch_and_of_its_rows_as_one_product():
+    """Few rows each need none; as one product they would be summed in parts."""
+    size = sm.signmuon_f8_matmul_workspace_bytes
+    assert size(8, 16, 300, 4096) == 0 < size(1, 8 * 16, 300, 4096)
+    assert size(1, 8 * 16, 300, 4096) % (8 * 16 * 300 * 4) == 0
 
 
 def test_f8_binding_refuses_other_tensors():
@@ -222,3 +222,9 @@ def test_f8_binding_refuses_other_tensors():
         sm.signmuon_f8_matmul(q, s.float(), q, s, 20, out, None)
     with pytest.raises(ValueError, match="GPU memory"):
         sm.signmuon_f8_matmul(q, s, q, s, 20, out, None)
+
+
+def test_f8_row_sizes_of_lengths_that_no_operand_has():
+    for k in (0, -1, (1 << 25) + 1, (1 << 63) - 1, -(1 << 63)):
+        assert sm.signmuon_f8_pitch(k) == sm.signmuon_f8_scale_pitch(k) == 0
+    assert sm.signmuon_f8_pitch(1 << 25) == 1 << 25 and sm.signmuon_f8_scale_pitch(1 << 25) == 1 << 18
