@@ -22,8 +22,8 @@
 //                       that no token has.
 //   embed_join_kernel   adds the partial sums of each row, in their order
 //
-// 8 workers x 4096 tokens, 32000 x 768, F32 from BF16: 155 us, of which 119 us are
-// what the stack's zeros alone take to store; 3 x 1501 tokens, 5003 x 515: 22 us,
+// 8 workers x 4096 tokens, 32000 x 768, F32 from BF16: 153 us, of which 119 us are
+// what the stack's zeros alone take to store; 3 x 1501 tokens, 5003 x 515: 20 us,
 // three launches that wait for one another.
 #include "grad_internal.h"
 
@@ -43,6 +43,17 @@ __device__ __forceinline__ uint32_t token_id(const void *ids, bool id64, int64_t
     return v >= 0 && v < (int64_t)vocab ? (uint32_t)v : vocab;
 }
 
+// A lane's N columns begin at c, or further back where they would pass the row's
+// end: a value that two lanes compute is the same in both. `n` of them are its own
+// to write (0 behind the end, fewer than N where the row is shorter than that).
+struct Columns {
+    int c, n;
+};
+template <int N>
+__device__ __forceinline__ Columns columns(int64_t c, int64_t cols) {
+    return {(int)(c + N <= cols ? c : cols < N ? 0 : cols - N), (int)(c >= cols ? 0 : cols < N ? cols : N)};
+}
+
 // 2^lg lanes take one row, 8 columns each at a time.
 template <bool TB, bool YB>
 __global__ __launch_bounds__(256) void embed_kernel(Embed e, int lg) {
@@ -52,11 +63,12 @@ __global__ __launch_bounds__(256) void embed_kernel(Embed e, int lg) {
     const uint32_t id = token_id(e.ids, e.id64, t, (uint32_t)e.vocab);
     const bool there = id < (uint32_t)e.vocab;
     for (int64_t c = (int64_t)(threadIdx.x & ((1 << lg) - 1)) * 8; c < e.cols; c += step) {
+        const Columns at = columns<8>(c, e.cols);
         float v[8];
-        unpack(load_raw<TB, 8>(e.table, there ? (int64_t)id * e.cols : 0, (int)c, (int)e.cols), (int)c, (int)e.cols, v);
+        unpack(load_raw<TB, 8>(e.table, there ? (int64_t)id * e.cols : 0, at.c, (int)e.cols), at.c, (int)e.cols, v, true);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = there ? v[j] * e.scale : 0.0f;
-        store_n<YB>(e.y, t * e.cols + c, (int)(e.cols - c < 8 ? e.cols - c : 8), v);
+        store_n<YB>(e.y, t * e.cols + at.c, at.n, v);
     }
 }
 
@@ -239,23 +251,23 @@ __global__ __launch_bounds__(256) void embed_merge_kernel(const uint64_t *from, 
 // ---------------------------------------------------------------------------
 // The gradient of a row's columns from their sum; `old`: what is there, to add to.
 template <bool GB, bool ADD>
-__device__ __forceinline__ void write_row(const EmbedGrad &e, int64_t worker, uint32_t id, int64_t c, int n,
+__device__ __forceinline__ void write_row(const EmbedGrad &e, int64_t worker, uint32_t id, Columns at,
                                           const float (&sum)[4], const Raw<GB, 4> &old) {
     float v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = e.scale * sum[j];
     if constexpr (ADD) {
         float o[4];
-        unpack(old, (int)c, (int)e.cols, o);
+        unpack(old, at.c, (int)e.cols, o, true);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] += o[j];
     }
-    if (n > 0) store_n<GB>(e.grad, (worker * e.vocab + id) * e.cols + c, n, v);
+    if (at.n > 0) store_n<GB>(e.grad, (worker * e.vocab + id) * e.cols + at.c, at.n, v);
 }
 
-__device__ __forceinline__ void write_partial(const EmbedGrad &e, int64_t worker, int seg, int which, int64_t c,
-                                              int n, const float (&sum)[4]) {
-    if (n > 0) store_n<false>(e.partial, ((worker * e.segments + seg) * 2 + which) * e.cols + c, n, sum);
+__device__ __forceinline__ void write_partial(const EmbedGrad &e, int64_t worker, int seg, int which, Columns at,
+                                              const float (&sum)[4]) {
+    if (at.n > 0) store_n<false>(e.partial, ((worker * e.segments + seg) * 2 + which) * e.cols + at.c, at.n, sum);
 }
 
 // Zeros in the rows of `rows` ids that no token has, by a workgroup (rows that
@@ -311,17 +323,15 @@ __global__ __launch_bounds__(256) void embed_sums_kernel(EmbedGrad e, const uint
     const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     if (w >= sum_waves) return;
     const int blocks = (int)((e.cols + kEmbedCols - 1) / kEmbedCols);
-    const int64_t c = (w % blocks) * kEmbedCols + lane * 4;
+    const Columns own = columns<4>((w % blocks) * kEmbedCols + lane * 4, e.cols);
     const int seg = (int)(w / blocks % e.segments);
     const int64_t worker = w / blocks / e.segments;
-    const int n = (int)(e.cols - c < 4 ? e.cols - c : 4);  // columns of this lane (below 1: none)
     keys += worker * e.tokens;
     const int64_t begin = (int64_t)seg * e.seg;
     const int64_t end = begin + e.seg < e.tokens ? begin + e.seg : e.tokens;
     const uint32_t none = (uint32_t)e.vocab;  // padding: sorted behind every row
     const uint32_t before = begin > 0 ? (uint32_t)(keys[begin - 1] >> 32) : none;
     const int64_t base = worker * e.tokens;
-    const bool whole = (w % blocks + 1) * kEmbedCols <= e.cols;
     uint32_t cur = none;  // a row that goes on
     bool first = true;    // none has ended in this segment
     float sum[4] = {};
@@ -338,24 +348,24 @@ __global__ __launch_bounds__(256) void embed_sums_kernel(EmbedGrad e, const uint
             for (int i = 0; i < kInFlight; ++i) {
                 const uint32_t id = __builtin_amdgcn_readlane(key_id, i0 + i);
                 const uint32_t t = id == none ? 0 : __builtin_amdgcn_readlane(key_at, i0 + i);
-                v[i] = load_raw<DB, 4>(e.dy, (base + t) * e.cols, (int)c, (int)e.cols);
+                v[i] = load_raw<DB, 4>(e.dy, (base + t) * e.cols, own.c, (int)e.cols);
                 if constexpr (ADD)
-                    old[i] = load_raw<GB, 4>(e.grad, (worker * e.vocab + (id == none ? 0 : id)) * e.cols, (int)c, (int)e.cols);
+                    old[i] = load_raw<GB, 4>(e.grad, (worker * e.vocab + (id == none ? 0 : id)) * e.cols, own.c, (int)e.cols);
             }
 #pragma unroll
             for (int i = 0; i < kInFlight; ++i) {
                 const uint32_t id = __builtin_amdgcn_readlane(key_id, i0 + i);
                 if (id == none) continue;
                 float x[4];
-                unpack(v[i], (int)c, (int)e.cols, x, whole);
+                unpack(v[i], own.c, (int)e.cols, x, true);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) sum[j] += x[j];
                 cur = id;
                 if (id != __builtin_amdgcn_readlane(key_next, i0 + i)) {
                     if (first && id == before)
-                        write_partial(e, worker, seg, 0, c, n, sum);
+                        write_partial(e, worker, seg, 0, own, sum);
                     else
-                        write_row<GB, ADD>(e, worker, id, c, n, sum, old[ADD ? i : 0]);
+                        write_row<GB, ADD>(e, worker, id, own, sum, old[ADD ? i : 0]);
                     first = false;
                     cur = none;
 #pragma unroll
@@ -364,8 +374,10 @@ __global__ __launch_bounds__(256) void embed_sums_kernel(EmbedGrad e, const uint
             }
         }
     }
-    if (cur != none) write_partial(e, worker, seg, first && cur == before ? 0 : 1, c, n, sum);
+    if (cur != none) write_partial(e, worker, seg, first && cur == before ? 0 : 1, own, sum);
 }
+
+constexpr int kJoined = 8;  // partial sums that a wave has under way
 
 // A row that begins in segment `seg` and goes on in the next ones: its last
 // partial there, then the first partials of the segments that it reaches.
@@ -375,38 +387,46 @@ __global__ __launch_bounds__(256) void embed_join_kernel(EmbedGrad e, const uint
     const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     if (w >= waves) return;
     const int blocks = (int)((e.cols + kEmbedCols - 1) / kEmbedCols);
-    const int64_t c = (w % blocks) * kEmbedCols + lane * 4;
+    const Columns own = columns<4>((w % blocks) * kEmbedCols + lane * 4, e.cols);
     const int seg = (int)(w / blocks % (e.segments - 1));
     const int64_t worker = w / blocks / (e.segments - 1);
     keys += worker * e.tokens;
     const int64_t begin = (int64_t)seg * e.seg, end = begin + e.seg;  // end < tokens: not the last segment
-    const uint32_t id = (uint32_t)(keys[end - 1] >> 32);
-    if (id == (uint32_t)e.vocab || (uint32_t)(keys[end] >> 32) != id) return;
+    // the row of the last token here, and of the first token of the segment i + lane
+    const uint32_t none = (uint32_t)e.vocab, id = (uint32_t)(keys[end - 1] >> 32);
+    auto first_of = [&](int i) {
+        const int64_t at = (int64_t)(i + lane) * e.seg;
+        return at < e.tokens ? (uint32_t)(keys[at] >> 32) : none;
+    };
+    const uint32_t before = begin > 0 ? (uint32_t)(keys[begin - 1] >> 32) : none;
+    uint64_t reached = __ballot(first_of(seg + 1) == id);
     // one that began in an earlier segment is joined there
-    if (begin > 0 && (uint32_t)(keys[begin - 1] >> 32) == id) return;
-    const int n = (int)(e.cols - c < 4 ? e.cols - c : 4);
+    if (id == none || !(reached & 1) || before == id) return;
+    int last = seg;  // the last segment that it reaches
+    while (reached == ~0ull) {
+        last += kWave;
+        reached = __ballot(first_of(last + 1) == id);
+    }
+    last += __builtin_ctzll(~reached);
     Raw<GB, 4> old;
-    if constexpr (ADD) old = load_raw<GB, 4>(e.grad, (worker * e.vocab + id) * e.cols, (int)c, (int)e.cols);
-    // the last token of the row, and its segment
-    const int64_t stop = end + wave_lower_bound(keys + end, e.tokens - end, (uint64_t)(id + 1) << 32, lane);
-    const int last = (int)((stop - 1) / e.seg);
+    if constexpr (ADD) old = load_raw<GB, 4>(e.grad, (worker * e.vocab + id) * e.cols, own.c, (int)e.cols);
     const int64_t at = (worker * e.segments + seg) * 2 * e.cols;
     float sum[4];
-    unpack(load_raw<false, 4>(e.partial, at + e.cols, (int)c, (int)e.cols), (int)c, (int)e.cols, sum);
-    for (int i = 1; i <= last - seg; i += 8) {
-        Raw<false, 4> v[8];
+    unpack(load_raw<false, 4>(e.partial, at + e.cols, own.c, (int)e.cols), own.c, (int)e.cols, sum, true);
+    for (int i = 1; i <= last - seg; i += kJoined) {
+        Raw<false, 4> v[kJoined];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            v[k] = load_raw<false, 4>(e.partial, at + (int64_t)(i + k <= last - seg ? i + k : i) * 2 * e.cols, (int)c, (int)e.cols);
+        for (int k = 0; k < kJoined; ++k)
+            v[k] = load_raw<false, 4>(e.partial, at + (int64_t)(i + k <= last - seg ? i + k : i) * 2 * e.cols, own.c, (int)e.cols);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kJoined; ++k) {
             float x[4];
-            unpack(v[k], (int)c, (int)e.cols, x);
+            unpack(v[k], own.c, (int)e.cols, x, true);
 #pragma unroll
             for (int j = 0; j < 4; ++j) sum[j] += i + k <= last - seg ? x[j] : 0.0f;
         }
     }
-    write_row<GB, ADD>(e, worker, id, c, n, sum, old);
+    write_row<GB, ADD>(e, worker, id, own, sum, old);
 }
 
 // The first of the rows that get their zeros beside the sort.
