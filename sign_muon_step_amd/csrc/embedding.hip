@@ -23,7 +23,7 @@
 //   embed_join_kernel   adds the partial sums of each row, in their order
 //
 // 8 workers x 4096 tokens, 32000 x 768, F32 from BF16: 153 us, of which 119 us are
-// what the stack's zeros alone take to store; 3 x 1501 tokens, 5003 x 515: 20 us,
+// what the stack's zeros alone take to store; 3 x 1501 tokens, 5003 x 515: 20.5 us,
 // three launches that wait for one another.
 #include "grad_internal.h"
 
@@ -43,15 +43,28 @@ __device__ __forceinline__ uint32_t token_id(const void *ids, bool id64, int64_t
     return v >= 0 && v < (int64_t)vocab ? (uint32_t)v : vocab;
 }
 
-// A lane's N columns begin at c, or further back where they would pass the row's
-// end: a value that two lanes compute is the same in both. `n` of them are its own
-// to write (0 behind the end, fewer than N where the row is shorter than that).
+// A lane's N columns of a row begin at c, or further back where they would pass the
+// row's end: a value that two lanes of a wave compute is the same in both. Those in
+// [from, n) are stored: none behind the end, fewer than N where the row is shorter
+// than that, and none below the wave's first column, which is another wave's (adding
+// to what is there, the two would each add).
 struct Columns {
-    int c, n;
+    int c, from, n;
 };
 template <int N>
-__device__ __forceinline__ Columns columns(int64_t c, int64_t cols) {
-    return {(int)(c + N <= cols ? c : cols < N ? 0 : cols - N), (int)(c >= cols ? 0 : cols < N ? cols : N)};
+__device__ __forceinline__ Columns columns(int64_t c, int64_t cols, int64_t first) {
+    const int64_t at = c + N <= cols ? c : cols < N ? 0 : cols - N;
+    return {(int)at, (int)(first > at ? first - at : 0), (int)(c >= cols ? 0 : cols < N ? cols : N)};
+}
+template <bool BF16, int N>
+__device__ __forceinline__ void store_columns(void *p, int64_t row, Columns at, const float (&v)[N]) {
+    if (at.from == 0 && at.n == N) {
+        store_n<BF16>(p, row + at.c, N, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j >= at.from && j < at.n) store1<BF16>(p, row + at.c + j, v[j]);
+    }
 }
 
 // 2^lg lanes take one row, 8 columns each at a time.
@@ -63,12 +76,12 @@ __global__ __launch_bounds__(256) void embed_kernel(Embed e, int lg) {
     const uint32_t id = token_id(e.ids, e.id64, t, (uint32_t)e.vocab);
     const bool there = id < (uint32_t)e.vocab;
     for (int64_t c = (int64_t)(threadIdx.x & ((1 << lg) - 1)) * 8; c < e.cols; c += step) {
-        const Columns at = columns<8>(c, e.cols);
+        const Columns at = columns<8>(c, e.cols, 0);
         float v[8];
         unpack(load_raw<TB, 8>(e.table, there ? (int64_t)id * e.cols : 0, at.c, (int)e.cols), at.c, (int)e.cols, v, true);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = there ? v[j] * e.scale : 0.0f;
-        store_n<YB>(e.y, t * e.cols + at.c, at.n, v);
+        store_columns<YB>(e.y, t * e.cols, at, v);
     }
 }
 
@@ -262,12 +275,12 @@ __device__ __forceinline__ void write_row(const EmbedGrad &e, int64_t worker, ui
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] += o[j];
     }
-    if (at.n > 0) store_n<GB>(e.grad, (worker * e.vocab + id) * e.cols + at.c, at.n, v);
+    store_columns<GB>(e.grad, (worker * e.vocab + id) * e.cols, at, v);
 }
 
 __device__ __forceinline__ void write_partial(const EmbedGrad &e, int64_t worker, int seg, int which, Columns at,
                                               const float (&sum)[4]) {
-    if (at.n > 0) store_n<false>(e.partial, ((worker * e.segments + seg) * 2 + which) * e.cols + at.c, at.n, sum);
+    store_columns<false>(e.partial, ((worker * e.segments + seg) * 2 + which) * e.cols, at, sum);
 }
 
 // Zeros in the rows of `rows` ids that no token has, by a workgroup (rows that
@@ -323,7 +336,8 @@ __global__ __launch_bounds__(256) void embed_sums_kernel(EmbedGrad e, const uint
     const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     if (w >= sum_waves) return;
     const int blocks = (int)((e.cols + kEmbedCols - 1) / kEmbedCols);
-    const Columns own = columns<4>((w % blocks) * kEmbedCols + lane * 4, e.cols);
+    const int64_t first_col = (w % blocks) * kEmbedCols;
+    const Columns own = columns<4>(first_col + lane * 4, e.cols, first_col);
     const int seg = (int)(w / blocks % e.segments);
     const int64_t worker = w / blocks / e.segments;
     keys += worker * e.tokens;
@@ -387,7 +401,8 @@ __global__ __launch_bounds__(256) void embed_join_kernel(EmbedGrad e, const uint
     const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     if (w >= waves) return;
     const int blocks = (int)((e.cols + kEmbedCols - 1) / kEmbedCols);
-    const Columns own = columns<4>((w % blocks) * kEmbedCols + lane * 4, e.cols);
+    const int64_t first_col = (w % blocks) * kEmbedCols;
+    const Columns own = columns<4>(first_col + lane * 4, e.cols, first_col);
     const int seg = (int)(w / blocks % (e.segments - 1));
     const int64_t worker = w / blocks / (e.segments - 1);
     keys += worker * e.tokens;

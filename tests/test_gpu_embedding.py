@@ -189,3 +189,12 @@ def test_a_captured_gradient_replays_like_eager_calls():
         sm.signmuon_embedding_backward(ids, dy, 2.0, grad, ws.t)
 
     replays_like_eager(call, [y, grad], refresh)
+
+
+@pytest.mark.parametrize("cols", [1, 3, 4, 5, 255, 256, 257, 258, 259, 260, 513, 515, 769, 1025, 1027])
+@pytest.mark.parametrize("grad_dtype", [torch.float32, torch.bfloat16])
+def test_adding_to_columns_at_the_border_of_two_waves(cols, grad_dtype):
+    """Each column is added to once, whatever part of it shares a vector with the
+    columns of another wave; rows of one segment and rows that several share."""
+    for kind, tokens, vocab in (("some", 3000, 4000), ("words", 3000, 4000), ("one", 500, 3)):
+        check_gradient(kind, 3, tokens, vocab, cols, torch.int32, torch.bfloat16, grad_dtype, True)
