@@ -1,6 +1,11 @@
 """Helpers for the tests of the gradient operators: output buffers between
-guard bytes, rounding units, captured replays."""
+guard bytes, rounding units, captured replays, and the library's own choices of
+kernels."""
+import ctypes
+
 import torch
+
+import sign_muon_step_amd as sm
 
 DEV = torch.device("cuda:0")
 GUARD = 1024
@@ -65,3 +70,22 @@ def replays_like_eager(call, outputs, refresh, rounds=3):
         torch.cuda.synchronize()
         for t, w in zip(outputs, want):
             assert same_bits(t, w), f"replay {i} differs from the eager call"
+
+
+class _Plan(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("tile", "splits", "chunk", "waves")]
+
+
+def f8_plan(batch, m, n, k):
+    """The library's own plan of an 8-bit product (csrc/grad_internal.h, F8Plan): which kernel and tile, the parts of k
+    and their blocks, and the waves that share a tile's k where m is small. No GPU needed."""
+    fn = sm.library()._ZN2sm7f8_planEllll
+    fn.restype, fn.argtypes = _Plan, [ctypes.c_int64] * 4
+    return fn(batch, m, n, k)
+
+
+def embed_segment(workers, tokens, cols):
+    """Sorted tokens that a wave of the table's gradient takes (csrc/grad_internal.h). No GPU needed."""
+    fn = sm.library()._ZN2sm13embed_segmentEill
+    fn.restype, fn.argtypes = ctypes.c_int32, [ctypes.c_int32, ctypes.c_int64, ctypes.c_int64]
+    return fn(workers, tokens, cols)
