@@ -415,7 +415,9 @@ size_t signmuon_layer_norm_workspace_bytes(int32_t workers, int64_t rows, int64_
  * block (0 for a block with no finite nonzero value), the scale byte e + 127,
  * and q = x * 2^-e rounded to nearest even. NaN gives NaN; an infinity gives
  * NaN in E4M3 and itself in E5M2. Padding bytes of q and qt are written as
- * zeros, padding scale bytes as 127. batch is at most 255, rows and cols 2^25.
+ * zeros, padding scale bytes as 127. A value within a 16th of 2^128 (E4M3: a 32nd)
+ * may be rounded up to stand for 2^128, which fp32 does not have. batch is at most
+ * 255, rows and cols 2^25.
  */
 int signmuon_f8_quant(const void *x, signmuon_dtype x_dtype, int32_t batch, int64_t rows,
                       int64_t cols, signmuon_f8 format, void *q, uint8_t *q_scale, void *qt,
@@ -427,15 +429,20 @@ size_t signmuon_f8_scale_pitch(int64_t k);
 
 /*
  * signmuon_f8_matmul -- out[i][r][c] = sum over k of a[i][r][k] * b[i][c][k]
- * of the values that the operands stand for, accumulated in fp32 on the matrix
- * cores and rounded once to out_dtype. For a BF16 out the matrix cores multiply
- * the bytes themselves and cut the products of each 8 consecutive k below 2^-13
- * of the largest one's power of two (1.4e-5 of a sum of random products); for an
- * F32 out they multiply the bytes widened to BF16, at half the rate, and add as
- * fp32 does (values below 2^-126 count as BF16 holds them). a is [batch][m] rows of k values, b
- * [batch][n] rows, or [n] rows shared by every i (b_shared = 1), both laid out
- * and padded as signmuon_f8_quant writes them (the bytes past k must be zero);
- * out is [batch][m][n]. For a linear layer y = x w^T with w [n][k]: the output
+ * of the values that the operands stand for, summed on the matrix cores and
+ * rounded once to out_dtype, which also chooses the sum's accuracy:
+ *  - F32: the bytes are widened to BF16 with their scale, at half the rate, and
+ *    the products are added with fp32's accuracy. Values from 2^-126 up to 2^128
+ *    are exact. Smaller ones count as BF16 holds them, and 2^128 and more, which
+ *    fp32 does not have either, as infinite.
+ *  - BF16: the bytes themselves are multiplied. Before they are added to fp32
+ *    sums, the products of each 8 consecutive k are cut below 2^-13 of the power
+ *    of two of the largest one (1.4e-5 of a sum of random products, where a BF16
+ *    result is rounded by up to 2^-8). Where large products cancel, what is left
+ *    of the small ones can be lost: a caller whose sums do that takes an F32 out.
+ * a is [batch][m] rows of k values, b [batch][n] rows, or [n] rows shared by
+ * every i (b_shared = 1), both laid out and padded as signmuon_f8_quant writes
+ * them (the bytes past k must be zero); out is [batch][m][n]. For a linear layer y = x w^T with w [n][k]: the output
  * takes x and w by rows; the input's gradient dy by rows and w by columns; the
  * weight's gradient of each worker dy and x by columns, batch = workers, which
  * fills signmuon_matrix.grad. workspace:

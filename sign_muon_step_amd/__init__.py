@@ -626,7 +626,10 @@ def signmuon_f8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, 
                        out: torch.Tensor, workspace: Optional[torch.Tensor], stream=None) -> None:
     """out [m][n] (or [B][m][n]) = a b^T over k values, of 8-bit operands as
     signmuon_f8_quant writes them: a [..][m][pitch(k)], b [..][n][pitch(k)].
-    With a batch, b may be one matrix ([n] or [1][n] rows) for every entry."""
+    With a batch, b may be one matrix ([n] or [1][n] rows) for every entry.
+    out's type chooses the sum's accuracy: a float32 out has fp32's, a bfloat16
+    one cuts the products of each 8 k below 2^-13 of the largest, at twice the
+    rate (see include/signmuon.h)."""
     shape = _rank(out, "out", (2, 3))
     m, n = shape[-2:]
     lead = shape[:-2]

@@ -12,10 +12,12 @@
 //        of the largest one (seen with one large and one small product, at
 //        every distance and place): 1.4e-5 of a sum of random products, far
 //        below BF16's 2^-8.
-//  F32   the bytes are converted to BF16 with their scale (exact: 4 bits of
-//        mantissa or less, and BF16 has fp32's exponents) and multiplied by
+//  F32   the bytes are converted to BF16 with their scale and multiplied by
 //        v_mfma_f32_*_bf16, which adds with fp32's accuracy at half the rate
-//        (6e-9 of the same sums).
+//        (6e-9 of the same sums). BF16 holds every value from 2^-126 to below
+//        2^128 (4 bits of mantissa or less, fp32's exponents); scales from 2^120
+//        on (E5M2: 2^113) can stand for more, which becomes infinite, where the
+//        other form has it.
 // Sums are fp32 in both.
 //
 // The products are computed as b a^T: the instruction's rows are out's columns,
