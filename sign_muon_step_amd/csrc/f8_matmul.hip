@@ -690,9 +690,16 @@ F8Plan f8_plan(int64_t batch, int64_t m, int64_t n, int64_t k) {
     F8Plan p{};
     p.splits = 1;
     p.chunk = (int32_t)(groups * 4);
-    // Few rows: each tile of 16 columns reads all of a, which costs more than b
-    // from about 32 rows on (n = 11008, k = 4096: 22.6 us at 32 rows and 30 at 48,
-    // where tiles of 128 take 20 and 21; n = k = 4096: 9.2 and 11.8 against 12.1 and 12.6).
+    // Few rows: each tile of 16 columns reads all of a, which costs more than b from
+    // about 32 rows on. Against tiles of 128 (us, BF16, n x k; 256 is never faster):
+    //              8 rows       16 rows      24 rows      32 rows
+    // 11008 x 4096 14.8 / 16.3  16.0 / 16.2  19.3 / 16.5  21.4 / 16.7
+    // 4096 x 4096   8.8 / 12.7   8.8 / 12.8   8.7 / 13.3   9.3 / 13.5
+    // 4096 x 11008 12.4 / 20.3  14.3 / 20.2  17.3 / 20.4  19.0 / 20.6
+    // 2304 x 768    8.6 / 9.4    8.7 / 9.4    8.7 / 9.4    8.7 / 9.4
+    // The rule goes by m alone: more than about 16 rows of a wide b (688 tiles of 16
+    // columns where the device has 256 compute units) would take 15 to 22 % less in
+    // tiles for a BF16 result, and the same for an F32 one (21.4 / 21.8 at 32 rows).
     if (m <= 32) {
         p.tile = 16;
         // waves that share a tile's k: 2 to 8, until each has one group of four
@@ -702,14 +709,17 @@ F8Plan f8_plan(int64_t batch, int64_t m, int64_t n, int64_t k) {
         while (p.waves < 8 && p.waves < groups && wgs * p.waves < 2048) p.waves *= 2;
         return p;
     }
-    // The tile and the parts of k (at least 4 blocks each) of the least time by
-    // this model, in units of about half a microsecond, fitted to both tiles at
-    // 8 to 11008 tiles and 6 to 64 blocks: a round of tiles (one of 256 or two of
-    // 128 a compute unit) takes 3 units a block and 10 more, or 2 and 4 more;
-    // adding the parts takes 10 and 2 MB of partial sums written or read a unit.
-    // E.g. 8192 x 2304 x 768 to bf16: 288 tiles of 256 in two rounds, 30.7 us, 1152 of
-    // 128 in three short ones, 25 us; 8 x 768 x 2304 x 2000 to fp32: 216 tiles in one
-    // round, 62 us, 864 in two, 66 us.
+    // The tile and the parts of k (whole groups of 4 blocks; the last part may be
+    // shorter) of the least time by this model, in units of about half a microsecond,
+    // fitted to both tiles at 8 to 11008 tiles and 6 to 64 blocks: a round of tiles
+    // (one of 256 or two of 128 a compute unit) takes 3 units a block and 10 more, or 2
+    // and 4 more, a group that is not full counted as a full one; adding the parts
+    // takes 10 and 2 MB of partial sums written or read a unit. The compute units are
+    // those of a whole MI355X, not asked for, since the workspace's size is told
+    // without a device and has to be that of the same plan.
+    // E.g. 8192 x 2304 x 768 to BF16: 288 tiles of 256 in two rounds, 29.3 us, 1152 of
+    // 128 in three short ones, 23.7 us; 8 x 768 x 2304 x 2000 to F32: 216 tiles in one
+    // round, 60 us, 864 in two, 63 us.
     double best = 0.0;
     for (const int32_t tile : {256, 128}) {
         const int64_t tiles = batch * ((m + tile - 1) / tile) * ((n + tile - 1) / tile);
