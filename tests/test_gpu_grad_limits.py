@@ -136,3 +136,25 @@ def test_layer_norm_sums_of_whole_numbers(workers, rows, cols, dtype, grad_dtype
         for got, want in ((dgamma, (dy[part].double() * x[part].double()).sum(0)), (dbeta, dy[part].double().sum(0))):
             assert float(want.abs().max()) < 2 ** 23
             assert same_bits(got.t[m] + 0.0, want.float().to(grad_dtype) + 0.0), f"worker {m}"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("workers,tokens,vocab,cols", [(1, 40, 9, 515), (3, 5000, 700, 130), (2, 16384, 300, 4096)])
+@pytest.mark.parametrize("add", [False, True])
+def test_nan_and_infinity_at_padding(workers, tokens, vocab, cols, add):
+    """What stands at tokens whose id is outside the table does not reach the gradient."""
+    g = torch.Generator(device=DEV).manual_seed(4)
+    ids = torch.randint(0, vocab, (workers, tokens), generator=g, device=DEV)
+    ids[:, ::3], ids[:, 1::7] = -1, vocab
+    ids[-1, tokens // 2:] = 1 << 40
+    dy = torch.randint(-8, 9, (workers, tokens, cols), generator=g, device=DEV, dtype=torch.int8).bfloat16()
+    away = (ids < 0) | (ids >= vocab)
+    grads = []
+    for value in (0.0, float("nan"), float("inf")):
+        dy[away] = value
+        grad = torch.full((workers, vocab, cols), 3.0, device=DEV)
+        ws = sm.bytes_tensor(sm.signmuon_embedding_workspace_bytes(workers, tokens, vocab, cols), DEV)
+        sm.signmuon_embedding_backward(ids, dy, 0.5, grad, ws, accumulate=add)
+        grads.append(grad)
+    assert bool(grads[0].isfinite().all())
+    assert same_bits(grads[0], grads[1]) and same_bits(grads[0], grads[2])
