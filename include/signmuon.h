@@ -442,13 +442,13 @@ size_t signmuon_f8_scale_pitch(int64_t k);
  *    of the small ones can be lost: a caller whose sums do that takes an F32 out.
  * a is [batch][m] rows of k values, b [batch][n] rows, or [n] rows shared by
  * every i (b_shared = 1), both laid out and padded as signmuon_f8_quant writes
- * them (the bytes past k must be zero); out is [batch][m][n]. For a linear layer y = x w^T with w [n][k]: the output
- * takes x and w by rows; the input's gradient dy by rows and w by columns; the
- * weight's gradient of each worker dy and x by columns, batch = workers, which
- * fills signmuon_matrix.grad. Entries of few rows (m up to 32) that share b may
- * each read it: as one product (batch = 1) of all their rows they read it once.
- * workspace: signmuon_f8_matmul_workspace_bytes(batch, m, n, k) bytes (may be 0,
- * then NULL).
+ * them (the bytes past k must be zero); out is [batch][m][n]. For a linear layer
+ * y = x w^T with w [n][k]: the output takes x and w by rows; the input's gradient
+ * dy by rows and w by columns; the weight's gradient of each worker dy and x by
+ * columns, batch = workers, which fills signmuon_matrix.grad. Entries of few rows
+ * (m up to 32) that share b may each read it: as one product (batch = 1) of all
+ * their rows they read it once. workspace:
+ * signmuon_f8_matmul_workspace_bytes(batch, m, n, k) bytes (may be 0, then NULL).
  * batch is at most 255, m 2^25, n 2^21 and k 2^22.
  */
 int signmuon_f8_matmul(const void *a, const uint8_t *a_scale, signmuon_f8 a_format, const void *b,
