@@ -51,7 +51,7 @@
 extern "C" {
 #endif
 
-#define SIGNMUON_ABI_VERSION 5
+#define SIGNMUON_ABI_VERSION 6
 
 /* Status codes. */
 enum {
@@ -308,8 +308,9 @@ size_t signmuon_workspace_bytes(const signmuon_matrix *mats, int32_t n_mats,
  * worker (summary §2 "Algorithmic flow", step 1: each worker's stochastic
  * gradient). The entry points below are the operators of a transformer's
  * training pass whose weight gradients go into such a stack as they are: the
- * embedding lookup and its gradient, layer norm and its gradients, and linear
- * layers in 8-bit floating point (quantisation and products). The workers'
+ * embedding lookup and its gradient, layer norm and root-mean-square norm and
+ * their gradients, and linear layers in 8-bit floating point (quantisation and
+ * products). The workers'
  * batches sit side by side: worker m's tokens at offset m * tokens. They
  * follow the conventions at the head of this file (device pointers, 16-byte
  * aligned bases, every argument checked before anything is enqueued, kernel
@@ -458,6 +459,48 @@ int signmuon_f8_matmul(const void *a, const uint8_t *a_scale, signmuon_f8 a_form
 
 /* Device workspace of signmuon_f8_matmul in bytes (0 on invalid arguments). */
 size_t signmuon_f8_matmul_workspace_bytes(int32_t batch, int64_t m, int64_t n, int64_t k);
+
+/*
+ * signmuon_rms_norm -- root-mean-square norm with the residual's addition, for
+ * each of rows rows of cols values:
+ *   h = x + residual, rounded to x_dtype (h = x where residual is NULL)
+ *   rstd = 1 / sqrt(sum(h^2) / cols + eps),  y = h * rstd * gamma
+ * x, residual, h and y are [rows][cols] of x_dtype, gamma is [cols] fp32. The
+ * norm is that of the rounded h, which the residual stream carries on. h
+ * receives it (NULL: not wanted; only with a residual) and may be x or residual
+ * (in place). y receives the output in x_dtype; q and q_scale receive it in
+ * 8 bits, quantised from fp32 as signmuon_f8_quant lays out its rows
+ * ([rows][signmuon_f8_pitch(cols)] and [rows][signmuon_f8_scale_pitch(cols)],
+ * padding included; format is ignored where q is NULL): the operand of a
+ * signmuon_f8_matmul. Either of y and q may be NULL, not both. rstd [rows] fp32 is
+ * kept for the backward pass (may be NULL). eps is positive and finite. Sums of
+ * squares are fp32: where one passes fp32's range, the row's output is 0.
+ */
+int signmuon_rms_norm(const void *x, const void *residual, signmuon_dtype x_dtype, int64_t rows,
+                      int64_t cols, const float *gamma, float eps, void *h, void *y,
+                      signmuon_f8 format, void *q, uint8_t *q_scale, float *rstd,
+                      signmuon_stream stream);
+
+/*
+ * signmuon_rms_norm_backward -- with xh = h * rstd and t = dy * gamma:
+ *   dx = dh + rstd * (t - xh * mean_c(t * xh)),  dgamma[m] = sum over worker m's rows of dy * xh
+ * dx is the gradient of x and of the residual alike. dy is the gradient of the
+ * output, dh that of h by the residual stream (NULL: none); h is what
+ * signmuon_rms_norm normed (its h, or x where it had no residual) and rstd its
+ * statistics. dy, dh, h and dx are [workers][rows][cols] of x_dtype, rstd
+ * [workers][rows], dgamma [workers][cols] of grad_dtype (the layout of
+ * signmuon_matrix.grad for a 1 x cols matrix). dx may be dy or dh (in place).
+ * Either of dx and dgamma may be NULL (not wanted), not both. workspace:
+ * signmuon_rms_norm_workspace_bytes(workers, rows, cols) bytes.
+ */
+int signmuon_rms_norm_backward(const void *dy, const void *dh, const void *h, signmuon_dtype x_dtype,
+                               int32_t workers, int64_t rows, int64_t cols, const float *gamma,
+                               const float *rstd, void *dx, void *dgamma, signmuon_dtype grad_dtype,
+                               void *workspace, size_t workspace_bytes, signmuon_stream stream);
+
+/* Device workspace of signmuon_rms_norm_backward in bytes (0 on invalid
+ * arguments). */
+size_t signmuon_rms_norm_workspace_bytes(int32_t workers, int64_t rows, int64_t cols);
 
 /* Text for a status code; for SIGNMUON_EHIP it names the HIP error of the
  * calling thread's last failure. Never NULL. */

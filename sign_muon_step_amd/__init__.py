@@ -21,7 +21,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsignmuon.so")
 
 F32, BF16 = 0, 1
-ABI_VERSION = 5
+ABI_VERSION = 6
 # device bytes of the static scratch behind signmuon_step_noalloc
 STATIC_SCRATCH_BYTES = 128 << 20
 
@@ -105,7 +105,10 @@ def library() -> ctypes.CDLL:
             ("f8_pitch", size, [i64]),
             ("f8_scale_pitch", size, [i64]),
             ("f8_matmul", i32, [vp, vp, i32, vp, vp, i32, i32, i64, i64, i64, i32, vp, i32, vp, size, vp]),
-            ("f8_matmul_workspace_bytes", size, [i32, i64, i64, i64])):
+            ("f8_matmul_workspace_bytes", size, [i32, i64, i64, i64]),
+            ("rms_norm", i32, [vp, vp, i32, i64, i64, vp, f32, vp, vp, i32, vp, vp, vp, vp]),
+            ("rms_norm_backward", i32, [vp, vp, vp, i32, i32, i64, i64, vp, vp, vp, vp, i32, vp, size, vp]),
+            ("rms_norm_workspace_bytes", size, [i32, i64, i64])):
         fn = getattr(lib, "signmuon_" + name)
         fn.restype, fn.argtypes = result, args
     lib.signmuon_packed_words.restype = ctypes.c_size_t
@@ -640,3 +643,48 @@ def signmuon_f8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, 
     args = (pa, pas, fa, pb, pbs, fb, batch, m, n, k, int(bool(one)), _operand(out, "out", _ACT, shape),
             _ACT[out.dtype], *_space(workspace))
     _on(stream, library().signmuon_f8_matmul, args, a, a_scale, b, b_scale, out, workspace)
+
+
+def signmuon_rms_norm(x: torch.Tensor, residual: Optional[torch.Tensor], gamma: torch.Tensor, eps: float,
+                      h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                      q: Optional[torch.Tensor] = None, q_scale: Optional[torch.Tensor] = None,
+                      rstd: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Root-mean-square norm of h = x + residual (or of x) over the last
+    dimension: h receives the sum (it may be x or residual), y the output in
+    x's type, q and q_scale the output in 8 bits (f8_empty(x.shape, ...), as
+    signmuon_f8_quant lays it out), rstd (x's other dimensions, fp32) what the
+    backward pass needs. y or q is given."""
+    cols = x.shape[-1] if x.dim() else 0
+    dtype = (x.dtype,)
+    pq, ps, fmt = _f8_operand(q, q_scale, "q", x.shape[:-1], cols)
+    args = (_operand(x, "x", _ACT, x.shape), _optional(residual, "residual", dtype, x.shape), _ACT[x.dtype],
+            x.numel() // max(cols, 1), cols, _operand(gamma, "gamma", _FP32, (cols,)), eps,
+            _optional(h, "h", dtype, x.shape), _optional(y, "y", dtype, x.shape), fmt or 0, pq, ps,
+            _optional(rstd, "rstd", _FP32, x.shape[:-1]))
+    _on(stream, library().signmuon_rms_norm, args, x, residual, gamma, h, y, q, q_scale, rstd)
+
+
+def signmuon_rms_norm_workspace_bytes(workers: int, rows: int, cols: int) -> int:
+    return int(library().signmuon_rms_norm_workspace_bytes(workers, rows, cols))
+
+
+def signmuon_rms_norm_backward(dy: torch.Tensor, dh: Optional[torch.Tensor], h: torch.Tensor, gamma: torch.Tensor,
+                               rstd: torch.Tensor, dx: Optional[torch.Tensor], dgamma: Optional[torch.Tensor],
+                               workspace: Optional[torch.Tensor], workers: int = 1, stream=None) -> None:
+    """Gradients of the root-mean-square norm: dx (of x and the residual
+    alike; it may be dy or dh) and dgamma, [Mw][C] or [Mw][1][C] (the layout of
+    Matrix.grad), one sum for each worker; h's rows are those of `workers`
+    workers, one after the other. dh is the residual stream's own gradient of h
+    (None: there is none). Either of dx and dgamma may be None."""
+    cols = h.shape[-1] if h.dim() else 0
+    rows = h.numel() // max(cols, 1)
+    if workers < 1 or rows % workers:
+        raise ValueError(f"h: {rows} rows are not those of {workers} workers")
+    dtype = (h.dtype,)
+    grad = dgamma.dtype if dgamma is not None else torch.float32
+    shape = (workers, 1, cols) if dgamma is not None and dgamma.dim() == 3 else (workers, cols)
+    args = (_operand(dy, "dy", dtype, h.shape), _optional(dh, "dh", dtype, h.shape), _operand(h, "h", _ACT, h.shape),
+            _ACT[h.dtype], workers, rows // workers, cols, _operand(gamma, "gamma", _FP32, (cols,)),
+            _operand(rstd, "rstd", _FP32, h.shape[:-1]), _optional(dx, "dx", dtype, h.shape),
+            _optional(dgamma, "dgamma", _ACT, shape), _ACT[grad], *_space(workspace))
+    _on(stream, library().signmuon_rms_norm_backward, args, dy, dh, h, gamma, rstd, dx, dgamma, workspace)

@@ -30,7 +30,6 @@
 namespace sm {
 namespace {
 
-constexpr int kWave = 64;
 static_assert(kSortChunk == 4 * 1024, "sorted by 1024 threads, 4 keys each");
 
 // The id of token t, or vocab where it lies outside [0, vocab).

@@ -41,7 +41,6 @@
 namespace sm {
 namespace {
 
-constexpr int kWave = 64;
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));

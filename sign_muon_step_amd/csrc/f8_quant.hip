@@ -19,42 +19,6 @@
 namespace sm {
 namespace {
 
-constexpr int kWave = 64;
-
-// e + 127 of a block from the bits of its largest finite size.
-template <bool E5M2>
-__device__ __forceinline__ int scale_byte(uint32_t top) {
-    // top = 1.m * 2^(field - 127) = f 2^p with p = field - 126; f > 0.875 where 1.m > 1.75
-    const int e = (int)(top >> 23) - 126 - (E5M2 ? 16 : 9) + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return top == 0 ? kF8Zero : (e < -127 ? 0 : e + 127);
-}
-
-// 2^(127 - byte): what values are multiplied by.
-__device__ __forceinline__ float inverse_scale(int byte) {
-    // byte <= 247 (the largest fp32 value), so the exponent field 254 - byte is positive
-    return __uint_as_float((uint32_t)(254 - byte) << 23);
-}
-
-template <bool E5M2>
-__device__ __forceinline__ uint32_t to_f8x4(float a, float b, float c, float d) {
-    int r = 0;
-    if (E5M2) {
-        r = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, r, false);
-        r = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, r, true);
-    } else {
-        r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, r, false);
-        r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
-    }
-    return (uint32_t)r;
-}
-
-__device__ __forceinline__ uint32_t finite_size(float v) {  // bits of |v|, 0 for NaN and infinities
-    const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
-    return b >= 0x7f800000u ? 0u : b;
-}
-
-__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-
 // Thread (wave w, lane l): rows 8 (4 w + l / 16) + 0..7 of the tile, columns
 // 8 (l % 16) + 0..7.
 template <bool BF16, bool E5M2, bool ROWS, bool COLS>

@@ -69,6 +69,14 @@ size_t norm_workspace(int32_t workers, int64_t rows, int64_t cols) {
 }
 
 // ---------------------------------------------------------------------------
+// Root-mean-square norm: check_norm, and
+// ---------------------------------------------------------------------------
+size_t rms_workspace(int32_t workers, int64_t rows, int64_t cols) {
+    const int32_t parts = sm::rms_parts(workers, rows, cols);
+    return parts > 1 ? (size_t)((int64_t)workers * parts * cols) * sizeof(float) : 0;
+}
+
+// ---------------------------------------------------------------------------
 // 8-bit floating point
 // ---------------------------------------------------------------------------
 constexpr int64_t kMaxK = (int64_t)1 << 22;     // a tile's rows of an operand lie within 2^31 bytes
@@ -322,6 +330,72 @@ int signmuon_f8_matmul(const void *a, const uint8_t *a_scale, signmuon_f8 a_form
     if (int rc = sm::launch_status()) return rc;
     if (f.splits == 1) return SIGNMUON_OK;
     sm::launch_f8_sums(f, st);
+    return sm::launch_status();
+}
+
+int signmuon_rms_norm(const void *x, const void *residual, signmuon_dtype x_dtype, int64_t rows,
+                      int64_t cols, const float *gamma, float eps, void *h, void *y,
+                      signmuon_f8 format, void *q, uint8_t *q_scale, float *rstd,
+                      signmuon_stream stream) {
+    if (!x || !gamma || (!y && !q) || !q != !q_scale || (h && !residual)) return SIGNMUON_EINVAL;
+    if (int rc = check_norm(1, rows, cols)) return rc;
+    if (!std::isfinite(eps) || eps <= 0.0f) return SIGNMUON_EINVAL;
+    if (!dtype_ok(x_dtype) || (q && !f8_ok(format))) return SIGNMUON_EDTYPE;
+    if (!all_aligned(x, residual, gamma, h, y, q, q_scale, rstd)) return SIGNMUON_EALIGN;
+    sm::RmsNorm n{};
+    n.x = x;
+    n.residual = residual;
+    n.gamma = gamma;
+    n.h = h;
+    n.y = y;
+    n.q = static_cast<uint8_t *>(q);
+    n.q_scale = q_scale;
+    n.rstd = rstd;
+    n.rows = rows;
+    n.cols = cols;
+    n.pitch = sm::f8_pitch(cols);
+    n.scale_pitch = sm::f8_scale_pitch(cols);
+    n.eps = eps;
+    n.bf16 = x_dtype == SIGNMUON_BF16;
+    n.e5m2 = format == SIGNMUON_E5M2;
+    sm::launch_rms_norm(n, static_cast<hipStream_t>(stream));
+    return sm::launch_status();
+}
+
+size_t signmuon_rms_norm_workspace_bytes(int32_t workers, int64_t rows, int64_t cols) {
+    if (check_norm(workers, rows, cols) != SIGNMUON_OK) return 0;
+    return rms_workspace(workers, rows, cols);
+}
+
+int signmuon_rms_norm_backward(const void *dy, const void *dh, const void *h, signmuon_dtype x_dtype,
+                               int32_t workers, int64_t rows, int64_t cols, const float *gamma,
+                               const float *rstd, void *dx, void *dgamma, signmuon_dtype grad_dtype,
+                               void *workspace, size_t workspace_bytes, signmuon_stream stream) {
+    if (!dy || !h || !gamma || !rstd || (!dx && !dgamma)) return SIGNMUON_EINVAL;
+    if (int rc = check_norm(workers, rows, cols)) return rc;
+    if (!dtype_ok(x_dtype) || !dtype_ok(grad_dtype)) return SIGNMUON_EDTYPE;
+    if (!all_aligned(dy, dh, h, gamma, rstd, dx, dgamma)) return SIGNMUON_EALIGN;
+    if (int rc = check_workspace(workspace, workspace_bytes, rms_workspace(workers, rows, cols))) return rc;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    sm::RmsGrad n{};
+    n.dy = dy;
+    n.dh = dh;
+    n.h = h;
+    n.gamma = gamma;
+    n.rstd = rstd;
+    n.dx = dx;
+    n.dgamma = dgamma;
+    n.partial = static_cast<float *>(workspace);
+    n.rows = rows;
+    n.cols = cols;
+    n.workers = workers;
+    n.parts = sm::rms_parts(workers, rows, cols);
+    n.bf16 = x_dtype == SIGNMUON_BF16;
+    n.grad_bf16 = grad_dtype == SIGNMUON_BF16;
+    sm::launch_rms_norm_backward(n, st);
+    if (int rc = sm::launch_status()) return rc;
+    if (n.parts == 1 || !dgamma) return SIGNMUON_OK;
+    sm::launch_rms_norm_sums(n, st);
     return sm::launch_status();
 }
 

@@ -128,6 +128,38 @@ void launch_f8_matmul(const F8Matmul &f, hipStream_t s);
 void launch_f8_sums(const F8Matmul &f, hipStream_t s);
 
 // ---------------------------------------------------------------------------
+// Root-mean-square norm.
+// ---------------------------------------------------------------------------
+struct RmsNorm {
+    const void *x, *residual;  // residual may be null
+    const float *gamma;
+    void *h, *y;               // either may be null
+    uint8_t *q, *q_scale;      // both or neither
+    float *rstd;               // may be null
+    int64_t rows, cols;
+    int64_t pitch, scale_pitch;  // of q: a row's bytes
+    float eps;
+    bool bf16, e5m2;
+};
+void launch_rms_norm(const RmsNorm &n, hipStream_t s);
+
+struct RmsGrad {
+    const void *dy, *dh, *h;  // dh may be null
+    const float *gamma, *rstd;
+    void *dx, *dgamma;        // either may be null
+    float *partial;  // [workers][parts][cols] sums of dy * xh; unused where parts = 1
+    int64_t rows;    // per worker
+    int64_t cols;
+    int32_t workers;
+    int32_t parts;  // blocks of rows per worker, each with a sum of its own
+    bool bf16, grad_bf16;
+};
+int32_t rms_parts(int32_t workers, int64_t rows, int64_t cols);
+void launch_rms_norm_backward(const RmsGrad &n, hipStream_t s);
+// Adds the parts' sums (parts > 1).
+void launch_rms_norm_sums(const RmsGrad &n, hipStream_t s);
+
+// ---------------------------------------------------------------------------
 // Device helpers
 // ---------------------------------------------------------------------------
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -138,6 +170,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef u32x2 u32x2_any __attribute__((aligned(2)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
+constexpr int kWave = 64;
 
 // Blocks go to the 8 XCDs round-robin: each XCD gets a contiguous run of n
 // pieces of work.
@@ -303,5 +337,85 @@ __device__ __forceinline__ void unpack(const Raw<BF16, N> &o, int c, int cols, f
         for (int j = 0; j < N; ++j) v[j] = c + j < cols ? v[j] : 0.0f;
     }
 }
+
+// ---------------------------------------------------------------------------
+// Rows held by teams of lanes
+// ---------------------------------------------------------------------------
+// Sums over a team of TS lanes (a part of a wave, or a whole workgroup).
+template <int TS>
+struct Team {
+    float *lds;  // TS > 64: [2][TS / 64][2]
+    int parity = 0;
+
+    __device__ __forceinline__ void sum2(float &a, float &b) {
+#pragma unroll
+        for (int d = 1; d < (TS < kWave ? TS : kWave); d <<= 1) {
+            a += __shfl_xor(a, d);
+            b += __shfl_xor(b, d);
+        }
+        if constexpr (TS > kWave) {
+            constexpr int W = TS / kWave;
+            float *at = lds + parity * 2 * W;
+            parity ^= 1;  // the next sums use the other half: one barrier each
+            if ((threadIdx.x & (kWave - 1)) == 0) {
+                at[2 * (threadIdx.x / kWave)] = a;
+                at[2 * (threadIdx.x / kWave) + 1] = b;
+            }
+            __syncthreads();
+            a = b = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                a += at[2 * w];
+                b += at[2 * w + 1];
+            }
+        }
+    }
+    __device__ __forceinline__ float sum(float a) {
+        float b = 0.0f;
+        sum2(a, b);
+        return a;
+    }
+};
+
+__device__ __forceinline__ int left(int cols, int c) {  // values of a chunk at column c
+    return cols - c < 0 ? 0 : cols - c < 8 ? cols - c : 8;
+}
+
+// ---------------------------------------------------------------------------
+// Quantisation of a block of 128 values
+// ---------------------------------------------------------------------------
+// e + 127 of a block from the bits of its largest finite size.
+template <bool E5M2>
+__device__ __forceinline__ int scale_byte(uint32_t top) {
+    // top = 1.m * 2^(field - 127) = f 2^p with p = field - 126; f > 0.875 where 1.m > 1.75
+    const int e = (int)(top >> 23) - 126 - (E5M2 ? 16 : 9) + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return top == 0 ? kF8Zero : (e < -127 ? 0 : e + 127);
+}
+
+// 2^(127 - byte): what values are multiplied by.
+__device__ __forceinline__ float inverse_scale(int byte) {
+    // byte <= 247 (the largest fp32 value), so the exponent field 254 - byte is positive
+    return __uint_as_float((uint32_t)(254 - byte) << 23);
+}
+
+template <bool E5M2>
+__device__ __forceinline__ uint32_t to_f8x4(float a, float b, float c, float d) {
+    int r = 0;
+    if (E5M2) {
+        r = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, r, false);
+        r = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, r, true);
+    } else {
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, r, false);
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+    }
+    return (uint32_t)r;
+}
+
+__device__ __forceinline__ uint32_t finite_size(float v) {  // bits of |v|, 0 for NaN and infinities
+    const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
+    return b >= 0x7f800000u ? 0u : b;
+}
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 }  // namespace sm

@@ -25,48 +25,6 @@
 namespace sm {
 namespace {
 
-constexpr int kWave = 64;
-
-// Sums over a team of TS lanes (a part of a wave, or a whole workgroup).
-template <int TS>
-struct Team {
-    float *lds;  // TS > 64: [2][TS / 64][2]
-    int parity = 0;
-
-    __device__ __forceinline__ void sum2(float &a, float &b) {
-#pragma unroll
-        for (int d = 1; d < (TS < kWave ? TS : kWave); d <<= 1) {
-            a += __shfl_xor(a, d);
-            b += __shfl_xor(b, d);
-        }
-        if constexpr (TS > kWave) {
-            constexpr int W = TS / kWave;
-            float *at = lds + parity * 2 * W;
-            parity ^= 1;  // the next sums use the other half: one barrier each
-            if ((threadIdx.x & (kWave - 1)) == 0) {
-                at[2 * (threadIdx.x / kWave)] = a;
-                at[2 * (threadIdx.x / kWave) + 1] = b;
-            }
-            __syncthreads();
-            a = b = 0.0f;
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                a += at[2 * w];
-                b += at[2 * w + 1];
-            }
-        }
-    }
-    __device__ __forceinline__ float sum(float a) {
-        float b = 0.0f;
-        sum2(a, b);
-        return a;
-    }
-};
-
-__device__ __forceinline__ int left(int cols, int c) {  // values of a chunk at column c
-    return cols - c < 0 ? 0 : cols - c < 8 ? cols - c : 8;
-}
-
 // One team per row, `teams` of the grid taking every teams-th row.
 template <bool BF16, int TS, int NIT, int THREADS>
 __global__ __launch_bounds__(THREADS) void norm_kernel(Norm n) {
