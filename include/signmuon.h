@@ -309,8 +309,8 @@ size_t signmuon_workspace_bytes(const signmuon_matrix *mats, int32_t n_mats,
  * gradient). The entry points below are the operators of a transformer's
  * training pass whose weight gradients go into such a stack as they are: the
  * embedding lookup and its gradient, layer norm and root-mean-square norm and
- * their gradients, and linear layers in 8-bit floating point (quantisation and
- * products). The workers'
+ * their gradients, linear layers in 8-bit floating point (quantisation and
+ * products), and the norm and clipping of the gradients themselves. The workers'
  * batches sit side by side: worker m's tokens at offset m * tokens. They
  * follow the conventions at the head of this file (device pointers, 16-byte
  * aligned bases, every argument checked before anything is enqueued, kernel
@@ -501,6 +501,42 @@ int signmuon_rms_norm_backward(const void *dy, const void *dh, const void *h, si
 /* Device workspace of signmuon_rms_norm_backward in bytes (0 on invalid
  * arguments). */
 size_t signmuon_rms_norm_workspace_bytes(int32_t workers, int64_t rows, int64_t cols);
+
+/* One weight's gradients, of every worker. */
+typedef struct {
+    const void *grad;  /* [Mw][n] of dtype: signmuon_matrix.grad, for one */
+    void *out;         /* [Mw][n] of dtype: the clipped gradients; it may be grad (in place).
+                          Ignored by signmuon_grad_norm */
+    int64_t n;         /* entries of one worker, 1 to 2^31 - 1 */
+    int32_t dtype;     /* signmuon_dtype */
+} signmuon_gradient;
+
+/*
+ * signmuon_grad_norm -- norms[m] = sqrt(sum of g^2 over all entries g of worker m
+ * in all n_grads tensors), fp32 [workers]: the global norm of each worker's
+ * gradients (workers = 1: of all entries). Squares are added in fp64, in a fixed
+ * order. The tensors may be of different types. n_grads is at most
+ * SIGNMUON_MAX_MATRICES, workers 255. workspace:
+ * signmuon_grad_norm_workspace_bytes(grads, n_grads, workers) bytes.
+ *
+ * signmuon_clip_grads -- the norms as above, and
+ *   out = grad * min(1, max_norm / norms[m])
+ * for every entry of worker m, with the factor in fp32 and each product rounded
+ * once. max_norm is positive and finite. A norm that is NaN makes every entry of
+ * its worker NaN; an infinite one makes its finite entries 0 and the others NaN:
+ * a worker that fails does not touch another's gradients. Where a worker's norm is
+ * at most max_norm, its gradients keep their bits (in place: they are not
+ * touched). An out must not overlap any other buffer of the call than its own
+ * grad.
+ */
+int signmuon_grad_norm(const signmuon_gradient *grads, int32_t n_grads, int32_t workers, float *norms,
+                       void *workspace, size_t workspace_bytes, signmuon_stream stream);
+int signmuon_clip_grads(const signmuon_gradient *grads, int32_t n_grads, int32_t workers, float max_norm,
+                        float *norms, void *workspace, size_t workspace_bytes, signmuon_stream stream);
+
+/* Device workspace of both in bytes (0 on invalid arguments; only the sizes are
+ * read). */
+size_t signmuon_grad_norm_workspace_bytes(const signmuon_gradient *grads, int32_t n_grads, int32_t workers);
 
 /* Text for a status code; for SIGNMUON_EHIP it names the HIP error of the
  * calling thread's last failure. Never NULL. */

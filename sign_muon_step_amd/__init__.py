@@ -51,6 +51,11 @@ class _Params(ctypes.Structure):
                 ("power_iters", ctypes.c_int32), ("payload", ctypes.c_int32)]
 
 
+class _Gradient(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
+
+
 class _Trace(ctypes.Structure):
     _fields_ = [("events", ctypes.POINTER(ctypes.c_void_p)), ("capacity", ctypes.c_int32),
                 ("kinds", ctypes.POINTER(ctypes.c_int32)), ("launches", ctypes.c_int32)]
@@ -93,7 +98,7 @@ def library() -> ctypes.CDLL:
     lib.signmuon_sign_int8.argtypes = [vp, ctypes.c_int, i64, i32, vp, vp]
     lib.signmuon_vote_update_int8.restype = ctypes.c_int
     lib.signmuon_vote_update_int8.argtypes = [vp, i32, i64, vp, ctypes.c_float, vp, vp]
-    f32, size = ctypes.c_float, ctypes.c_size_t
+    f32, size, gp = ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(_Gradient)
     for name, result, args in (
             ("embedding", i32, [vp, i32, vp, i32, i64, i64, i64, f32, vp, i32, vp]),
             ("embedding_backward", i32, [vp, i32, vp, i32, i32, i64, i64, i64, f32, vp, i32, i32, vp, size, vp]),
@@ -108,7 +113,10 @@ def library() -> ctypes.CDLL:
             ("f8_matmul_workspace_bytes", size, [i32, i64, i64, i64]),
             ("rms_norm", i32, [vp, vp, i32, i64, i64, vp, f32, vp, vp, i32, vp, vp, vp, vp]),
             ("rms_norm_backward", i32, [vp, vp, vp, i32, i32, i64, i64, vp, vp, vp, vp, i32, vp, size, vp]),
-            ("rms_norm_workspace_bytes", size, [i32, i64, i64])):
+            ("rms_norm_workspace_bytes", size, [i32, i64, i64]),
+            ("grad_norm", i32, [gp, i32, i32, vp, vp, size, vp]),
+            ("clip_grads", i32, [gp, i32, i32, f32, vp, vp, size, vp]),
+            ("grad_norm_workspace_bytes", size, [gp, i32, i32])):
         fn = getattr(lib, "signmuon_" + name)
         fn.restype, fn.argtypes = result, args
     lib.signmuon_packed_words.restype = ctypes.c_size_t
@@ -688,3 +696,59 @@ def signmuon_rms_norm_backward(dy: torch.Tensor, dh: Optional[torch.Tensor], h: 
             _operand(rstd, "rstd", _FP32, h.shape[:-1]), _optional(dx, "dx", dtype, h.shape),
             _optional(dgamma, "dgamma", _ACT, shape), _ACT[grad], *_space(workspace))
     _on(stream, library().signmuon_rms_norm_backward, args, dy, dh, h, gamma, rstd, dx, dgamma, workspace)
+
+
+class Gradients:
+    """The gradients of all weights, checked and marshalled once for repeated
+    calls of signmuon_grad_norm and signmuon_clip_grads on the same buffers: each
+    tensor is [Mw][...] (Matrix.grad), float32 or bfloat16. outs receives the
+    clipped gradients, tensor by tensor (None: in place); each is of its
+    gradient's type and shape, and overlaps no other buffer."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None):
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if not self.grads or len(self.outs) != len(self.grads):
+            raise ValueError(f"{len(self.grads)} gradients and {len(self.outs)} outs")
+        self.workers = self.grads[0].shape[0] if self.grads[0].dim() else 0
+        self.n = len(self.grads)
+        self.arr = (_Gradient * self.n)()
+        device, spans = self.grads[0].device, []
+        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            if g.dim() < 1 or g.shape[0] != self.workers or not g.numel():
+                raise ValueError(f"grads[{i}]: shape {tuple(g.shape)}, expected [{self.workers}][...] and entries")
+            at = _operand(g, f"grads[{i}]", _ACT, g.shape)
+            to = _operand(o, f"outs[{i}]", (g.dtype,), g.shape)
+            if g.device != device or o.device != device:
+                raise ValueError(f"gradients on {device} and on {o.device if g.device == device else g.device}")
+            size = g.numel() * g.element_size()
+            spans += [(at, at + size, True)] if at == to else [(at, at + size, False), (to, to + size, True)]
+            self.arr[i] = _Gradient(at, to, g.numel() // self.workers, _ACT[g.dtype])
+        # a gradient may be read twice; what is written overlaps nothing
+        end, written = 0, False
+        for a, b, out in sorted(spans):
+            if a < end and (out or written):
+                raise ValueError("a buffer that is written overlaps another one")
+            end, written = (b, out) if b > end else (end, written)
+
+    def __len__(self) -> int:
+        return self.n
+
+
+def signmuon_grad_norm_workspace_bytes(grads: Gradients) -> int:
+    return int(library().signmuon_grad_norm_workspace_bytes(grads.arr, grads.n, grads.workers))
+
+
+def signmuon_grad_norm(grads: Gradients, norms: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """norms [Mw] (fp32): the 2-norm of each worker's gradients over all weights."""
+    args = (grads.arr, grads.n, grads.workers, _operand(norms, "norms", _FP32, (grads.workers,)), *_space(workspace))
+    _on(stream, library().signmuon_grad_norm, args, grads.grads[0], norms, workspace)
+
+
+def signmuon_clip_grads(grads: Gradients, max_norm: float, norms: torch.Tensor, workspace: torch.Tensor,
+                        stream=None) -> None:
+    """norms as signmuon_grad_norm, and each worker's gradients times
+    min(1, max_norm / its norm)."""
+    args = (grads.arr, grads.n, grads.workers, max_norm, _operand(norms, "norms", _FP32, (grads.workers,)),
+            *_space(workspace))
+    _on(stream, library().signmuon_clip_grads, args, grads.grads[0], norms, workspace)

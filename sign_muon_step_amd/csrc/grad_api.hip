@@ -77,6 +77,84 @@ size_t rms_workspace(int32_t workers, int64_t rows, int64_t cols) {
 }
 
 // ---------------------------------------------------------------------------
+// Gradient norms and clipping
+// ---------------------------------------------------------------------------
+struct ClipPlan {
+    int64_t units;  // of a worker
+    size_t factors, total;
+};
+
+inline int64_t clip_units(int64_t n) { return (n + sm::kClipUnit - 1) / sm::kClipUnit; }
+
+// The sizes alone, then what a call reads and writes.
+int check_gradients(const signmuon_gradient *grads, int32_t n_grads, int32_t workers, ClipPlan &p) {
+    if (!grads || n_grads < 1 || workers < 1) return SIGNMUON_EINVAL;
+    if (n_grads > SIGNMUON_MAX_MATRICES || workers > kMaxWorkers) return SIGNMUON_ERANGE;
+    p.units = 0;
+    for (int32_t i = 0; i < n_grads; ++i) {
+        if (grads[i].n < 1) return SIGNMUON_EINVAL;
+        if (grads[i].n > kMaxN) return SIGNMUON_ERANGE;
+        p.units += clip_units(grads[i].n);
+    }
+    p.factors = align_up((size_t)(p.units * workers) * sizeof(double));
+    p.total = p.factors + (size_t)workers * sizeof(float);
+    return SIGNMUON_OK;
+}
+
+// The norms of every worker, and, where `most` is given, what is clipped by them.
+int run_gradients(const signmuon_gradient *grads, int32_t n_grads, int32_t workers, bool clip, float most,
+                  float *norms, void *workspace, size_t workspace_bytes, hipStream_t st) {
+    ClipPlan p{};
+    if (int rc = check_gradients(grads, n_grads, workers, p)) return rc;
+    if (!norms || (clip && (!std::isfinite(most) || most <= 0.0f))) return SIGNMUON_EINVAL;
+    for (int32_t i = 0; i < n_grads; ++i) {
+        if (!grads[i].grad || (clip && !grads[i].out)) return SIGNMUON_EINVAL;
+        if (!dtype_ok(grads[i].dtype)) return SIGNMUON_EDTYPE;
+        if (!aligned16(grads[i].grad) || (clip && !aligned16(grads[i].out))) return SIGNMUON_EALIGN;
+    }
+    if (!aligned16(norms)) return SIGNMUON_EALIGN;
+    if (int rc = check_workspace(workspace, workspace_bytes, p.total)) return rc;
+    char *ws = static_cast<char *>(workspace);
+    auto batches = [&](auto launch) -> int {
+        int64_t unit = 0;
+        for (int32_t i0 = 0; i0 < n_grads; i0 += sm::kClipTensors) {
+            sm::ClipBatch b{};
+            b.partial = reinterpret_cast<double *>(ws);
+            b.factors = reinterpret_cast<const float *>(ws + p.factors);
+            b.units = p.units;
+            b.unit0 = unit;
+            b.workers = workers;
+            int64_t here = 0;
+            for (int32_t i = i0; i < n_grads && i < i0 + sm::kClipTensors; ++i) {
+                const int t = b.tensors++;
+                b.grad[t] = grads[i].grad;
+                b.out[t] = grads[i].out;
+                b.n[t] = grads[i].n;
+                b.first[t] = (int32_t)here;
+                b.bf16[t] = grads[i].dtype == SIGNMUON_BF16;
+                here += clip_units(grads[i].n);
+            }
+            b.batch_units = (int32_t)here;
+            unit += here;
+            launch(b, st);
+            if (int rc = sm::launch_status()) return rc;
+        }
+        return SIGNMUON_OK;
+    };
+    if (int rc = batches(sm::launch_clip_norm)) return rc;
+    sm::ClipFinish f{};
+    f.partial = reinterpret_cast<const double *>(ws);
+    f.norms = norms;
+    f.factors = reinterpret_cast<float *>(ws + p.factors);
+    f.units = p.units;
+    f.most = clip ? most : 1.0f;
+    f.workers = workers;
+    sm::launch_clip_finish(f, st);
+    if (int rc = sm::launch_status()) return rc;
+    return clip ? batches(sm::launch_clip_scale) : SIGNMUON_OK;
+}
+
+// ---------------------------------------------------------------------------
 // 8-bit floating point
 // ---------------------------------------------------------------------------
 constexpr int64_t kMaxK = (int64_t)1 << 22;     // a tile's rows of an operand lie within 2^31 bytes
@@ -397,6 +475,23 @@ int signmuon_rms_norm_backward(const void *dy, const void *dh, const void *h, si
     if (n.parts == 1 || !dgamma) return SIGNMUON_OK;
     sm::launch_rms_norm_sums(n, st);
     return sm::launch_status();
+}
+
+size_t signmuon_grad_norm_workspace_bytes(const signmuon_gradient *grads, int32_t n_grads, int32_t workers) {
+    ClipPlan p{};
+    return check_gradients(grads, n_grads, workers, p) == SIGNMUON_OK ? p.total : 0;
+}
+
+int signmuon_grad_norm(const signmuon_gradient *grads, int32_t n_grads, int32_t workers, float *norms,
+                       void *workspace, size_t workspace_bytes, signmuon_stream stream) {
+    return run_gradients(grads, n_grads, workers, false, 0.0f, norms, workspace, workspace_bytes,
+                         static_cast<hipStream_t>(stream));
+}
+
+int signmuon_clip_grads(const signmuon_gradient *grads, int32_t n_grads, int32_t workers, float max_norm,
+                        float *norms, void *workspace, size_t workspace_bytes, signmuon_stream stream) {
+    return run_gradients(grads, n_grads, workers, true, max_norm, norms, workspace, workspace_bytes,
+                         static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

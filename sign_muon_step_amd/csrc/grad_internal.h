@@ -160,6 +160,36 @@ void launch_rms_norm_backward(const RmsGrad &n, hipStream_t s);
 void launch_rms_norm_sums(const RmsGrad &n, hipStream_t s);
 
 // ---------------------------------------------------------------------------
+// Gradient norms and clipping.
+// ---------------------------------------------------------------------------
+constexpr int kClipUnit = 16384;   // entries of a tensor and worker that a workgroup takes
+constexpr int kClipTensors = 96;   // of one launch: its descriptors are the kernel's argument
+
+struct ClipBatch {
+    const void *grad[kClipTensors];  // [workers][n]
+    void *out[kClipTensors];
+    int64_t n[kClipTensors];
+    int32_t first[kClipTensors];     // unit of the batch that the tensor begins with
+    bool bf16[kClipTensors];
+    double *partial;                 // [workers][units]
+    const float *factors;            // [workers]
+    int64_t units;                   // of a worker, all batches
+    int64_t unit0;                   // that this batch begins with
+    int32_t batch_units, tensors, workers;
+};
+void launch_clip_norm(const ClipBatch &b, hipStream_t s);
+void launch_clip_scale(const ClipBatch &b, hipStream_t s);
+
+struct ClipFinish {
+    const double *partial;
+    float *norms, *factors;  // [workers]
+    int64_t units;
+    float most;
+    int32_t workers;
+};
+void launch_clip_finish(const ClipFinish &f, hipStream_t s);
+
+// ---------------------------------------------------------------------------
 // Device helpers
 // ---------------------------------------------------------------------------
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));

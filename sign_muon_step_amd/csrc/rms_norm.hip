@@ -67,7 +67,6 @@ __global__ __launch_bounds__(THREADS) void rms_kernel(RmsNorm n) {
     Team<TS> team{lds};
     const int tl = threadIdx.x % TS, cols = (int)n.cols;
     const int64_t teams = (int64_t)gridDim.x * (THREADS / TS);
-    const float inv = 1.0f / (float)n.cols;
     float g[NIT][8];
 #pragma unroll
     for (int i = 0; i < NIT; ++i) {
@@ -99,7 +98,7 @@ __global__ __launch_bounds__(THREADS) void rms_kernel(RmsNorm n) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) square = fmaf(v[i][j], v[i][j], square);
         }
-        const float rstd = 1.0f / sqrtf(team.sum(square) * inv + n.eps);
+        const float rstd = 1.0f / sqrtf(team.sum(square) / (float)n.cols + n.eps);
         // behind the sum every lane has what it reads of the row: h may be x or the residual
 #pragma unroll
         for (int i = 0; i < NIT; ++i) {
@@ -121,7 +120,6 @@ template <bool BF16, int F8>
 __global__ __launch_bounds__(1024) void rms_long_kernel(RmsNorm n) {
     __shared__ float lds[64];
     Team<1024> team{lds};
-    const float inv = 1.0f / (float)n.cols;
     auto sum_at = [&](int64_t row, int64_t c, int have, float(&v)[8]) {
         load_n<BF16>(n.x, row * n.cols + c, have, v);
         if (!n.residual) return;
@@ -140,7 +138,7 @@ __global__ __launch_bounds__(1024) void rms_long_kernel(RmsNorm n) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) square = fmaf(v[j], v[j], square);
         }
-        const float rstd = 1.0f / sqrtf(team.sum(square) * inv + n.eps);
+        const float rstd = 1.0f / sqrtf(team.sum(square) / (float)n.cols + n.eps);
         // whole waves, so that all lanes of a block take part in its largest size
         for (int64_t c = threadIdx.x * 8; c - (threadIdx.x % kWave) * 8 < n.cols; c += 8192) {
             const int have = left(n.cols, c);

@@ -98,3 +98,77 @@ def test_rms_norm_binding_refuses_other_tensors():
         back(y, None, x, gamma, s, x, torch.zeros(1, 6).half(), None)
     with pytest.raises(ValueError, match="GPU memory"):
         back(y, None, x, gamma, s, y, None, None)
+
+
+# ---------------------------------------------------------------------------
+# Gradient norms and clipping
+# ---------------------------------------------------------------------------
+def entry(grad=A, out=A, n=10, dtype=0):
+    return sm._Gradient(grad, out, n, dtype)
+
+
+def test_clip_arguments(lib):
+    names = "grads n_grads workers max_norm norms workspace workspace_bytes stream".split()
+
+    def array(*entries):
+        return (sm._Gradient * len(entries))(*entries)
+
+    good = [array(entry(), entry(n=100000, dtype=1)), 2, 3, 1.0, A, *WS, None]
+    need = lib.signmuon_grad_norm_workspace_bytes(good[0], 2, 3)
+    assert need >= 3 * (1 + 7) * 8 + 3 * 4
+    for change, status in [(dict(grads=None), EINVAL), (dict(n_grads=0), EINVAL), (dict(workers=0), EINVAL),
+                           (dict(norms=None), EINVAL), (dict(max_norm=0.0), EINVAL), (dict(max_norm=-1.0), EINVAL),
+                           (dict(max_norm=float("nan")), EINVAL), (dict(max_norm=float("inf")), EINVAL),
+                           (dict(workers=256), ERANGE), (dict(n_grads=4097), ERANGE),
+                           (dict(grads=array(entry(n=0), entry())), EINVAL),
+                           (dict(grads=array(entry(), entry(n=1 << 31))), ERANGE),
+                           (dict(grads=array(entry(grad=None), entry())), EINVAL),
+                           (dict(grads=array(entry(out=None), entry())), EINVAL),
+                           (dict(grads=array(entry(), entry(dtype=2))), EDTYPE),
+                           (dict(grads=array(entry(), entry(grad=A + 4))), EALIGN),
+                           (dict(grads=array(entry(), entry(out=A + 2))), EALIGN),
+                           (dict(norms=A + 4), EALIGN), (dict(workspace=None), EWORKSPACE),
+                           (dict(workspace_bytes=need - 1), EWORKSPACE), (dict(workspace=WS[0] + 8), EALIGN)]:
+        assert calls_with(lib.signmuon_clip_grads, names, good, **change) == status, change
+    names.remove("max_norm")
+    del good[3]
+    for change, status in [(dict(grads=None), EINVAL), (dict(norms=None), EINVAL), (dict(workers=-1), EINVAL),
+                           (dict(workspace_bytes=need - 1), EWORKSPACE),
+                           (dict(grads=array(entry(out=None), entry(dtype=-1))), EDTYPE),
+                           (dict(grads=array(entry(out=None, grad=A + 8), entry())), EALIGN)]:
+        assert calls_with(lib.signmuon_grad_norm, names, good, **change) == status, change
+
+
+def test_gradients_refuses_other_tensors():
+    a, b = torch.zeros(2, 6), torch.zeros(2, 3, 5)
+    assert len(sm.Gradients([a, b])) == 2 and sm.Gradients([a, b]).workers == 2
+    assert sm.signmuon_grad_norm_workspace_bytes(sm.Gradients([a, b])) > 0
+    for grads, outs, error, match in [([], None, ValueError, "0 gradients"), ([a, b], [a], ValueError, "1 outs"),
+                                      ([a, b[:1]], None, ValueError, r"grads\[1\]"),
+                                      ([a.half()], None, TypeError, r"grads\[0\]"),
+                                      ([torch.zeros(6, 2).t()], None, ValueError, "contiguous"),
+                                      ([torch.zeros(2, 0)], None, ValueError, "entries"),
+                                      ([torch.zeros(())], None, ValueError, "entries"),
+                                      ([a], [a.bfloat16()], TypeError, r"outs\[0\]"),
+                                      ([a], [torch.zeros(2, 5)], ValueError, r"outs\[0\]"),
+                                      ([a, a], None, ValueError, "overlaps"),
+                                      ([a, a], [torch.zeros(2, 6), a], ValueError, "overlaps"),
+                                      ([a, b], [torch.zeros(2, 6), a.new_zeros(2, 3, 5).copy_(b)], None, "")]:
+        if error is None:
+            sm.Gradients(grads, outs)
+        else:
+            with pytest.raises(error, match=match):
+                sm.Gradients(grads, outs)
+    flat = torch.zeros(100)
+    with pytest.raises(ValueError, match="overlaps"):
+        sm.Gradients([a, torch.zeros(2, 20)], [flat[:12].view(2, 6), flat[8:48].view(2, 20)])
+    sm.Gradients([a, a], [torch.zeros(2, 6), torch.zeros(2, 6)])  # read twice, written apart
+    g, ws = sm.Gradients([a, b]), torch.zeros(256, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="norms"):
+        sm.signmuon_grad_norm(g, torch.zeros(3), ws)
+    with pytest.raises(TypeError, match="norms"):
+        sm.signmuon_clip_grads(g, 1.0, torch.zeros(2).double(), ws)
+    with pytest.raises(ValueError, match="GPU memory"):
+        sm.signmuon_clip_grads(g, 1.0, torch.zeros(2), ws)
+    with pytest.raises(ValueError, match="GPU memory"):
+        sm.signmuon_grad_norm(g, torch.zeros(2), ws)
