@@ -310,7 +310,8 @@ size_t signmuon_workspace_bytes(const signmuon_matrix *mats, int32_t n_mats,
  * training pass whose weight gradients go into such a stack as they are: the
  * embedding lookup and its gradient, layer norm and root-mean-square norm and
  * their gradients, linear layers in 8-bit floating point (quantisation and
- * products), and the norm and clipping of the gradients themselves. The workers'
+ * products), the loss of an output layer and its gradients, and the norm and
+ * clipping of the gradients themselves. The workers'
  * batches sit side by side: worker m's tokens at offset m * tokens. They
  * follow the conventions at the head of this file (device pointers, 16-byte
  * aligned bases, every argument checked before anything is enqueued, kernel
@@ -501,6 +502,63 @@ int signmuon_rms_norm_backward(const void *dy, const void *dh, const void *h, si
 /* Device workspace of signmuon_rms_norm_backward in bytes (0 on invalid
  * arguments). */
 size_t signmuon_rms_norm_workspace_bytes(int32_t workers, int64_t rows, int64_t cols);
+
+/*
+ * signmuon_linear_cross_entropy -- softmax cross entropy of an output layer, without
+ * keeping its logits l[t][v] = scale * sum over c of x[t][c] * w[v][c]:
+ *   lse[t] = log(sum over v of exp(l[t][v])),  loss[t] = lse[t] - l[t][targets[t]]
+ * x is [tokens][cols] of x_dtype, w [vocab][cols] of w_dtype (the output layer's
+ * weight, or the embedding's table where they share it), targets [tokens]; loss and
+ * lse are [tokens] fp32, and either may be NULL, not both. A target below 0 or at
+ * least vocab (padding) has the loss 0. Logits are summed with fp32's accuracy,
+ * BF16 and F32 operands alike (F32 ones at a third to a sixth of the rate). tokens
+ * is the count over all workers. workspace:
+ * signmuon_linear_cross_entropy_workspace_bytes(tokens, vocab, cols, x_dtype, w_dtype)
+ * bytes.
+ */
+int signmuon_linear_cross_entropy(const void *x, signmuon_dtype x_dtype, const void *w, signmuon_dtype w_dtype,
+                                  const void *targets, signmuon_itype target_type, int64_t tokens,
+                                  int64_t vocab, int64_t cols, float scale, float *loss, float *lse,
+                                  void *workspace, size_t workspace_bytes, signmuon_stream stream);
+
+/* Device workspace of signmuon_linear_cross_entropy in bytes (0 on invalid
+ * arguments). */
+size_t signmuon_linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols,
+                                                     signmuon_dtype x_dtype, signmuon_dtype w_dtype);
+
+/*
+ * signmuon_linear_cross_entropy_backward -- its gradients, with
+ *   g[t][v] = scale * dloss[t] * (exp(l[t][v] - lse[t]) - (1 where v = targets[t])),
+ * 0 for a token whose target is padding (whatever x holds there):
+ *   dx[t] = sum over v of g[t][v] * w[v]
+ *   dw[m][v] = sum over worker m's tokens t of g[t][v] * x[t]
+ * The logits are computed again, a piece of the vocabulary at a time. x and dx are
+ * [workers][tokens][cols] of x_dtype; targets, lse (of signmuon_linear_cross_entropy
+ * for the same x, w and scale) and dloss (the gradient of each loss, 1 / count for a
+ * mean) [workers][tokens]; dw is [workers][vocab][cols] of grad_dtype, the layout of
+ * signmuon_matrix.grad. accumulate = 1 adds to what dw holds (the gradient of an
+ * embedding that shares the table, as signmuon_embedding_backward adds to this
+ * one's). Either of dx and dw may be NULL (not wanted), not both. For an F32 result g
+ * and the factors that meet it are held in 16 bits of mantissa (3e-6 of a sum of
+ * random products), for a BF16 result in 8, as its own rounding, and what is below
+ * 2^-126 of them counts as 0; sums are fp32. workspace:
+ * signmuon_linear_cross_entropy_backward_workspace_bytes(workers, tokens, vocab, cols,
+ * x_dtype, w_dtype, grad_dtype) bytes, which does not grow with tokens * vocab past
+ * a piece of 512 MB.
+ */
+int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype, const void *w,
+                                           signmuon_dtype w_dtype, const void *targets,
+                                           signmuon_itype target_type, int32_t workers, int64_t tokens,
+                                           int64_t vocab, int64_t cols, float scale, const float *lse,
+                                           const float *dloss, void *dx, void *dw, signmuon_dtype grad_dtype,
+                                           int32_t accumulate, void *workspace, size_t workspace_bytes,
+                                           signmuon_stream stream);
+
+/* Device workspace of signmuon_linear_cross_entropy_backward in bytes (0 on
+ * invalid arguments). */
+size_t signmuon_linear_cross_entropy_backward_workspace_bytes(int32_t workers, int64_t tokens, int64_t vocab,
+                                                              int64_t cols, signmuon_dtype x_dtype,
+                                                              signmuon_dtype w_dtype, signmuon_dtype grad_dtype);
 
 /* One weight's gradients, of every worker. */
 typedef struct {

@@ -114,6 +114,11 @@ def library() -> ctypes.CDLL:
             ("rms_norm", i32, [vp, vp, i32, i64, i64, vp, f32, vp, vp, i32, vp, vp, vp, vp]),
             ("rms_norm_backward", i32, [vp, vp, vp, i32, i32, i64, i64, vp, vp, vp, vp, i32, vp, size, vp]),
             ("rms_norm_workspace_bytes", size, [i32, i64, i64]),
+            ("linear_cross_entropy", i32, [vp, i32, vp, i32, vp, i32, i64, i64, i64, f32, vp, vp, vp, size, vp]),
+            ("linear_cross_entropy_workspace_bytes", size, [i64, i64, i64, i32, i32]),
+            ("linear_cross_entropy_backward", i32, [vp, i32, vp, i32, vp, i32, i32, i64, i64, i64, f32, vp, vp, vp, vp,
+                                                    i32, i32, vp, size, vp]),
+            ("linear_cross_entropy_backward_workspace_bytes", size, [i32, i64, i64, i64, i32, i32, i32]),
             ("grad_norm", i32, [gp, i32, i32, vp, vp, size, vp]),
             ("clip_grads", i32, [gp, i32, i32, f32, vp, vp, size, vp]),
             ("grad_norm_workspace_bytes", size, [gp, i32, i32])):
@@ -696,6 +701,55 @@ def signmuon_rms_norm_backward(dy: torch.Tensor, dh: Optional[torch.Tensor], h: 
             _operand(rstd, "rstd", _FP32, h.shape[:-1]), _optional(dx, "dx", dtype, h.shape),
             _optional(dgamma, "dgamma", _ACT, shape), _ACT[grad], *_space(workspace))
     _on(stream, library().signmuon_rms_norm_backward, args, dy, dh, h, gamma, rstd, dx, dgamma, workspace)
+
+
+def signmuon_linear_cross_entropy_workspace_bytes(tokens: int, vocab: int, cols: int, x_dtype: torch.dtype,
+                                                  w_dtype: torch.dtype) -> int:
+    return int(library().signmuon_linear_cross_entropy_workspace_bytes(tokens, vocab, cols, _ACT[x_dtype],
+                                                                       _ACT[w_dtype]))
+
+
+def signmuon_linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, scale: float,
+                                  loss: Optional[torch.Tensor], lse: Optional[torch.Tensor], workspace: torch.Tensor,
+                                  stream=None) -> None:
+    """Softmax cross entropy of the logits scale * x w^T, which are not kept: x
+    [..][C], w [V][C], targets of x's other dimensions (outside [0, V): padding,
+    whose loss is 0). loss and lse (fp32, targets' shape): lse is the logarithm of
+    the sum of exponentials, kept for the backward pass; either may be None."""
+    vocab, cols = _rank(w, "w", (2,))
+    args = (_operand(x, "x", _ACT, targets.shape + (cols,)), _ACT[x.dtype], _operand(w, "w", _ACT, w.shape),
+            _ACT[w.dtype], _operand(targets, "targets", _ITYPE, targets.shape), _ITYPE[targets.dtype], targets.numel(),
+            vocab, cols, scale, _optional(loss, "loss", _FP32, targets.shape), _optional(lse, "lse", _FP32, targets.shape),
+            *_space(workspace))
+    _on(stream, library().signmuon_linear_cross_entropy, args, x, w, targets, loss, lse, workspace)
+
+
+def signmuon_linear_cross_entropy_backward_workspace_bytes(workers: int, tokens: int, vocab: int, cols: int,
+                                                           x_dtype: torch.dtype, w_dtype: torch.dtype,
+                                                           grad_dtype: torch.dtype) -> int:
+    return int(library().signmuon_linear_cross_entropy_backward_workspace_bytes(
+        workers, tokens, vocab, cols, _ACT[x_dtype], _ACT[w_dtype], _ACT[grad_dtype]))
+
+
+def signmuon_linear_cross_entropy_backward(x: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, scale: float,
+                                           lse: torch.Tensor, dloss: torch.Tensor, dx: Optional[torch.Tensor],
+                                           dw: Optional[torch.Tensor], workspace: torch.Tensor,
+                                           accumulate: bool = False, stream=None) -> None:
+    """Gradients of the loss: dx [Mw][T][C] (x's type) and dw [Mw][V][C] (the
+    layout of Matrix.grad), one sum for each worker, written or added to dw with
+    accumulate. x [Mw][T][C], targets, lse and dloss (the gradient of each loss)
+    [Mw][T]. Either of dx and dw may be None. The workspace is that of dw's type
+    (of x's where dw is None)."""
+    workers, tokens = _rank(targets, "targets", (2,))
+    vocab, cols = _rank(w, "w", (2,))
+    shape = (workers, tokens)
+    grad = x.dtype if dw is None else dw.dtype
+    args = (_operand(x, "x", _ACT, shape + (cols,)), _ACT[x.dtype], _operand(w, "w", _ACT, w.shape), _ACT[w.dtype],
+            _operand(targets, "targets", _ITYPE, shape), _ITYPE[targets.dtype], workers, tokens, vocab, cols, scale,
+            _operand(lse, "lse", _FP32, shape), _operand(dloss, "dloss", _FP32, shape),
+            _optional(dx, "dx", (x.dtype,), shape + (cols,)), _optional(dw, "dw", _ACT, (workers, vocab, cols)),
+            _ACT[grad], int(bool(accumulate)), *_space(workspace))
+    _on(stream, library().signmuon_linear_cross_entropy_backward, args, x, w, targets, lse, dloss, dx, dw, workspace)
 
 
 class Gradients:

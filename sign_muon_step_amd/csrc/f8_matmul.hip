@@ -42,11 +42,8 @@ namespace sm {
 namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-__device__ __forceinline__ int first_lane(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 __device__ __forceinline__ v8i join(u32x4 lo, u32x4 hi) {
     return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
@@ -54,17 +51,6 @@ __device__ __forceinline__ v8i join(u32x4 lo, u32x4 hi) {
 
 // Nothing behind this runs before v is in its registers.
 __device__ __forceinline__ void hold(const v8i &v) { asm volatile("" : : "v"(v) : "memory"); }
-
-// v is computed here, not behind a later branch.
-__device__ __forceinline__ void pin(f32x16 &v) { asm volatile("" : "+a"(v)); }
-
-// Zeros written straight to where they are kept (one zero for all of them would
-// take sixteen registers of its own).
-__device__ __forceinline__ f32x16 zeros() {
-    float z = 0.0f;
-    asm volatile("" : "+v"(z));
-    return f32x16{z, z, z, z, z, z, z, z, z, z, z, z, z, z, z, z};
-}
 
 // 2^(byte - 127).
 __device__ __forceinline__ float scale_of(int byte) { return __int_as_float(byte << 23); }
@@ -104,44 +90,12 @@ __device__ __forceinline__ void store_out(const F8Matmul &f, int64_t at, int hav
 constexpr int kSliceBytes = kF8Block;  // bytes, i.e. values, of k per row and slice
 constexpr int kStages = 2;
 
-// s_waitcnt with vmcnt = N alone.
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
-}
-
-// Workgroup barrier that does not wait for the loads into LDS still in flight.
-__device__ __forceinline__ void barrier() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
-
-constexpr uint32_t kOutside = 0x80000000u;  // buffer offset beyond every extent: loads zeros
-
-// A load of 16 (or 4) bytes a lane straight into LDS at lds + 16 (4) * lane.
-// Asm without outputs, so that the compiler does not order every LDS read
-// behind the loads in flight; M0 is reserved, and nothing else here reads it.
-__device__ __forceinline__ void load16_lds(uint32_t lds, uint32_t offset, u32x4 buffer) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds), "v"(offset), "s"(buffer)
-                 : "memory");
-}
+// The same of 4 bytes a lane (see load16_lds).
 __device__ __forceinline__ void load4_lds(uint32_t lds, uint32_t offset, u32x4 buffer) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :
                  : "s"(lds), "v"(offset), "s"(buffer)
                  : "memory");
-}
-
-// A raw buffer over `bytes` bytes (below 2^31) from p on.
-__device__ __forceinline__ u32x4 make_buffer(const uint8_t *p, int64_t bytes) {
-    const uint64_t a = reinterpret_cast<uint64_t>(p);
-    return u32x4{(uint32_t)first_lane((int)(uint32_t)a), (uint32_t)first_lane((int)((uint32_t)(a >> 32) & 0xffffu)),
-                 (uint32_t)first_lane((int)bytes), 0x00020000u};
 }
 
 // LDS byte of 16-byte chunk c of a slice's row r.

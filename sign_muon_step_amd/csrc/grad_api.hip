@@ -155,6 +155,132 @@ int run_gradients(const signmuon_gradient *grads, int32_t n_grads, int32_t worke
 }
 
 // ---------------------------------------------------------------------------
+// Softmax cross entropy of an output layer: check_embedding, and
+// ---------------------------------------------------------------------------
+constexpr float kLog2E = 1.44269504088896340736f;
+// What a piece of the vocabulary may take of the workspace where more than one
+// tile's columns do: its maxima and sums, or its g, and the planes of its weights.
+constexpr int64_t kLossForward = (int64_t)128 << 20, kLossBackward = (int64_t)512 << 20;
+
+inline int loss_planes(int dtype) { return dtype == SIGNMUON_F32 ? 3 : 1; }
+
+// Operands that the tiles read where they lie: BF16 rows of whole vectors.
+inline bool loss_direct(int dtype, int64_t cols) { return dtype == SIGNMUON_BF16 && cols % 8 == 0; }
+
+// Entries of the vocabulary in a piece: tiles, at most `most` entries, all pieces
+// about as large.
+int64_t loss_piece(int64_t vocab, int64_t most) {
+    const int64_t tiles = (vocab + sm::kLossTile - 1) / sm::kLossTile;
+    const int64_t each = most / sm::kLossTile > 1 ? most / sm::kLossTile : 1;
+    const int64_t pieces = (tiles + each - 1) / each;
+    return (tiles + pieces - 1) / pieces * sm::kLossTile;
+}
+
+struct LossPlan {
+    int64_t piece, pitch;
+    int32_t splits;               // of dx
+    bool accumulate;              // dx over several pieces in a buffer of its own
+    size_t x, w, partial, state, target, g, dx, sums, total;
+};
+
+LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int w_dtype) {
+    LossPlan p{};
+    p.pitch = sm::loss_pitch(cols);
+    int64_t most = kLossForward * 128 / (8 * tokens);
+    const int64_t w_row = loss_direct(w_dtype, cols) ? 0 : loss_planes(w_dtype) * p.pitch * 2;
+    if (w_row && kLossForward / w_row < most) most = kLossForward / w_row;
+    p.piece = loss_piece(vocab, most);
+    size_t at = 0;
+    auto section = [&](int64_t bytes) {
+        const size_t here = at;
+        at += align_up((size_t)bytes);
+        return here;
+    };
+    p.x = section(loss_direct(x_dtype, cols) ? 0 : loss_planes(x_dtype) * tokens * p.pitch * 2);
+    p.w = section(w_row * p.piece);
+    p.partial = section(tokens * (p.piece / 128) * (int64_t)sizeof(float2));
+    p.state = section(p.piece < vocab ? tokens * (int64_t)sizeof(float2) : 0);
+    p.target = section(tokens * (int64_t)sizeof(float));
+    p.total = at;
+    return p;
+}
+
+LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int w_dtype,
+                        int grad_dtype) {
+    LossPlan p{};
+    const int64_t rows = workers * tokens;
+    p.pitch = sm::loss_pitch(cols);
+    const int64_t planes = x_dtype == SIGNMUON_F32 || grad_dtype == SIGNMUON_F32 ? 2 : 1;
+    int64_t most = kLossBackward / (planes * rows * 2);
+    const int64_t w_row = loss_direct(w_dtype, cols) ? 0 : loss_planes(w_dtype) * p.pitch * 2;
+    if (w_row && kLossBackward / w_row < most) most = kLossBackward / w_row;
+    p.piece = loss_piece(vocab, most);
+    // parts of k until dx has a tile for every compute unit, eight slices at least in each
+    const int64_t tiles = ((rows + sm::kLossTile - 1) / sm::kLossTile) * ((cols + sm::kLossTile - 1) / sm::kLossTile);
+    const int64_t parts = 256 / tiles, slices = p.piece / sm::kLossSlice / 8;
+    p.splits = (int32_t)(parts < slices ? (parts > 1 ? parts : 1) : (slices > 1 ? slices : 1));
+    p.accumulate = p.piece < vocab && x_dtype == SIGNMUON_BF16;
+    size_t at = 0;
+    auto section = [&](int64_t bytes) {
+        const size_t here = at;
+        at += align_up((size_t)bytes);
+        return here;
+    };
+    p.x = section(loss_planes(x_dtype) * rows * p.pitch * 2);
+    p.w = section(w_row * p.piece);
+    p.g = section(planes * rows * p.piece * 2);
+    p.dx = section(p.accumulate ? rows * cols * (int64_t)sizeof(float) : 0);
+    p.sums = section(p.splits > 1 ? p.splits * rows * cols * (int64_t)sizeof(float) : 0);
+    p.total = at;
+    return p;
+}
+
+// The pairs of planes that a product of na by nb planes takes: all whose sizes are
+// above what the last planes leave out.
+void loss_pairs(sm::LossTile &f, int na, int nb) {
+    const int most = na > nb ? na : nb;  // planes i and j count where i + j is below it
+    f.pairs = 0;
+    for (int i = 0; i < na; ++i)
+        for (int j = 0; j < nb && i + j < most; ++j) {
+            f.plane_a[f.pairs] = (uint8_t)i;
+            f.plane_b[f.pairs++] = (uint8_t)j;
+        }
+}
+
+void loss_split(sm::LossTile &f, int32_t splits) {
+    const int64_t slices = f.pairs * ((f.k + sm::kLossSlice - 1) / sm::kLossSlice);
+    f.chunk = (int32_t)((slices + splits - 1) / splits);
+    f.splits = (int32_t)((slices + f.chunk - 1) / f.chunk);
+}
+
+// One operand's planes, in the workspace or where it lies.
+void loss_operand(const uint16_t *(&planes)[sm::kLossPlanes], int n, const void *at, int64_t plane_entries) {
+    for (int i = 0; i < n; ++i) planes[i] = static_cast<const uint16_t *>(at) + i * plane_entries;
+}
+
+int loss_split_planes(const void *in, int dtype, int64_t rows, int64_t cols, int64_t pitch, void *to,
+                      const void *targets, bool targets64, int64_t vocab, hipStream_t st) {
+    sm::LossPlanes f{};
+    f.in = in;
+    f.planes = loss_planes(dtype);
+    for (int i = 0; i < f.planes; ++i) f.out[i] = static_cast<uint16_t *>(to) + i * rows * pitch;
+    f.targets = targets;
+    f.targets64 = targets64;
+    f.rows = rows;
+    f.cols = cols;
+    f.pitch = pitch;
+    f.vocab = vocab;
+    f.bf16 = dtype == SIGNMUON_BF16;
+    sm::launch_loss_planes(f, st);
+    return sm::launch_status();
+}
+
+inline int64_t entry_bytes(int dtype) { return dtype == SIGNMUON_BF16 ? 2 : 4; }
+inline const void *at_entry(const void *p, int64_t i, int dtype) {
+    return static_cast<const char *>(p) + i * entry_bytes(dtype);
+}
+
+// ---------------------------------------------------------------------------
 // 8-bit floating point
 // ---------------------------------------------------------------------------
 constexpr int64_t kMaxK = (int64_t)1 << 22;     // a tile's rows of an operand lie within 2^31 bytes
@@ -492,6 +618,201 @@ int signmuon_clip_grads(const signmuon_gradient *grads, int32_t n_grads, int32_t
                         float *norms, void *workspace, size_t workspace_bytes, signmuon_stream stream) {
     return run_gradients(grads, n_grads, workers, true, max_norm, norms, workspace, workspace_bytes,
                          static_cast<hipStream_t>(stream));
+}
+
+size_t signmuon_linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols,
+                                                     signmuon_dtype x_dtype, signmuon_dtype w_dtype) {
+    if (check_embedding(1, tokens, vocab, cols) != SIGNMUON_OK || !dtype_ok(x_dtype) || !dtype_ok(w_dtype)) return 0;
+    return loss_plan(tokens, vocab, cols, x_dtype, w_dtype).total;
+}
+
+int signmuon_linear_cross_entropy(const void *x, signmuon_dtype x_dtype, const void *w, signmuon_dtype w_dtype,
+                                  const void *targets, signmuon_itype target_type, int64_t tokens,
+                                  int64_t vocab, int64_t cols, float scale, float *loss, float *lse,
+                                  void *workspace, size_t workspace_bytes, signmuon_stream stream) {
+    if (!x || !w || !targets || (!loss && !lse)) return SIGNMUON_EINVAL;
+    if (int rc = check_embedding(1, tokens, vocab, cols)) return rc;
+    if (!std::isfinite(scale)) return SIGNMUON_EINVAL;
+    if ((target_type != SIGNMUON_I32 && target_type != SIGNMUON_I64) || !dtype_ok(x_dtype) || !dtype_ok(w_dtype))
+        return SIGNMUON_EDTYPE;
+    if (!all_aligned(x, w, targets, loss, lse)) return SIGNMUON_EALIGN;
+    const LossPlan p = loss_plan(tokens, vocab, cols, x_dtype, w_dtype);
+    if (int rc = check_workspace(workspace, workspace_bytes, p.total)) return rc;
+    char *ws = static_cast<char *>(workspace);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const bool direct_x = loss_direct(x_dtype, cols), direct_w = loss_direct(w_dtype, cols);
+    const int nx = loss_planes(x_dtype), nw = loss_planes(w_dtype);
+    if (!direct_x)
+        if (int rc = loss_split_planes(x, x_dtype, tokens, cols, p.pitch, ws + p.x, nullptr, false, vocab, st)) return rc;
+    for (int64_t v0 = 0; v0 < vocab; v0 += p.piece) {
+        const int64_t here = vocab - v0 < p.piece ? vocab - v0 : p.piece;
+        const void *rows = at_entry(w, v0 * cols, w_dtype);
+        if (!direct_w)
+            if (int rc = loss_split_planes(rows, w_dtype, here, cols, p.pitch, ws + p.w, nullptr, false, vocab, st))
+                return rc;
+        sm::LossTile f{};
+        loss_operand(f.a, nx, direct_x ? x : ws + p.x, tokens * p.pitch);
+        loss_operand(f.b, nw, direct_w ? rows : ws + p.w, here * p.pitch);
+        f.a_pitch = f.b_pitch = p.pitch * 2;
+        f.m = tokens;
+        f.n = here;
+        f.k = cols;
+        f.batch = 1;
+        loss_pairs(f, nx, nw);
+        loss_split(f, 1);
+        f.targets = targets;
+        f.targets64 = target_type == SIGNMUON_I64;
+        f.partial = reinterpret_cast<float2 *>(ws + p.partial);
+        f.target = reinterpret_cast<float *>(ws + p.target);
+        f.vocab = vocab;
+        f.vocab0 = v0;
+        f.scale = scale;
+        f.factor = scale * kLog2E;
+        sm::launch_loss_logits(f, false, st);
+        if (int rc = sm::launch_status()) return rc;
+        sm::LossJoin j{};
+        j.partial = f.partial;
+        j.state = reinterpret_cast<float2 *>(ws + p.state);
+        j.target = f.target;
+        j.targets = targets;
+        j.targets64 = f.targets64;
+        j.loss = loss;
+        j.lse = lse;
+        j.rows = tokens;
+        j.blocks = (here + 127) / 128;
+        j.vocab = vocab;
+        j.first = v0 == 0;
+        j.last = v0 + here == vocab;
+        sm::launch_loss_join(j, st);
+        if (int rc = sm::launch_status()) return rc;
+    }
+    return SIGNMUON_OK;
+}
+
+size_t signmuon_linear_cross_entropy_backward_workspace_bytes(int32_t workers, int64_t tokens, int64_t vocab,
+                                                              int64_t cols, signmuon_dtype x_dtype,
+                                                              signmuon_dtype w_dtype, signmuon_dtype grad_dtype) {
+    if (check_embedding(workers, tokens, vocab, cols) != SIGNMUON_OK || !dtype_ok(x_dtype) || !dtype_ok(w_dtype) ||
+        !dtype_ok(grad_dtype))
+        return 0;
+    return loss_grad_plan(workers, tokens, vocab, cols, x_dtype, w_dtype, grad_dtype).total;
+}
+
+int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype, const void *w,
+                                           signmuon_dtype w_dtype, const void *targets,
+                                           signmuon_itype target_type, int32_t workers, int64_t tokens,
+                                           int64_t vocab, int64_t cols, float scale, const float *lse,
+                                           const float *dloss, void *dx, void *dw, signmuon_dtype grad_dtype,
+                                           int32_t accumulate, void *workspace, size_t workspace_bytes,
+                                           signmuon_stream stream) {
+    if (!x || !w || !targets || !lse || !dloss || (!dx && !dw)) return SIGNMUON_EINVAL;
+    if (int rc = check_embedding(workers, tokens, vocab, cols)) return rc;
+    if (!std::isfinite(scale) || (accumulate != 0 && accumulate != 1)) return SIGNMUON_EINVAL;
+    if ((target_type != SIGNMUON_I32 && target_type != SIGNMUON_I64) || !dtype_ok(x_dtype) || !dtype_ok(w_dtype) ||
+        !dtype_ok(grad_dtype))
+        return SIGNMUON_EDTYPE;
+    if (!all_aligned(x, w, targets, lse, dloss, dx, dw)) return SIGNMUON_EALIGN;
+    const LossPlan p = loss_grad_plan(workers, tokens, vocab, cols, x_dtype, w_dtype, grad_dtype);
+    if (int rc = check_workspace(workspace, workspace_bytes, p.total)) return rc;
+    char *ws = static_cast<char *>(workspace);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const int64_t rows = workers * tokens;
+    const bool direct_w = loss_direct(w_dtype, cols), targets64 = target_type == SIGNMUON_I64;
+    const bool x32 = x_dtype == SIGNMUON_F32, grad32 = grad_dtype == SIGNMUON_F32;
+    const int nx = loss_planes(x_dtype), nw = loss_planes(w_dtype);
+    uint16_t *const g = reinterpret_cast<uint16_t *>(ws + p.g);
+    if (int rc = loss_split_planes(x, x_dtype, rows, cols, p.pitch, ws + p.x, targets, targets64, vocab, st)) return rc;
+    for (int64_t v0 = 0; v0 < vocab; v0 += p.piece) {
+        const int64_t here = vocab - v0 < p.piece ? vocab - v0 : p.piece;
+        const int64_t g_pitch = (here + sm::kLossTile - 1) / sm::kLossTile * sm::kLossTile;
+        const bool first = v0 == 0, last = v0 + here == vocab;
+        const void *w_rows = at_entry(w, v0 * cols, w_dtype);
+        if (!direct_w)
+            if (int rc = loss_split_planes(w_rows, w_dtype, here, cols, p.pitch, ws + p.w, nullptr, false, vocab, st))
+                return rc;
+        sm::LossTile f{};
+        loss_operand(f.a, nx, ws + p.x, rows * p.pitch);
+        loss_operand(f.b, nw, direct_w ? w_rows : ws + p.w, here * p.pitch);
+        f.a_pitch = f.b_pitch = p.pitch * 2;
+        f.m = rows;
+        f.n = here;
+        f.k = cols;
+        f.batch = 1;
+        loss_pairs(f, nx, nw);
+        loss_split(f, 1);
+        f.targets = targets;
+        f.targets64 = targets64;
+        f.lse = lse;
+        f.dloss = dloss;
+        f.g[0] = g;
+        f.g[1] = (x32 && dx) || (grad32 && dw) ? g + rows * g_pitch : nullptr;
+        f.g_pitch = g_pitch;
+        f.vocab = vocab;
+        f.vocab0 = v0;
+        f.scale = scale;
+        f.factor = scale * kLog2E;
+        sm::launch_loss_logits(f, true, st);
+        if (int rc = sm::launch_status()) return rc;
+        if (dx) {
+            sm::LossTile d{};
+            loss_operand(d.a, 2, g, rows * g_pitch);
+            loss_operand(d.b, nw, f.b[0], here * p.pitch);
+            d.a_pitch = g_pitch * 2;
+            d.b_pitch = p.pitch * 2;
+            d.m = rows;
+            d.n = cols;
+            d.k = here;
+            d.batch = 1;
+            loss_pairs(d, x32 ? 2 : 1, x32 && nw > 1 ? 2 : 1);
+            loss_split(d, p.splits);
+            d.out_batch = rows;
+            // over several pieces the sums so far lie in dx itself, or in fp32 beside it
+            float *const sums = x32 ? static_cast<float *>(dx) : reinterpret_cast<float *>(ws + p.dx);
+            float *const parts = reinterpret_cast<float *>(ws + p.sums);
+            const float *const prev = first ? nullptr : sums;
+            void *const out = last ? dx : sums;
+            const bool out_bf16 = last && !x32;
+            d.prev = d.splits > 1 ? nullptr : prev;
+            d.out = d.splits > 1 ? parts : out;
+            d.out_bf16 = d.splits > 1 ? false : out_bf16;
+            sm::launch_loss_dx(d, st);
+            if (int rc = sm::launch_status()) return rc;
+            if (d.splits > 1) {
+                sm::LossSums u{};
+                u.partial = parts;
+                u.prev = prev;
+                u.out = out;
+                u.total = rows * cols;
+                u.splits = d.splits;
+                u.out_bf16 = out_bf16;
+                sm::launch_loss_sums(u, st);
+                if (int rc = sm::launch_status()) return rc;
+            }
+        }
+        if (dw) {
+            sm::LossTile d{};
+            loss_operand(d.a, 2, g, rows * g_pitch);
+            loss_operand(d.b, nx, ws + p.x, rows * p.pitch);
+            d.a_pitch = g_pitch * 2;
+            d.b_pitch = p.pitch * 2;
+            d.a_batch = tokens * d.a_pitch;
+            d.b_batch = tokens * d.b_pitch;
+            d.m = here;
+            d.n = cols;
+            d.k = tokens;
+            d.batch = workers;
+            loss_pairs(d, grad32 ? 2 : 1, grad32 && nx > 1 ? 2 : 1);
+            loss_split(d, 1);
+            d.out = const_cast<void *>(at_entry(dw, v0 * cols, grad_dtype));
+            d.out_batch = vocab;
+            d.out_bf16 = !grad32;
+            d.prev = accumulate ? d.out : nullptr;
+            d.prev_bf16 = d.out_bf16;
+            sm::launch_loss_dw(d, st);
+            if (int rc = sm::launch_status()) return rc;
+        }
+    }
+    return SIGNMUON_OK;
 }
 
 }  // extern "C"

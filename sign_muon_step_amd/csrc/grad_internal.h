@@ -160,6 +160,75 @@ void launch_rms_norm_backward(const RmsGrad &n, hipStream_t s);
 void launch_rms_norm_sums(const RmsGrad &n, hipStream_t s);
 
 // ---------------------------------------------------------------------------
+// Softmax cross entropy of an output layer.
+// ---------------------------------------------------------------------------
+constexpr int kLossTile = 256;  // rows and columns of a workgroup's tile
+constexpr int kLossSlice = 64;  // k of a slice in LDS
+constexpr int kLossPlanes = 3, kLossPairs = 6;
+inline int64_t loss_pitch(int64_t cols) { return (cols + 7) / 8 * 8; }  // entries of a plane's row
+
+// A matrix as BF16 planes [planes][rows][pitch].
+struct LossPlanes {
+    const void *in;
+    uint16_t *out[kLossPlanes];
+    const void *targets;  // of the rows, or null: rows without a target become zeros
+    int64_t rows, cols, pitch, vocab;
+    int32_t planes;
+    bool bf16, targets64;
+};
+void launch_loss_planes(const LossPlanes &f, hipStream_t s);
+
+// A product a b^T of planes, out [m][n], sums over k and over pairs of planes.
+struct LossTile {
+    const uint16_t *a[kLossPlanes], *b[kLossPlanes];
+    int64_t a_pitch, b_pitch;  // bytes of a row in memory
+    int64_t a_batch, b_batch;  // bytes between batch entries
+    int64_t m, n, k;
+    int32_t batch, pairs;
+    int32_t splits, chunk;     // chunk: slices of a split, of all pairs' slices in a row
+    uint8_t plane_a[kLossPairs], plane_b[kLossPairs];
+    // logits
+    const void *targets;
+    const float *lse, *dloss;
+    float2 *partial;           // [columns of 128][m]: maximum and sum, in units of log 2
+    float *target;             // [m] logit of the target
+    uint16_t *g[2];            // planes [m][g_pitch]; the second may be null
+    int64_t g_pitch;
+    int64_t vocab, vocab0;     // vocab0: the piece's first entry
+    float scale, factor;       // factor: scale / log 2
+    bool targets64;
+    // values
+    const void *prev;          // added; null: nothing
+    void *out;
+    int64_t out_batch;         // rows between batch entries, and between parts of k
+    bool prev_bf16, out_bf16;
+};
+void launch_loss_logits(const LossTile &f, bool grad, hipStream_t s);
+void launch_loss_dx(const LossTile &f, hipStream_t s);
+void launch_loss_dw(const LossTile &f, hipStream_t s);
+
+struct LossJoin {
+    const float2 *partial;
+    float2 *state;  // [rows] between pieces of the vocabulary
+    const float *target;
+    const void *targets;
+    float *loss, *lse;
+    int64_t rows, blocks, vocab;
+    bool first, last, targets64;
+};
+void launch_loss_join(const LossJoin &f, hipStream_t s);
+
+struct LossSums {
+    const float *partial;  // [splits][total]
+    const float *prev;     // added; null: nothing
+    void *out;
+    int64_t total;
+    int32_t splits;
+    bool out_bf16;
+};
+void launch_loss_sums(const LossSums &f, hipStream_t s);
+
+// ---------------------------------------------------------------------------
 // Gradient norms and clipping.
 // ---------------------------------------------------------------------------
 constexpr int kClipUnit = 16384;   // entries of a tensor and worker that a workgroup takes
@@ -447,5 +516,56 @@ __device__ __forceinline__ uint32_t finite_size(float v) {  // bits of |v|, 0 fo
 }
 
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// ---------------------------------------------------------------------------
+// Tiles of matrix products, fed straight into LDS
+// ---------------------------------------------------------------------------
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ int first_lane(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// v is computed here, not behind a later branch.
+__device__ __forceinline__ void pin(f32x16 &v) { asm volatile("" : "+a"(v)); }
+
+// Zeros written straight to where they are kept (one zero for all of them would
+// take sixteen registers of its own).
+__device__ __forceinline__ f32x16 zeros() {
+    float z = 0.0f;
+    asm volatile("" : "+v"(z));
+    return f32x16{z, z, z, z, z, z, z, z, z, z, z, z, z, z, z, z};
+}
+
+// s_waitcnt with vmcnt = N alone.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
+// Workgroup barrier that does not wait for the loads into LDS still in flight.
+__device__ __forceinline__ void barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+constexpr uint32_t kOutside = 0x80000000u;  // buffer offset beyond every extent: loads zeros
+
+// A load of 16 bytes a lane straight into LDS at lds + 16 * lane.
+// Asm without outputs, so that the compiler does not order every LDS read
+// behind the loads in flight; M0 is reserved, and nothing else here reads it.
+__device__ __forceinline__ void load16_lds(uint32_t lds, uint32_t offset, u32x4 buffer) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(offset), "s"(buffer)
+                 : "memory");
+}
+// A raw buffer over `bytes` bytes (below 2^31) from p on.
+__device__ __forceinline__ u32x4 make_buffer(const uint8_t *p, int64_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    return u32x4{(uint32_t)first_lane((int)(uint32_t)a), (uint32_t)first_lane((int)((uint32_t)(a >> 32) & 0xffffu)),
+                 (uint32_t)first_lane((int)bytes), 0x00020000u};
+}
 
 }  // namespace sm

@@ -172,3 +172,73 @@ def test_gradients_refuses_other_tensors():
         sm.signmuon_clip_grads(g, 1.0, torch.zeros(2), ws)
     with pytest.raises(ValueError, match="GPU memory"):
         sm.signmuon_grad_norm(g, torch.zeros(2), ws)
+
+
+# ---------------------------------------------------------------------------
+# Softmax cross entropy of an output layer
+# ---------------------------------------------------------------------------
+SMALL = [(dict(tokens=0), EINVAL), (dict(vocab=0), EINVAL), (dict(cols=-1), EINVAL), (dict(scale=float("nan")), EINVAL),
+         (dict(scale=float("inf")), EINVAL), (dict(x_dtype=2), EDTYPE), (dict(w_dtype=-1), EDTYPE),
+         (dict(target_type=2), EDTYPE), (dict(x=A + 2), EALIGN), (dict(w=A + 8), EALIGN), (dict(targets=A + 4), EALIGN),
+         (dict(workspace=None), EWORKSPACE), (dict(workspace=WS[0] + 8), EALIGN), (dict(tokens=(1 << 25) + 1), ERANGE),
+         (dict(vocab=(1 << 20) + 1), ERANGE), (dict(cols=(1 << 20) + 1), ERANGE), (dict(vocab=1 << 20, cols=2048), ERANGE),
+         (dict(x=None), EINVAL), (dict(w=None), EINVAL), (dict(targets=None), EINVAL)]
+
+
+def test_linear_cross_entropy_arguments(lib):
+    names = ("x x_dtype w w_dtype targets target_type tokens vocab cols scale loss lse workspace workspace_bytes "
+             "stream").split()
+    good = [A, 1, A, 0, A, 1, 10, 1000, 20, 1.0, A, A, *WS, None]
+    size = lib.signmuon_linear_cross_entropy_workspace_bytes
+    need = size(10, 1000, 20, 1, 0)
+    assert need > 0
+    for change, status in SMALL + [(dict(loss=None, lse=None), EINVAL), (dict(loss=A + 4), EALIGN),
+                                   (dict(lse=A + 8), EALIGN), (dict(workspace_bytes=need - 1), EWORKSPACE)]:
+        assert calls_with(lib.signmuon_linear_cross_entropy, names, good, **change) == status, change
+    assert size(0, 10, 10, 0, 0) == size(10, 0, 10, 0, 0) == size(10, 10, 0, 0, 0) == size(10, 10, 10, 2, 0) == 0
+    # the logits of 8192 tokens would take 1.6 GB
+    assert 0 < size(8192, 50257, 768, 1, 1) < 64 << 20
+
+
+def test_linear_cross_entropy_backward_arguments(lib):
+    names = ("x x_dtype w w_dtype targets target_type workers tokens vocab cols scale lse dloss dx dw grad_dtype "
+             "accumulate workspace workspace_bytes stream").split()
+    good = [A, 1, A, 1, A, 0, 2, 10, 1000, 20, 1.0, A, A, A, A, 0, 0, *WS, None]
+    size = lib.signmuon_linear_cross_entropy_backward_workspace_bytes
+    need = size(2, 10, 1000, 20, 1, 1, 0)
+    assert need > 0
+    for change, status in SMALL + [(dict(dx=None, dw=None), EINVAL), (dict(lse=None), EINVAL), (dict(dloss=None), EINVAL),
+                                   (dict(accumulate=2), EINVAL), (dict(grad_dtype=2), EDTYPE), (dict(workers=0), EINVAL),
+                                   (dict(workers=256), ERANGE), (dict(tokens=1 << 25), ERANGE), (dict(lse=A + 4), EALIGN),
+                                   (dict(dloss=A + 8), EALIGN), (dict(dx=A + 2), EALIGN), (dict(dw=A + 2), EALIGN),
+                                   (dict(workspace_bytes=need - 1), EWORKSPACE)]:
+        assert calls_with(lib.signmuon_linear_cross_entropy_backward, names, good, **change) == status, change
+    assert size(0, 10, 10, 10, 0, 0, 0) == size(1, 10, 10, 10, 0, 0, 3) == size(1, 10, 10, 10, 0, 5, 0) == 0
+
+
+def test_linear_cross_entropy_binding_refuses_other_tensors():
+    x, w, ids = torch.zeros(2, 5, 6), torch.zeros(7, 6), torch.zeros(2, 5, dtype=torch.int64)
+    s, ws = torch.zeros(2, 5), torch.zeros(1 << 20, dtype=torch.uint8)
+    call = sm.signmuon_linear_cross_entropy
+    for args, error, match in [((x.half(), w, ids, 1.0, s, s), TypeError, "x: dtype"),
+                               ((x[:, :, :5], w, ids, 1.0, s, s), ValueError, "x: shape"),
+                               ((x, w[0], ids, 1.0, s, s), ValueError, "w: 1 dim"),
+                               ((x, w.double(), ids, 1.0, s, s), TypeError, "w: dtype"),
+                               ((x, w, ids.float(), 1.0, s, s), TypeError, "targets"),
+                               ((x, w, ids[:, :4], 1.0, s, s), ValueError, "x: shape"),
+                               ((x, w, ids, 1.0, s[0], s), ValueError, "loss"),
+                               ((x, w, ids, 1.0, s, s.bfloat16()), TypeError, "lse"),
+                               ((x, torch.zeros(6, 7).t(), ids, 1.0, s, s), ValueError, "contiguous"),
+                               ((x, w, ids, 1.0, s, s), ValueError, "GPU memory")]:
+        with pytest.raises(error, match=match):
+            call(*args, ws)
+    back, dx, dw = sm.signmuon_linear_cross_entropy_backward, torch.zeros(2, 5, 6), torch.zeros(2, 7, 6)
+    for args, error, match in [((x[0], w, ids[0], 1.0, s, s, dx, dw), ValueError, "targets"),
+                               ((x, w, ids, 1.0, s[:1], s, dx, dw), ValueError, "lse"),
+                               ((x, w, ids, 1.0, s, s.double(), dx, dw), TypeError, "dloss"),
+                               ((x, w, ids, 1.0, s, s, dx.bfloat16(), dw), TypeError, "dx"),
+                               ((x, w, ids, 1.0, s, s, dx, dw[:1]), ValueError, "dw"),
+                               ((x, w, ids, 1.0, s, s, dx, dw.half()), TypeError, "dw"),
+                               ((x, w, ids, 1.0, s, s, dx, dw), ValueError, "GPU memory")]:
+        with pytest.raises(error, match=match):
+            back(*args, ws)
