@@ -242,8 +242,9 @@ void loss_pairs(sm::LossTile &f, int na, int nb) {
     f.pairs = 0;
     for (int i = 0; i < na; ++i)
         for (int j = 0; j < nb && i + j < most; ++j) {
-            f.plane_a[f.pairs] = (uint8_t)i;
-            f.plane_b[f.pairs++] = (uint8_t)j;
+            f.order_a |= (uint32_t)i << (2 * f.pairs);
+            f.order_b |= (uint32_t)j << (2 * f.pairs);
+            ++f.pairs;
         }
 }
 

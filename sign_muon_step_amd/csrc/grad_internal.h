@@ -186,7 +186,7 @@ struct LossTile {
     int64_t m, n, k;
     int32_t batch, pairs;
     int32_t splits, chunk;     // chunk: slices of a split, of all pairs' slices in a row
-    uint8_t plane_a[kLossPairs], plane_b[kLossPairs];
+    uint32_t order_a, order_b;  // the planes of pair i in bits 2 i on
     // logits
     const void *targets;
     const float *lse, *dloss;

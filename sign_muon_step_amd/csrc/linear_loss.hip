@@ -118,8 +118,8 @@ struct Loader {
     u32x4 buffer[2];
     uint32_t at[2], past[2], step[2];  // of the lane's first load, where the slice's k ends; between loads
     int chunk[2];
-    int v, slice, end;       // the tile, the next slice to load and the end of its slices
-    int per;                 // slices of a pair of planes
+    int v, slice, end;  // the tile, the next slice to load and the end of its slices
+    int per, ks, pair;  // slices of a pair of planes; the slice's place in them
     Tile t;
 
     __device__ __forceinline__ void start(const LossTile &f, int v_, int total, int wave, int lane) {
@@ -138,12 +138,16 @@ struct Loader {
         t = tile_at<TILE>(f, there ? v : 0, total);
         slice = t.split * f.chunk;
         end = slice + f.chunk < f.pairs * per ? slice + f.chunk : f.pairs * per;
+        pair = first_lane(slice / per);
+        ks = slice - pair * per;
         place(f, there);
     }
+    // A slice's buffer, from the slice's k on, and where its k ends.
     template <bool TRANS>
-    __device__ __forceinline__ void operand(int o, const uint16_t *plane, int64_t pitch, int64_t first, int64_t rows,
-                                            int64_t k, int ks, bool there) {
-        const uint8_t *p = reinterpret_cast<const uint8_t *>(plane);
+    __device__ __forceinline__ void operand(int o, const uint16_t *const (&planes)[kLossPlanes], uint32_t order,
+                                            int64_t batch, int64_t pitch, int64_t first, int64_t rows, int64_t k,
+                                            bool there) {
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(planes[order >> (2 * pair) & 3]) + batch;
         const int64_t k0 = (int64_t)ks * kSlice;
         if (TRANS) {
             const int64_t have = k - k0 < kSlice ? k - k0 : kSlice;
@@ -156,11 +160,25 @@ struct Loader {
         }
     }
     __device__ __forceinline__ void place(const LossTile &f, bool there) {
-        const int pair = first_lane(slice / per), ks = slice - pair * per;
-        const char *pa = reinterpret_cast<const char *>(f.a[f.plane_a[pair]]) + t.batch * f.a_batch;
-        const char *pb = reinterpret_cast<const char *>(f.b[f.plane_b[pair]]) + t.batch * f.b_batch;
-        operand<TA>(0, reinterpret_cast<const uint16_t *>(pa), f.a_pitch, t.row0, f.m, f.k, ks, there);
-        operand<TB>(1, reinterpret_cast<const uint16_t *>(pb), f.b_pitch, t.col0, f.n, f.k, ks, there);
+        operand<TA>(0, f.a, f.order_a, t.batch * f.a_batch, f.a_pitch, t.row0, f.m, f.k, there);
+        operand<TB>(1, f.b, f.order_b, t.batch * f.b_batch, f.b_pitch, t.col0, f.n, f.k, there);
+    }
+    // The next slice of the same planes: the buffer's start moves on.
+    template <bool TRANS>
+    __device__ __forceinline__ void move(int o, int64_t pitch, int64_t k) {
+        const uint32_t by = TRANS ? (uint32_t)(kSlice * pitch) : (uint32_t)(kSlice * 2);
+        const int left = (int)k - ks * kSlice;  // of k
+        u32x4 &b = buffer[o];
+        const uint32_t lo = b[0] + by;
+        b[1] += lo < by ? 1u : 0u;
+        b[0] = lo;
+        if (TRANS)  // rows of this slice
+            b[2] -= left < kSlice ? (uint32_t)((kSlice - left) * pitch) : 0u;
+        else
+            b[2] -= by;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) b[i] = (uint32_t)first_lane((int)b[i]);  // it stays in scalar registers
+        if (!TRANS) past[o] = chunk[o] * 8 < left ? 0u : kOutside;
     }
     // Load i of the current slice to LDS; `to`: the wave's place in the slice's stage.
     __device__ __forceinline__ void issue(int i, uint32_t to) const {
@@ -172,8 +190,13 @@ struct Loader {
         if (++slice == end) {
             v += gridDim.x;
             tile(f, total);
-        } else {
+        } else if (++ks == per) {
+            ks = 0;
+            ++pair;
             place(f, v < total);
+        } else if (v < total) {
+            move<TA>(0, f.a_pitch, f.k);
+            move<TB>(1, f.b_pitch, f.k);
         }
     }
 };
