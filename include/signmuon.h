@@ -538,10 +538,9 @@ size_t signmuon_linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t voc
  * mean) [workers][tokens]; dw is [workers][vocab][cols] of grad_dtype, the layout of
  * signmuon_matrix.grad. accumulate = 1 adds to what dw holds (the gradient of an
  * embedding that shares the table, as signmuon_embedding_backward adds to this
- * one's). Either of dx and dw may be NULL (not wanted), not both. For an F32 result g
- * and the factors that meet it are held in 16 bits of mantissa (3e-6 of a sum of
- * random products), for a BF16 result in 8, as its own rounding, and what is below
- * 2^-126 of them counts as 0; sums are fp32. workspace:
+ * one's). Either of dx and dw may be NULL (not wanted), not both. An F32 result is
+ * summed with fp32's accuracy; for a BF16 one, g and the factors that meet it are
+ * rounded to BF16 first. What is below 2^-126 of them counts as 0. workspace:
  * signmuon_linear_cross_entropy_backward_workspace_bytes(workers, tokens, vocab, cols,
  * x_dtype, w_dtype, grad_dtype) bytes, which does not grow with tokens * vocab past
  * a piece of 512 MB.

@@ -210,8 +210,8 @@ LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t 
     LossPlan p{};
     const int64_t rows = workers * tokens;
     p.pitch = sm::loss_pitch(cols);
-    const int64_t planes = x_dtype == SIGNMUON_F32 || grad_dtype == SIGNMUON_F32 ? 2 : 1;
-    int64_t most = kLossBackward / (planes * rows * 2);
+    const int64_t entry = x_dtype == SIGNMUON_F32 || grad_dtype == SIGNMUON_F32 ? 4 : 2;  // bytes of g's
+    int64_t most = kLossBackward / (entry * rows);
     const int64_t w_row = loss_direct(w_dtype, cols) ? 0 : loss_planes(w_dtype) * p.pitch * 2;
     if (w_row && kLossBackward / w_row < most) most = kLossBackward / w_row;
     p.piece = loss_piece(vocab, most);
@@ -228,34 +228,40 @@ LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t 
     };
     p.x = section(loss_planes(x_dtype) * rows * p.pitch * 2);
     p.w = section(w_row * p.piece);
-    p.g = section(planes * rows * p.piece * 2);
+    p.g = section(entry * rows * p.piece);
     p.dx = section(p.accumulate ? rows * cols * (int64_t)sizeof(float) : 0);
     p.sums = section(p.splits > 1 ? p.splits * rows * cols * (int64_t)sizeof(float) : 0);
     p.total = at;
     return p;
 }
 
-// The pairs of planes that a product of na by nb planes takes: all whose sizes are
-// above what the last planes leave out.
-void loss_pairs(sm::LossTile &f, int na, int nb) {
-    const int most = na > nb ? na : nb;  // planes i and j count where i + j is below it
+// The pairs of planes i of a and j of b with i + j below the longer one's count. An
+// fp32 a (in one piece) meets each plane of b with as many of its own.
+void loss_pairs(sm::LossTile &f, int na, int nb, bool whole_a = false) {
+    const int most = na > nb ? na : nb;
     f.pairs = 0;
-    for (int i = 0; i < na; ++i)
-        for (int j = 0; j < nb && i + j < most; ++j) {
-            f.order_a |= (uint32_t)i << (2 * f.pairs);
-            f.order_b |= (uint32_t)j << (2 * f.pairs);
-            ++f.pairs;
-        }
+    f.order_a = f.order_b = 0;
+    auto pair = [&](int a, int b) {
+        f.order_a |= (uint32_t)a << (2 * f.pairs);
+        f.order_b |= (uint32_t)b << (2 * f.pairs);
+        ++f.pairs;
+    };
+    for (int j = 0; j < nb; ++j) {
+        const int here = na < most - j ? na : most - j;
+        for (int i = 0; i < (whole_a ? 1 : here); ++i) pair(i, j);
+    }
 }
 
-void loss_split(sm::LossTile &f, int32_t splits) {
-    const int64_t slices = f.pairs * ((f.k + sm::kLossSlice - 1) / sm::kLossSlice);
+// The tile, and the slices of each part of k.
+void loss_tiles(sm::LossTile &f, int32_t splits, int64_t slice) {
+    f.tile = sm::kLossTile;
+    const int64_t slices = f.pairs * ((f.k + slice - 1) / slice);
     f.chunk = (int32_t)((slices + splits - 1) / splits);
     f.splits = (int32_t)((slices + f.chunk - 1) / f.chunk);
 }
 
 // One operand's planes, in the workspace or where it lies.
-void loss_operand(const uint16_t *(&planes)[sm::kLossPlanes], int n, const void *at, int64_t plane_entries) {
+void loss_operand(const void *(&planes)[sm::kLossPlanes], int n, const void *at, int64_t plane_entries) {
     for (int i = 0; i < n; ++i) planes[i] = static_cast<const uint16_t *>(at) + i * plane_entries;
 }
 
@@ -660,7 +666,7 @@ int signmuon_linear_cross_entropy(const void *x, signmuon_dtype x_dtype, const v
         f.k = cols;
         f.batch = 1;
         loss_pairs(f, nx, nw);
-        loss_split(f, 1);
+        loss_tiles(f, 1, sm::kLossSlice);
         f.targets = targets;
         f.targets64 = target_type == SIGNMUON_I64;
         f.partial = reinterpret_cast<float2 *>(ws + p.partial);
@@ -680,7 +686,7 @@ int signmuon_linear_cross_entropy(const void *x, signmuon_dtype x_dtype, const v
         j.loss = loss;
         j.lse = lse;
         j.rows = tokens;
-        j.blocks = (here + 127) / 128;
+        j.blocks = (here + f.tile / 2 - 1) / (f.tile / 2);
         j.vocab = vocab;
         j.first = v0 == 0;
         j.last = v0 + here == vocab;
@@ -721,7 +727,9 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
     const bool direct_w = loss_direct(w_dtype, cols), targets64 = target_type == SIGNMUON_I64;
     const bool x32 = x_dtype == SIGNMUON_F32, grad32 = grad_dtype == SIGNMUON_F32;
     const int nx = loss_planes(x_dtype), nw = loss_planes(w_dtype);
-    uint16_t *const g = reinterpret_cast<uint16_t *>(ws + p.g);
+    void *const g = ws + p.g;
+    const bool g32 = (x32 && dx) || (grad32 && dw);
+    const int64_t g_entry = g32 ? 4 : 2, g_slice = g32 ? sm::kLossWideSlice : sm::kLossSlice;
     if (int rc = loss_split_planes(x, x_dtype, rows, cols, p.pitch, ws + p.x, targets, targets64, vocab, st)) return rc;
     for (int64_t v0 = 0; v0 < vocab; v0 += p.piece) {
         const int64_t here = vocab - v0 < p.piece ? vocab - v0 : p.piece;
@@ -740,13 +748,13 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
         f.k = cols;
         f.batch = 1;
         loss_pairs(f, nx, nw);
-        loss_split(f, 1);
+        loss_tiles(f, 1, sm::kLossSlice);
         f.targets = targets;
         f.targets64 = targets64;
         f.lse = lse;
         f.dloss = dloss;
-        f.g[0] = g;
-        f.g[1] = (x32 && dx) || (grad32 && dw) ? g + rows * g_pitch : nullptr;
+        f.g = g;
+        f.g32 = g32;
         f.g_pitch = g_pitch;
         f.vocab = vocab;
         f.vocab0 = v0;
@@ -756,16 +764,18 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
         if (int rc = sm::launch_status()) return rc;
         if (dx) {
             sm::LossTile d{};
-            loss_operand(d.a, 2, g, rows * g_pitch);
+            d.a[0] = g;
             loss_operand(d.b, nw, f.b[0], here * p.pitch);
-            d.a_pitch = g_pitch * 2;
+            d.a_pitch = g_pitch * g_entry;
             d.b_pitch = p.pitch * 2;
             d.m = rows;
             d.n = cols;
             d.k = here;
             d.batch = 1;
-            loss_pairs(d, x32 ? 2 : 1, x32 && nw > 1 ? 2 : 1);
-            loss_split(d, p.splits);
+            d.g32 = g32;
+            d.planes = x32 ? 3 : 1;
+            loss_pairs(d, d.planes, x32 ? nw : 1, g32);
+            loss_tiles(d, p.splits, g_slice);
             d.out_batch = rows;
             // over several pieces the sums so far lie in dx itself, or in fp32 beside it
             float *const sums = x32 ? static_cast<float *>(dx) : reinterpret_cast<float *>(ws + p.dx);
@@ -792,9 +802,9 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
         }
         if (dw) {
             sm::LossTile d{};
-            loss_operand(d.a, 2, g, rows * g_pitch);
+            d.a[0] = g;
             loss_operand(d.b, nx, ws + p.x, rows * p.pitch);
-            d.a_pitch = g_pitch * 2;
+            d.a_pitch = g_pitch * g_entry;
             d.b_pitch = p.pitch * 2;
             d.a_batch = tokens * d.a_pitch;
             d.b_batch = tokens * d.b_pitch;
@@ -802,8 +812,10 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
             d.n = cols;
             d.k = tokens;
             d.batch = workers;
-            loss_pairs(d, grad32 ? 2 : 1, grad32 && nx > 1 ? 2 : 1);
-            loss_split(d, 1);
+            d.g32 = g32;
+            d.planes = grad32 ? 3 : 1;
+            loss_pairs(d, d.planes, grad32 ? nx : 1, g32);
+            loss_tiles(d, 1, g_slice);
             d.out = const_cast<void *>(at_entry(dw, v0 * cols, grad_dtype));
             d.out_batch = vocab;
             d.out_bf16 = !grad32;

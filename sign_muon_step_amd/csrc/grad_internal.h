@@ -162,8 +162,9 @@ void launch_rms_norm_sums(const RmsGrad &n, hipStream_t s);
 // ---------------------------------------------------------------------------
 // Softmax cross entropy of an output layer.
 // ---------------------------------------------------------------------------
-constexpr int kLossTile = 256;  // rows and columns of a workgroup's tile
-constexpr int kLossSlice = 64;  // k of a slice in LDS
+constexpr int kLossTile = 256;      // rows and columns of the largest tile
+constexpr int kLossSlice = 64;      // k of a slice in LDS
+constexpr int kLossWideSlice = 32;  // the same where a is fp32
 constexpr int kLossPlanes = 3, kLossPairs = 6;
 inline int64_t loss_pitch(int64_t cols) { return (cols + 7) / 8 * 8; }  // entries of a plane's row
 
@@ -180,19 +181,22 @@ void launch_loss_planes(const LossPlanes &f, hipStream_t s);
 
 // A product a b^T of planes, out [m][n], sums over k and over pairs of planes.
 struct LossTile {
-    const uint16_t *a[kLossPlanes], *b[kLossPlanes];
+    const void *a[kLossPlanes], *b[kLossPlanes];  // BF16; a[0] fp32 where g32 and a is g
     int64_t a_pitch, b_pitch;  // bytes of a row in memory
     int64_t a_batch, b_batch;  // bytes between batch entries
     int64_t m, n, k;
     int32_t batch, pairs;
     int32_t splits, chunk;     // chunk: slices of a split, of all pairs' slices in a row
     uint32_t order_a, order_b;  // the planes of pair i in bits 2 i on
+    int32_t tile;              // 256 or 128
+    int32_t planes;            // of an fp32 a: 1 or 3
+    bool g32;                  // g is fp32, not BF16
     // logits
     const void *targets;
     const float *lse, *dloss;
-    float2 *partial;           // [columns of 128][m]: maximum and sum, in units of log 2
+    float2 *partial;           // [columns of tile / 2][m]: maximum and sum, in units of log 2
     float *target;             // [m] logit of the target
-    uint16_t *g[2];            // planes [m][g_pitch]; the second may be null
+    void *g;                   // [m][g_pitch]
     int64_t g_pitch;
     int64_t vocab, vocab0;     // vocab0: the piece's first entry
     float scale, factor;       // factor: scale / log 2

@@ -16,11 +16,11 @@
 // product of planes is a longer sum: the pairs (h h), (h m), (m h), (m m),
 // (h l), (l h) leave out parts below 2^-22 of the operands' product (6e-9 of a sum of
 // random ones). Six BF16 products run at 2.6 times the rate of fp32's own matrix
-// instruction. Logits take all planes of their operands. g and the operands of dx
-// and dw take two planes, and the pairs (h h), (h m), (m h), where the result is
-// fp32, which is off by up to 2^-16 of each factor (3e-6 of a sum of random
-// products; an exponential of an fp32 logit of 16 is off by 1e-6 itself), and one
-// plane where the result is BF16, whose own rounding is as large.
+// instruction. Logits and fp32 results take all planes of their operands; a BF16
+// result takes one of g and of the operand that meets it, whose rounding is that of
+// the result. g is stored in fp32 where a result is, and its planes are made in
+// registers: it is read once for all of them. x and w are laid out as planes by a
+// pass of their own where they are not BF16 rows of whole vectors.
 //
 // The products are computed as b a^T: the instruction's rows are out's columns,
 // so that a lane's accumulators hold four consecutive columns of one row of out,
@@ -36,44 +36,74 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-constexpr int kWaves = 4, kSlice = kLossSlice, kStages = 2;
+constexpr int kWaves = 4, kStages = 2;
 
 // ---------------------------------------------------------------------------
 // Operands
 // ---------------------------------------------------------------------------
 // A slice of an operand lies in LDS as it does in memory:
-//  - rows of 64 k (TRANS = false: k runs along memory's rows), 128 bytes, whose
-//    16-byte chunks are XOR-swizzled so that 16 consecutive rows' reads fall on all banks;
-//  - 64 rows of TILE columns (TRANS = true: memory's rows are k), read by the
-//    instruction that transposes 4 x 16 values on the way; its 32-byte segments are
-//    XOR-swizzled by the row, so that 4 rows' reads fall on all banks.
-template <bool TRANS, int TILE>
+//  - kRows16, kRows32: k runs along memory's rows, and a slice has 128 bytes of each,
+//    whose 16-byte chunks are XOR-swizzled so that 16 consecutive rows' reads fall on all banks;
+//  - kCols16: memory's rows are k, and a slice has TILE columns of each. They are
+//    read by the instruction that transposes 4 x 16 values on the way; the 32-byte
+//    segments are XOR-swizzled by the row, so that 4 rows' reads fall on all banks;
+//  - kCols32: the same in fp32, read value by value; each 8 rows begin 128 bytes
+//    further on, so that the two halves of a wave, 8 rows apart, read other banks.
+enum { kRows16, kCols16, kRows32, kCols32 };
+
+template <int KIND, int TILE, int SLICE>
 struct Operand {
-    static constexpr int kBytes = TILE * kSlice * 2;
-    static constexpr int kLoads = kBytes / 1024 / kWaves;  // per wave and slice
-    static constexpr int kRowBytes = TRANS ? TILE * 2 : kSlice * 2;
-    static constexpr int kRows = 1024 / kRowBytes;         // of a load
+    static constexpr bool kTrans = KIND == kCols16 || KIND == kCols32;
+    static constexpr int kSize = KIND == kRows16 || KIND == kCols16 ? 2 : 4;
+    static constexpr int kLine = (kTrans ? TILE : SLICE) * kSize;  // bytes of a row in the slice
+    static constexpr int kCount = kTrans ? SLICE : TILE;           // rows
+    static constexpr int kPad = KIND == kCols32 ? 128 : 0;         // bytes behind each 8 rows
+    static constexpr int kBytes = kCount * kLine + kCount / 8 * kPad;
+    static constexpr int kRows = 1024 / kLine;                     // of a load
+    static constexpr int kLoads = kCount / kRows / kWaves;         // per wave and slice
+    static_assert(kTrans || kLine == 128, "whole lines");
 
     // A lane's place in a load: the wave's loads are kWaves * kRows rows apart, and the swizzle is the same in all.
     static __device__ __forceinline__ int row(int wave, int lane) { return wave * kRows + lane / (kWave / kRows); }
     static __device__ __forceinline__ int chunk(int wave, int lane) {
-        const int r = row(wave, lane), c = lane & (kRowBytes / 16 - 1);
-        return TRANS ? c ^ ((r & 3) << 2) : c ^ ((r >> 1) & 7);
+        const int r = row(wave, lane), c = lane & (kLine / 16 - 1);
+        return KIND == kCols16 ? c ^ ((r & 3) << 2) : KIND == kCols32 ? c : c ^ ((r >> 1) & 7);
     }
-    // Block i of the wave's rows from w0 on, 16 k from 16 s on, of a slice in LDS.
+    // Where load i of a wave lies, from the wave's first on.
+    static constexpr int place(int i) { return i * kWaves * 1024 + i * kWaves * kRows / 8 * kPad; }
+
+    // Block i of the wave's rows from w0 on, 16 k from 16 s on, of a slice in LDS: 8 k a lane.
     static __device__ __forceinline__ bf16x8 read(const char *slice, int w0, int i, int s, int lane) {
-        if (TRANS) {
+        if constexpr (KIND == kCols16) {
             const int l = lane & 15, g = lane >> 4;
             const int k = 16 * s + 8 * (g >> 1) + l / 4;  // and 4 more
             const int c = w0 / 8 + i * 4 + (g & 1) * 2 + (l & 3) / 2;
-            const char *p = slice + k * kRowBytes + ((c ^ ((l / 4) << 2)) << 4) + (l & 1) * 8;
+            const char *p = slice + k * kLine + ((c ^ ((l / 4) << 2)) << 4) + (l & 1) * 8;
             typedef __attribute__((address_space(3))) i16x4 *Lds;
             const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p));
-            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p + 4 * kRowBytes));
+            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p + 4 * kLine));
             return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            const int row = w0 + i * 32 + (lane & 31), c = 2 * s + (lane >> 5);
+            return *reinterpret_cast<const bf16x8 *>(slice + row * kLine + ((c ^ ((row >> 1) & 7)) << 4));
         }
-        const int row = w0 + i * 32 + (lane & 31), c = 2 * s + (lane >> 5);
-        return *reinterpret_cast<const bf16x8 *>(slice + row * kRowBytes + ((c ^ ((row >> 1) & 7)) << 4));
+    }
+    // The same of an fp32 operand.
+    static __device__ __forceinline__ void read(const char *slice, int w0, int i, int s, int lane, float (&v)[8]) {
+        const int half = lane >> 5;
+        if constexpr (KIND == kCols32) {
+            const char *p = slice + (2 * s + half) * (8 * kLine + kPad) + (w0 + i * 32 + (lane & 31)) * 4;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const float *>(p + j * kLine);
+        } else {
+            const int row = w0 + i * 32 + (lane & 31), c = 4 * s + 2 * half;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 q = *reinterpret_cast<const f32x4 *>(slice + row * kLine + (((c + h) ^ ((row >> 1) & 7)) << 4));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[4 * h + j] = q[j];
+            }
+        }
     }
 };
 
@@ -107,13 +137,13 @@ __device__ __forceinline__ Tile tile_at(const LossTile &f, int v, int total) {
 // The slices of a workgroup's tiles, one after the other, on their way into LDS:
 // the pairs of planes of a tile, and the slices of k of a pair. A lane's offsets
 // stay; a slice is a buffer's start and length. What lies outside an operand, and
-// slices past the last tile's, lie beyond the length and give zeros. TRANS: columns
-// past the last one hold what follows in memory, and end in results that are not
-// kept.
-template <bool TA, bool TB, int TILE>
+// slices past the last tile's, lie beyond the length and give zeros. Columns past
+// the last one of an operand whose rows are k hold what follows in memory, and end
+// in results that are not kept.
+template <int KA, int KB, int TILE, int SLICE>
 struct Loader {
-    using A = Operand<TA, TILE>;
-    using B = Operand<TB, TILE>;
+    using A = Operand<KA, TILE, SLICE>;
+    using B = Operand<KB, TILE, SLICE>;
     static constexpr int kLoads = A::kLoads + B::kLoads, kStage = A::kBytes + B::kBytes;
     u32x4 buffer[2];
     uint32_t at[2], past[2], step[2];  // of the lane's first load, where the slice's k ends; between loads
@@ -129,7 +159,7 @@ struct Loader {
         at[1] = (uint32_t)(B::row(wave, lane) * f.b_pitch + chunk[1] * 16);
         step[0] = (uint32_t)first_lane((int)(kWaves * A::kRows * f.a_pitch));
         step[1] = (uint32_t)first_lane((int)(kWaves * B::kRows * f.b_pitch));
-        per = (int)((f.k + kSlice - 1) / kSlice);
+        per = (int)((f.k + SLICE - 1) / SLICE);
         v = v_;
         tile(f, total);
     }
@@ -143,47 +173,49 @@ struct Loader {
         place(f, there);
     }
     // A slice's buffer, from the slice's k on, and where its k ends.
-    template <bool TRANS>
-    __device__ __forceinline__ void operand(int o, const uint16_t *const (&planes)[kLossPlanes], uint32_t order,
+    template <class O>
+    __device__ __forceinline__ void operand(int o, const void *const (&planes)[kLossPlanes], uint32_t order,
                                             int64_t batch, int64_t pitch, int64_t first, int64_t rows, int64_t k,
                                             bool there) {
-        const uint8_t *p = reinterpret_cast<const uint8_t *>(planes[order >> (2 * pair) & 3]) + batch;
-        const int64_t k0 = (int64_t)ks * kSlice;
-        if (TRANS) {
-            const int64_t have = k - k0 < kSlice ? k - k0 : kSlice;
-            buffer[o] = make_buffer(p + k0 * pitch + first * 2, there ? have * pitch - first * 2 : 0);
+        const int plane = O::kSize == 4 ? 0 : order >> (2 * pair) & 3;  // fp32 operands have one
+        const uint8_t *p = static_cast<const uint8_t *>(planes[plane]) + batch;
+        const int64_t k0 = (int64_t)ks * SLICE;
+        if (O::kTrans) {
+            const int64_t have = k - k0 < SLICE ? k - k0 : SLICE;
+            buffer[o] = make_buffer(p + k0 * pitch + first * O::kSize, there ? have * pitch - first * O::kSize : 0);
             past[o] = 0;
         } else {
             const int64_t have = rows - first < TILE ? rows - first : TILE;
-            buffer[o] = make_buffer(p + first * pitch + k0 * 2, there ? have * pitch - k0 * 2 : 0);
-            past[o] = k0 + chunk[o] * 8 < k ? 0u : kOutside;
+            buffer[o] = make_buffer(p + first * pitch + k0 * O::kSize, there ? have * pitch - k0 * O::kSize : 0);
+            past[o] = k0 + chunk[o] * (16 / O::kSize) < k ? 0u : kOutside;
         }
     }
     __device__ __forceinline__ void place(const LossTile &f, bool there) {
-        operand<TA>(0, f.a, f.order_a, t.batch * f.a_batch, f.a_pitch, t.row0, f.m, f.k, there);
-        operand<TB>(1, f.b, f.order_b, t.batch * f.b_batch, f.b_pitch, t.col0, f.n, f.k, there);
+        operand<A>(0, f.a, f.order_a, t.batch * f.a_batch, f.a_pitch, t.row0, f.m, f.k, there);
+        operand<B>(1, f.b, f.order_b, t.batch * f.b_batch, f.b_pitch, t.col0, f.n, f.k, there);
     }
     // The next slice of the same planes: the buffer's start moves on.
-    template <bool TRANS>
+    template <class O>
     __device__ __forceinline__ void move(int o, int64_t pitch, int64_t k) {
-        const uint32_t by = TRANS ? (uint32_t)(kSlice * pitch) : (uint32_t)(kSlice * 2);
-        const int left = (int)k - ks * kSlice;  // of k
+        const uint32_t by = O::kTrans ? (uint32_t)(SLICE * pitch) : (uint32_t)(SLICE * O::kSize);
+        const int left = (int)k - ks * SLICE;  // of k
         u32x4 &b = buffer[o];
         const uint32_t lo = b[0] + by;
         b[1] += lo < by ? 1u : 0u;
         b[0] = lo;
-        if (TRANS)  // rows of this slice
-            b[2] -= left < kSlice ? (uint32_t)((kSlice - left) * pitch) : 0u;
+        if (O::kTrans)  // rows of this slice
+            b[2] -= left < SLICE ? (uint32_t)((SLICE - left) * pitch) : 0u;
         else
             b[2] -= by;
 #pragma unroll
         for (int i = 0; i < 3; ++i) b[i] = (uint32_t)first_lane((int)b[i]);  // it stays in scalar registers
-        if (!TRANS) past[o] = chunk[o] * 8 < left ? 0u : kOutside;
+        if (!O::kTrans) past[o] = chunk[o] * (16 / O::kSize) < left ? 0u : kOutside;
     }
     // Load i of the current slice to LDS; `to`: the wave's place in the slice's stage.
     __device__ __forceinline__ void issue(int i, uint32_t to) const {
         const int o = i < A::kLoads ? 0 : 1, r = o ? i - A::kLoads : i;
-        load16_lds(to + (uint32_t)(o * A::kBytes + r * kWaves * 1024), (at[o] | past[o]) + (uint32_t)r * step[o], buffer[o]);
+        load16_lds(to + (uint32_t)(o ? A::kBytes + B::place(r) : A::place(r)), (at[o] | past[o]) + (uint32_t)r * step[o],
+                   buffer[o]);
     }
     // On to the next slice.
     __device__ __forceinline__ void advance(const LossTile &f, int total) {
@@ -195,8 +227,8 @@ struct Loader {
             ++pair;
             place(f, v < total);
         } else if (v < total) {
-            move<TA>(0, f.a_pitch, f.k);
-            move<TB>(1, f.b_pitch, f.k);
+            move<A>(0, f.a_pitch, f.k);
+            move<B>(1, f.b_pitch, f.k);
         }
     }
 };
@@ -214,6 +246,93 @@ __device__ __forceinline__ int column(int n, int e, int lane) { return n * 32 + 
 template <int F>
 using Acc = f32x16[F][F];
 
+template <int F>
+__device__ __forceinline__ void clear(Acc<F> &acc) {
+#pragma unroll
+    for (int i = 0; i < F * F; ++i) acc[i / F][i % F] = zeros();
+}
+
+// The accumulators' values, four columns of a row at a time as group(i, n, q, v)
+// makes them of block (i, n), to out as BF16 or fp32 (WIDE), through a wave's part of
+// LDS so that whole lines are written. out: the wave's first entry, rows of `pitch`
+// entries, of which `rows` and `cols` exist. Where rows begin at whole vectors,
+// buffer stores, which drop what lies outside; otherwise plain stores.
+constexpr int out_bytes(int F) { return F * 32; }              // of a row at a time
+constexpr int out_pitch(int F) { return out_bytes(F) + 16; }
+constexpr int out_lds(int F) { return 32 * out_pitch(F); }     // of a wave
+
+template <int F, bool WIDE, class G>
+__device__ __forceinline__ void write(Acc<F> &acc, char *mine, void *out, int64_t pitch, int rows, int cols, int lane,
+                                      G &&group) {
+    constexpr int E = WIDE ? 4 : 2, W = 16 / E;                 // bytes of a value, values of a store
+    constexpr int kCols = out_bytes(F) / E;                     // columns at a time
+    constexpr int kLanes = out_bytes(F) / 16, kRows = kWave / kLanes;  // lanes of a row, rows of a store
+    static_assert(kCols % 8 == 0 && F * 32 % kCols == 0, "whole passes");
+    // made anew for each tile, so that no address is kept in registers meanwhile
+    asm volatile("" : "+v"(lane));
+    const int r0 = lane / kLanes, c16 = lane % kLanes, row = lane & 31, half = lane >> 5;
+    rows = rows < 0 ? 0 : rows < F * 32 ? rows : F * 32;
+    cols = cols < 0 ? 0 : cols < F * 32 ? cols : F * 32;
+    const int step = (int)pitch * E;
+    char *p = static_cast<char *>(out);
+    const bool even = pitch % W == 0;
+    const __amdgpu_buffer_rsrc_t buffer =
+        __builtin_amdgcn_make_buffer_rsrc(p, 0, rows > 0 && cols > 0 ? (rows - 1) * step + cols * E : 0, 0x00020000);
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int n0 = 0; n0 < F * 32; n0 += kCols) {
+            // no accumulator leaves its register before its turn
+#pragma unroll
+            for (int n = n0 / 32; n < (n0 + kCols + 31) / 32; ++n) pin(acc[i][n]);
+#pragma unroll
+            for (int n = n0; n < n0 + kCols; n += 8) {
+                char *to = mine + row * out_pitch(F) + (n - n0 + half * 4) * E;
+                float v[4];
+                group(i, n / 32, n % 32 / 8, v);
+                if constexpr (WIDE)
+                    *reinterpret_cast<f32x4 *>(to) = f32x4{v[0], v[1], v[2], v[3]};
+                else
+                    *reinterpret_cast<u32x2 *>(to) = u32x2{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3])};
+            }
+            // lanes read what others wrote (LDS accesses of a wave keep their order)
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_wave_barrier();
+            auto staged = [&](int r) { return *reinterpret_cast<const u32x4 *>(mine + (r * kRows + r0) * out_pitch(F) + c16 * 16); };
+            if (even) {
+                const uint32_t at = n0 + c16 * W < cols ? (uint32_t)(r0 * step + (n0 + c16 * W) * E) : kOutside;
+                u32x4 v[32 / kRows];
+#pragma unroll
+                for (int r = 0; r < 32 / kRows; ++r) v[r] = staged(r);
+#pragma unroll
+                for (int r = 0; r < 32 / kRows; ++r)
+                    __builtin_amdgcn_raw_buffer_store_b128(v[r], buffer, (int)(at + (uint32_t)((i * 32 + r * kRows) * step)), 0, 0);
+            } else {
+                const int here = cols - n0;  // columns from this pass's first on
+#pragma unroll 1
+                for (int r = 0; r < 32 / kRows; ++r)
+                    if (i * 32 + r * kRows + r0 < rows && c16 * W + W <= here)
+                        *reinterpret_cast<u32x4_any *>(p + (int64_t)(i * 32 + r * kRows + r0) * step + (n0 + c16 * W) * E) =
+                            staged(r);
+                // the last columns of a row, one by one
+                if (here > 0 && here < kCols && i * 32 + row < rows && half == 0)
+#pragma unroll 1
+                    for (int c = here / W * W; c < here; ++c) {
+                        char *q = p + (int64_t)(i * 32 + row) * step + (n0 + c) * E;
+                        const char *from = mine + row * out_pitch(F) + c * E;
+                        if constexpr (WIDE)
+                            *reinterpret_cast<uint32_t *>(q) = *reinterpret_cast<const uint32_t *>(from);
+                        else
+                            *reinterpret_cast<uint16_t *>(q) = *reinterpret_cast<const uint16_t *>(from);
+                    }
+            }
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    clear<F>(acc);
+}
+
 // A row's maximum and sum of exponentials over the wave's columns, and the target's
 // logit, in units of log 2.
 template <int F>
@@ -221,11 +340,16 @@ __device__ __forceinline__ void finish_lse(const LossTile &f, Acc<F> &acc, int64
     constexpr int kCols = F * 32;
     if (col0 < f.n) {
         const int have = (int)(f.n - col0 < kCols ? f.n - col0 : kCols);
+        int target[F];  // column, or -1
 #pragma unroll
         for (int i = 0; i < F; ++i) {
             const int64_t row = row0 + i * 32 + (lane & 31);
-            const bool there = row < f.m;
-            const int64_t target = (there ? target_of(f, row) : -1) - f.vocab0 - col0;
+            const int64_t at = row < f.m ? target_of(f, row) - f.vocab0 - col0 : -1;
+            target[i] = at >= 0 && at < have ? (int)at : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            const int64_t row = row0 + i * 32 + (lane & 31);
             float l[F][16], top = -INFINITY;
 #pragma unroll
             for (int n = 0; n < F; ++n) {
@@ -243,13 +367,12 @@ __device__ __forceinline__ void finish_lse(const LossTile &f, Acc<F> &acc, int64
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) top = fmaxf(fmaxf(l[n][e], l[n][e + 1]), top);
             top = fmaxf(top, __shfl_xor(top, 32));
-            const bool here = target >= 0 && target < have;
-            if (__any(here)) {
+            if (__any(target[i] >= 0)) {
 #pragma unroll
                 for (int n = 0; n < F; ++n)
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        if (here && column(n, e, lane) == (int)target) f.target[row] = l[n][e];
+                        if (column(n, e, lane) == target[i]) f.target[row] = l[n][e];
             }
             const float base = top == -INFINITY ? 0.0f : top;  // a block of minus infinities adds nothing
             float sum[2] = {};
@@ -259,117 +382,118 @@ __device__ __forceinline__ void finish_lse(const LossTile &f, Acc<F> &acc, int64
                 for (int e = 0; e < 16; ++e) sum[e & 1] += __builtin_amdgcn_exp2f(l[n][e] - base);
             sum[0] += sum[1];
             sum[0] += __shfl_xor(sum[0], 32);
-            if (there && lane < 32) f.partial[(col0 / kCols) * f.m + row] = make_float2(top, sum[0]);
+            if (row < f.m && lane < 32) f.partial[(col0 / kCols) * f.m + row] = make_float2(top, sum[0]);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-#pragma unroll
-    for (int i = 0; i < F * F; ++i) acc[i / F][i % F] = zeros();
+    clear<F>(acc);
 }
 
-// g, in one or two planes; zeros in columns past the vocabulary.
-template <int F>
-__device__ __forceinline__ void finish_grad(const LossTile &f, Acc<F> &acc, int64_t row0, int64_t col0, int lane) {
+// g; zeros in the columns past the vocabulary that a tile has.
+template <int F, bool WIDE>
+__device__ __forceinline__ void finish_grad(const LossTile &f, Acc<F> &acc, char *mine, int64_t row0, int64_t col0,
+                                            int lane) {
     constexpr int kCols = F * 32;
     const int have = (int)(f.n - col0 < 0 ? 0 : f.n - col0 < kCols ? f.n - col0 : kCols);
+    int target[F], limit[F];  // of the lane's rows: the target's column, and the columns that count
+    float d[F], base[F];
+    bool any = false, whole = true;
 #pragma unroll
     for (int i = 0; i < F; ++i) {
         const int64_t row = row0 + i * 32 + (lane & 31);
         const bool in = row < f.m;
-        const int64_t target = in ? target_of(f, row) : -1;
-        const bool there = target >= 0 && target < f.vocab;
+        const int64_t t = in ? target_of(f, row) : -1, at = t - f.vocab0 - col0;
         // a token without a target has no gradient, whatever its logits are
-        const float d = there ? f.scale * f.dloss[row] : 0.0f, base = in ? f.lse[row] * kLog2E : 0.0f;
-        const int64_t local = target - f.vocab0 - col0;
-        const bool any = __any(there && local >= 0 && local < kCols);
-#pragma unroll
-        for (int n = 0; n < F; ++n) {
-            pin(acc[i][n]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float v[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int c = column(n, q * 4 + j, lane);
-                    const float p = __builtin_amdgcn_exp2f(fmaf(acc[i][n][q * 4 + j], f.factor, -base));
-                    v[j] = there && c < have ? d * (any && c == local ? p - 1.0f : p) : 0.0f;
-                }
-                if (!in) continue;
-                const int64_t at = row * f.g_pitch + col0 + column(n, q * 4, lane);
-                const u32x2 h = {to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3])};
-                *reinterpret_cast<u32x2 *>(f.g[0] + at) = h;
-                if (f.g[1]) {
-                    const float r[4] = {v[0] - __uint_as_float(h[0] << 16), v[1] - __uint_as_float(h[0] & 0xffff0000u),
-                                        v[2] - __uint_as_float(h[1] << 16), v[3] - __uint_as_float(h[1] & 0xffff0000u)};
-                    *reinterpret_cast<u32x2 *>(f.g[1] + at) = u32x2{to_bf16x2(r[0], r[1]), to_bf16x2(r[2], r[3])};
-                }
-            }
-            acc[i][n] = zeros();
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        const bool there = t >= 0 && t < f.vocab;
+        d[i] = there ? f.scale * f.dloss[row] : 0.0f;
+        base[i] = there ? f.lse[row] * kLog2E : 0.0f;
+        target[i] = there && at >= 0 && at < have ? (int)at : -1;
+        limit[i] = there ? have : 0;
+        any |= target[i] >= 0;
+        whole &= limit[i] == kCols;
     }
+    const bool plain = __all(whole && !any);
+    write<F, WIDE>(acc, mine, reinterpret_cast<char *>(f.g) + (row0 * f.g_pitch + col0) * (WIDE ? 4 : 2), f.g_pitch,
+                   (int)(f.m - row0 < kCols ? f.m - row0 : kCols), kCols, lane,
+                   [&](int i, int n, int q, float(&v)[4]) {
+#pragma unroll
+                       for (int j = 0; j < 4; ++j)
+                           v[j] = __builtin_amdgcn_exp2f(fmaf(acc[i][n][q * 4 + j], f.factor, -base[i]));
+                       if (plain) {
+#pragma unroll
+                           for (int j = 0; j < 4; ++j) v[j] *= d[i];
+                       } else {
+#pragma unroll
+                           for (int j = 0; j < 4; ++j) {
+                               const int c = column(n, q * 4 + j, lane);
+                               v[j] = c < limit[i] ? d[i] * (c == target[i] ? v[j] - 1.0f : v[j]) : 0.0f;
+                           }
+                       }
+                   });
 }
 
 // A product's values, added to what `prev` holds.
-template <int F>
-__device__ __forceinline__ void finish_values(const LossTile &f, Acc<F> &acc, int64_t row0, int64_t col0, int64_t first,
-                                              int lane) {
+template <int F, bool WIDE>
+__device__ __forceinline__ void finish_values(const LossTile &f, Acc<F> &acc, char *mine, const Tile &t, int64_t row0,
+                                              int64_t col0, int lane) {
+    const int64_t first = (f.out_batch * (t.split * (int64_t)f.batch + t.batch) + row0) * f.n + col0;
+    const int rows = (int)(f.m - row0 < F * 32 ? f.m - row0 : F * 32), cols = (int)(f.n - col0 < F * 32 ? f.n - col0 : F * 32);
+    write<F, WIDE>(acc, mine, static_cast<char *>(f.out) + first * (WIDE ? 4 : 2), f.n, rows, cols, lane,
+                   [&](int i, int n, int q, float(&v)[4]) {
 #pragma unroll
-    for (int i = 0; i < F; ++i) {
-        const int64_t row = row0 + i * 32 + (lane & 31);
+                       for (int j = 0; j < 4; ++j) v[j] = acc[i][n][q * 4 + j];
+                       if (!f.prev) return;
+                       const int row = i * 32 + (lane & 31), col = column(n, q * 4, lane);
+                       const int have = row >= rows ? 0 : left(cols, col) < 4 ? left(cols, col) : 4;
+                       float p[4];
+                       if (f.prev_bf16)
+                           load_n<true>(f.prev, first + row * f.n + col, have, p);
+                       else
+                           load_n<false>(f.prev, first + row * f.n + col, have, p);
 #pragma unroll
-        for (int n = 0; n < F; ++n) {
-            pin(acc[i][n]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t col = col0 + column(n, q * 4, lane), at = (first + row) * f.n + col;
-                const int have = (int)(row >= f.m || f.n - col < 0 ? 0 : f.n - col < 4 ? f.n - col : 4);
-                float v[4], p[4];
-                if (f.prev_bf16)
-                    load_n<true>(f.prev, at, f.prev ? have : 0, p);
-                else
-                    load_n<false>(f.prev, at, f.prev ? have : 0, p);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = acc[i][n][q * 4 + j] + p[j];
-                if (f.out_bf16)
-                    store_n<true>(f.out, at, have, v);
-                else
-                    store_n<false>(f.out, at, have, v);
-            }
-            acc[i][n] = zeros();
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
+                       for (int j = 0; j < 4; ++j) v[j] += p[j];
+                   });
+}
+
+constexpr std::integral_constant<int, 0> kLow{};
+constexpr std::integral_constant<int, 1> kHigh{};
+
+// Nothing behind this runs before v is in its registers.
+__device__ __forceinline__ void hold(const bf16x8 &v) { asm volatile("" : : "v"(v) : "memory"); }
+
+// The place of slice c's loads of a wave. Opaque: each load adds its constant to
+// this, where the compiler would keep every sum in a scalar register of its own and
+// run out of them.
+template <class L>
+__device__ __forceinline__ uint32_t stage_of(uint32_t lds, unsigned c, int wave) {
+    uint32_t to = lds + c % kStages * L::kStage + (uint32_t)wave * 1024u;
+    asm volatile("" : "+s"(to));
+    return to;
 }
 
 enum { kLse, kGrad, kValues };
 
-// A workgroup takes every gridDim-th tile; four waves of half a tile each way. The
-// loads run two slices ahead of the products, on into the next tile, so that a
-// tile's first slices are there when the one before it is done.
-template <bool TA, bool TB, int TILE, int END>
-__global__ __launch_bounds__(kWaves *kWave) void loss_tile_kernel(LossTile f, int total) {
-    using L = Loader<TA, TB, TILE>;
+// Products of BF16 operands. A workgroup takes every gridDim-th tile; four waves of
+// half a tile each way. The loads run two slices ahead of the products, on into the
+// next tile, so that a tile's first slices are there when the one before it is done.
+// WIDE: results in fp32.
+template <int KA, int KB, int TILE, int END, bool WIDE>
+__global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_tile_kernel(LossTile f, int total) {
+    using L = Loader<KA, KB, TILE, kLossSlice>;
     using A = typename L::A;
     using B = typename L::B;
     constexpr int F = TILE / 64;  // 32 x 32 blocks of a wave, each way
-    __shared__ __attribute__((aligned(1024))) char lds[kStages * L::kStage];
+    constexpr int kOut = kStages * L::kStage;
+    __shared__ __attribute__((aligned(1024))) char lds[kOut + (END == kLse ? 0 : kWaves * out_lds(F))];
     const int lane = threadIdx.x & (kWave - 1), wave = first_lane(threadIdx.x / kWave);
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char *)lds);
     const int wm = wave / 2 * (TILE / 2), wn = wave % 2 * (TILE / 2);
 
     L loader;
     loader.start(f, blockIdx.x, total, wave, lane);
-    auto place = [&](unsigned c) {
-        uint32_t to = lds0 + c % kStages * L::kStage + (uint32_t)wave * 1024u;
-        // opaque: each load adds its constant to this, where the compiler would
-        // keep every sum in a scalar register of its own and run out of them
-        asm volatile("" : "+s"(to));
-        return to;
-    };
 #pragma unroll 1
     for (unsigned c = 0; c < kStages; ++c) {
-        const uint32_t to = place(c);
+        const uint32_t to = stage_of<L>(lds0, c, wave);
 #pragma unroll
         for (int i = 0; i < L::kLoads; ++i) loader.issue(i, to);
         loader.advance(f, total);
@@ -385,8 +509,7 @@ __global__ __launch_bounds__(kWaves *kWave) void loss_tile_kernel(LossTile f, in
         fr[H][s][i] = i < F ? B::read(stage + A::kBytes, wn, i, 2 * H + s, lane) : A::read(stage, wm, i - F, 2 * H + s, lane);
     };
     f32x16 acc[F][F];
-#pragma unroll
-    for (int i = 0; i < F * F; ++i) acc[i / F][i % F] = zeros();
+    clear<F>(acc);
     // The products of half a slice, from the registers, a step for each; extra(step)
     // is what else the step issues, so that the matrix pipe does not wait behind a
     // run of reads or loads.
@@ -400,23 +523,25 @@ __global__ __launch_bounds__(kWaves *kWave) void loss_tile_kernel(LossTile f, in
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    constexpr std::integral_constant<int, 0> kLow{};
-    constexpr std::integral_constant<int, 1> kHigh{};
     wait_loads<L::kLoads>();  // slice 0
     barrier();
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(kLow, 0, r);
 
-    // Steps of the low half: the reads of the high half in the first half of them,
-    // then at step kMeet all waves have read slice c and slice c + 1 has landed, so
-    // that slice c + 2 is loaded to slice c's place from there on, and slice c + 1
-    // may be read.
-    constexpr int kMeet = kSteps * 5 / 8, kPerRead = kReads * 2 / kSteps, kPerLoad = L::kLoads * 2 / kSteps;
-    static_assert(kPerRead * kSteps == 2 * kReads && kPerLoad * kSteps == 2 * L::kLoads, "whole steps");
-    auto load_step = [&](uint32_t to, int s) {  // s: steps from kMeet on
+    // Steps of the low half: the reads of the high half, two a step, then at step
+    // kMeet all waves have read slice c and slice c + 1 has landed, so that slice c + 2
+    // is loaded to slice c's place from there on, a load every kSpread steps, and
+    // slice c + 1 may be read. Few loads at a time: at 8192 x 32000 x 4096 the four
+    // products take 7.1 ms so, 7.2 with a load every second step and 7.6 with one
+    // each step.
+    constexpr int kMeet = kReads / 2 + 2, kSpread = (2 * kSteps - kMeet) / L::kLoads;
+    static_assert(kMeet < kSteps && kSpread > 0, "room for the reads and loads");
+    auto steps = [&](auto h, unsigned c, uint32_t to, int s, int gone) {
 #pragma unroll
-        for (int i = s * kPerLoad; i < (s + 1) * kPerLoad; ++i)
-            if (i < L::kLoads) loader.issue(i, to);
+        for (int r = 2 * s; r < 2 * s + 2; ++r)
+            if (r < kReads) read(h, c, r);
+        if (s + gone >= kMeet && (s + gone - kMeet) % kSpread == 0 && (s + gone - kMeet) / kSpread < L::kLoads)
+            loader.issue((s + gone - kMeet) / kSpread, to);
     };
     const int per = loader.per;
     unsigned c = 0;  // slices so far
@@ -427,35 +552,164 @@ __global__ __launch_bounds__(kWaves *kWave) void loss_tile_kernel(LossTile f, in
         const int end = begin + f.chunk < f.pairs * per ? begin + f.chunk : f.pairs * per;
 #pragma unroll 1
         for (int j = begin; j < end; ++j, ++c) {
-            const uint32_t to = place(c);
+            const uint32_t to = stage_of<L>(lds0, c, wave);
             products(kLow, [&](int s) {
-#pragma unroll
-                for (int r = s * kPerRead; r < (s + 1) * kPerRead; ++r)
-                    if (r < kReads) read(kHigh, c, r);
                 if (s == kMeet) {
 #pragma unroll
-                    for (int r = 0; r < kReads; ++r) asm volatile("" : : "v"(fr[1][r / (2 * F)][r % (2 * F)]) : "memory");
+                    for (int r = 0; r < kReads; ++r) hold(fr[1][r / (2 * F)][r % (2 * F)]);
                     wait_loads<0>();
                     barrier();
                 }
-                if (s >= kMeet) load_step(to, s - kMeet);
+                steps(kHigh, c, to, s, 0);
             });
-            products(kHigh, [&](int s) {
-#pragma unroll
-                for (int r = s * kPerRead; r < (s + 1) * kPerRead; ++r)
-                    if (r < kReads) read(kLow, c + 1, r);
-                load_step(to, kSteps - kMeet + s);
-            });
+            products(kHigh, [&](int s) { steps(kLow, c + 1, to, s, kSteps); });
 #pragma unroll
             for (int i = 0; i < F * F; ++i) pin(acc[i / F][i % F]);
             loader.advance(f, total);
         }
+        char *mine = lds + kOut + wave * out_lds(F);
         if constexpr (END == kLse)
             finish_lse<F>(f, acc, t.row0 + wm, t.col0 + wn, lane);
         else if constexpr (END == kGrad)
-            finish_grad<F>(f, acc, t.row0 + wm, t.col0 + wn, lane);
+            finish_grad<F, WIDE>(f, acc, mine, t.row0 + wm, t.col0 + wn, lane);
         else
-            finish_values<F>(f, acc, t.row0 + wm, t.col0 + wn, f.out_batch * (t.split * (int64_t)f.batch + t.batch), lane);
+            finish_values<F, WIDE>(f, acc, mine, t, t.row0 + wm, t.col0 + wn, lane);
+    }
+    wait_loads<0>();  // loads past the last tile write LDS too
+}
+
+// Products of an fp32 a, taken apart into planes in registers, and a BF16 b. PLANES:
+// of a; 1, or 3 for the first plane of b, 2 for its second and 1 for its third. A slice
+// is 32 k: while 16 of them are multiplied, the next 16 are read and taken apart.
+template <int KA, int TILE, int PLANES, bool WIDE>
+__global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_wide_kernel(LossTile f, int total) {
+    using L = Loader<KA, kCols16, TILE, kLossWideSlice>;
+    using A = typename L::A;
+    using B = typename L::B;
+    constexpr int F = TILE / 64;
+    constexpr int kOut = kStages * L::kStage;
+    __shared__ __attribute__((aligned(1024))) char lds[kOut + kWaves * out_lds(F)];
+    const int lane = threadIdx.x & (kWave - 1), wave = first_lane(threadIdx.x / kWave);
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char *)lds);
+    const int wm = wave / 2 * (TILE / 2), wn = wave % 2 * (TILE / 2);
+
+    L loader;
+    loader.start(f, blockIdx.x, total, wave, lane);
+#pragma unroll 1
+    for (unsigned c = 0; c < kStages; ++c) {
+        const uint32_t to = stage_of<L>(lds0, c, wave);
+#pragma unroll
+        for (int i = 0; i < L::kLoads; ++i) loader.issue(i, to);
+        loader.advance(f, total);
+    }
+
+    float raw[F][8];
+    u32x4 plane[2][PLANES][F];  // [half][plane][block]
+    bf16x8 fb[2][F];
+    auto read = [&](auto h, unsigned c, int r) {  // of half h of slice c
+        constexpr int H = decltype(h)::value;
+        const char *stage = lds + c % kStages * L::kStage;
+        if (r < F)
+            A::read(stage, wm, r, H, lane, raw[r]);
+        else
+            fb[H][r - F] = B::read(stage + A::kBytes, wn, r - F, H, lane);
+    };
+    constexpr int kReads = 2 * F, kParts = 4 * F;
+    auto part = [&](auto h, int p) {  // two values of a block into planes
+        constexpr int H = decltype(h)::value;
+        const int i = p / 4, j = p % 4;
+        float x = raw[i][2 * j], y = raw[i][2 * j + 1];
+#pragma unroll
+        for (int q = 0; q < PLANES; ++q) {
+            const uint32_t w = to_bf16x2(x, y);
+            plane[H][q][i][j] = w;
+            x -= __uint_as_float(w << 16);
+            y -= __uint_as_float(w & 0xffff0000u);
+        }
+    };
+    f32x16 acc[F][F];
+    clear<F>(acc);
+    wait_loads<L::kLoads>();  // slice 0
+    barrier();
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read(kLow, 0, r);
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) part(kLow, p);
+
+    // As above: the reads of the next 16 k first, then, at kMeet of the low half, the
+    // slice's place is free for the loads; the reads' values are taken apart from
+    // kMeet on.
+    constexpr int kRound = F * F, kPerRead = 4 / F, kMeet = kRound * 5 / 8 + (F == 2 ? 1 : 0);
+    static_assert(kPerRead * kMeet >= kReads && kMeet < kRound, "room for the reads");
+    auto half = [&](auto planes, auto h, unsigned c, uint32_t to) {
+        constexpr int N = decltype(planes)::value, H = decltype(h)::value, kSteps = N * kRound;
+        // the loads: from kMeet of the low half to the end of the high one
+        constexpr int kRest = 2 * kSteps - kMeet, kSpread = kRest / L::kLoads > 0 ? kRest / L::kLoads : 1;
+        constexpr int kPerLoad = (L::kLoads + kRest - 1) / kRest;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            if (s == kMeet && H == 0) {
+#pragma unroll
+                for (int i = 0; i < F; ++i) {
+                    hold(fb[1][i]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) asm volatile("" : : "v"(raw[i][j]) : "memory");
+                }
+                wait_loads<0>();
+                barrier();
+            }
+#pragma unroll
+            for (int r = s * kPerRead; r < (s + 1) * kPerRead; ++r)
+                if (r < kReads) {
+                    if (H == 0)
+                        read(kHigh, c, r);
+                    else
+                        read(kLow, c + 1, r);
+                }
+            const int g = s + H * kSteps - kMeet;  // steps since the loads may begin
+            if (g >= 0 && g % kSpread == 0)
+#pragma unroll
+                for (int i = g / kSpread * kPerLoad; i < (g / kSpread + 1) * kPerLoad; ++i)
+                    if (i < L::kLoads) loader.issue(i, to);
+            if (s >= kMeet)
+#pragma unroll
+                for (int p = (s - kMeet) * kParts / (kSteps - kMeet); p < (s + 1 - kMeet) * kParts / (kSteps - kMeet); ++p) {
+                    if (H == 0)
+                        part(kHigh, p);
+                    else
+                        part(kLow, p);
+                }
+            const int q = s / kRound, i = s % kRound / F, n = s % F;
+            acc[i][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[H][n], __builtin_bit_cast(bf16x8, plane[H][q][i]),
+                                                                acc[i][n], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    const int per = loader.per;
+    unsigned c = 0;  // slices so far
+#pragma unroll 1
+    for (int v = blockIdx.x; v < total; v += gridDim.x) {
+        const Tile t = tile_at<TILE>(f, v, total);
+        const int begin = t.split * f.chunk;
+        const int end = begin + f.chunk < f.pairs * per ? begin + f.chunk : f.pairs * per;
+        int j = begin;
+        auto slices = [&](auto planes, int stop) {
+#pragma unroll 1
+            for (; j < stop; ++j, ++c) {
+                const uint32_t to = stage_of<L>(lds0, c, wave);
+                half(planes, kLow, c, to);
+                half(planes, kHigh, c, to);
+#pragma unroll
+                for (int i = 0; i < F * F; ++i) pin(acc[i / F][i % F]);
+                loader.advance(f, total);
+            }
+        };
+        if constexpr (PLANES == 3) {
+            slices(std::integral_constant<int, 3>{}, end < per ? end : per);
+            slices(std::integral_constant<int, 2>{}, end < 2 * per ? end : 2 * per);
+        }
+        slices(std::integral_constant<int, 1>{}, end);
+        finish_values<F, WIDE>(f, acc, lds + kOut + wave * out_lds(F), t, t.row0 + wm, t.col0 + wn, lane);
     }
     wait_loads<0>();  // loads past the last tile write LDS too
 }
@@ -552,12 +806,41 @@ __global__ __launch_bounds__(256) void loss_sums_kernel(LossSums f) {
         store_n<false>(f.out, at, have, v);
 }
 
-template <bool TA, bool TB, int END>
+int tiles_of(const LossTile &f) {
+    const int64_t t = f.tile;
+    return (int)((f.m + t - 1) / t * ((f.n + t - 1) / t) * f.batch * f.splits);
+}
+
+// One workgroup a compute unit (TILE 128: two), a multiple of the XCDs.
+dim3 grid_of(const LossTile &f) {
+    const int total = tiles_of(f), most = device_cus() / 8 * 8 * (f.tile == 256 ? 1 : 2);
+    return dim3((unsigned)(total < most ? total : most));
+}
+
+template <int KA, int KB, int END, bool WIDE>
 void launch_tiles(const LossTile &f, hipStream_t s) {
-    constexpr int TILE = kLossTile;
-    const int64_t tiles = (f.m + TILE - 1) / TILE * ((f.n + TILE - 1) / TILE) * f.batch * f.splits;
-    const int total = (int)tiles, most = device_cus() / 8 * 8;
-    loss_tile_kernel<TA, TB, TILE, END><<<dim3((unsigned)(total < most ? total : most)), kWaves * kWave, 0, s>>>(f, total);
+    if (f.tile == 256)
+        loss_tile_kernel<KA, KB, 256, END, WIDE><<<grid_of(f), kWaves * kWave, 0, s>>>(f, tiles_of(f));
+    else
+        loss_tile_kernel<KA, KB, 128, END, WIDE><<<grid_of(f), kWaves * kWave, 0, s>>>(f, tiles_of(f));
+}
+
+template <int KA, int PLANES, bool WIDE>
+void launch_wide(const LossTile &f, hipStream_t s) {
+    if (f.tile == 256)
+        loss_wide_kernel<KA, 256, PLANES, WIDE><<<grid_of(f), kWaves * kWave, 0, s>>>(f, tiles_of(f));
+    else
+        loss_wide_kernel<KA, 128, PLANES, WIDE><<<grid_of(f), kWaves * kWave, 0, s>>>(f, tiles_of(f));
+}
+
+template <int K16, int K32>
+void launch_values(const LossTile &f, hipStream_t s) {
+    if (!f.g32)
+        f.out_bf16 ? launch_tiles<K16, kCols16, kValues, false>(f, s) : launch_tiles<K16, kCols16, kValues, true>(f, s);
+    else if (f.planes == 3)
+        launch_wide<K32, 3, true>(f, s);
+    else
+        f.out_bf16 ? launch_wide<K32, 1, false>(f, s) : launch_wide<K32, 1, true>(f, s);
 }
 
 }  // namespace
@@ -572,15 +855,18 @@ void launch_loss_planes(const LossPlanes &f, hipStream_t s) {
 }
 
 void launch_loss_logits(const LossTile &f, bool grad, hipStream_t s) {
-    grad ? launch_tiles<false, false, kGrad>(f, s) : launch_tiles<false, false, kLse>(f, s);
+    if (!grad)
+        launch_tiles<kRows16, kRows16, kLse, true>(f, s);
+    else
+        f.g32 ? launch_tiles<kRows16, kRows16, kGrad, true>(f, s) : launch_tiles<kRows16, kRows16, kGrad, false>(f, s);
 }
 
 void launch_loss_join(const LossJoin &f, hipStream_t s) {
     loss_join_kernel<<<dim3((unsigned)((f.rows + kWave - 1) / kWave)), 1024, 0, s>>>(f);
 }
 
-void launch_loss_dx(const LossTile &f, hipStream_t s) { launch_tiles<false, true, kValues>(f, s); }
-void launch_loss_dw(const LossTile &f, hipStream_t s) { launch_tiles<true, true, kValues>(f, s); }
+void launch_loss_dx(const LossTile &f, hipStream_t s) { launch_values<kRows16, kRows32>(f, s); }
+void launch_loss_dw(const LossTile &f, hipStream_t s) { launch_values<kCols16, kCols32>(f, s); }
 
 void launch_loss_sums(const LossSums &f, hipStream_t s) {
     loss_sums_kernel<<<dim3((unsigned)((f.total + 1023) / 1024)), 256, 0, s>>>(f);

@@ -4,8 +4,8 @@ implementation in 64 bits.
 Tolerances count roundings, with u = 2^-24. Sums on the matrix cores follow the
 probabilistic bound for a chain of n roundings (Higham and Mary, SIAM J. Sci.
 Comput. 2019): 4 sqrt(n) u times the sum of the terms' sizes. What is held in one
-BF16 plane is off by 2^-8 of itself, in two by 2^-16, in three by 2^-24; a
-product of two operands in planes leaves out at most as much once more."""
+BF16 plane is off by 2^-8 of itself, in two by 2^-16, in three by 2^-24; of a
+product of two operands in three planes, pairs of 2^-8 by 2^-16 are left out."""
 import math
 
 import pytest
@@ -113,17 +113,15 @@ def gradients_in_64(x, w, targets, scale, lse, dloss, grad_dtype):
     g_tol = torch.where(there, d.abs() * p_tol + 3 * U * g.abs(), 0.0)
     x64, w64 = x.double().flatten(0, 1), w.double()
 
-    def planes(dtype, n):
-        return 0.0 if dtype == BF16 else {1: 2.0 ** -8, 2: 2.0 ** -16}[n]
-
     def product(rows, a, a_tol, b, b_dtype, fp32):
-        n = 2 if fp32 else 1
-        part = {1: 2.0 ** -8, 2: 2.0 ** -16}[n] + planes(b_dtype, n) * (1 if n == 1 else 2)
+        n = 3 if fp32 else 1
+        # g; an fp32 operand that meets it; two pairs that are left out of three planes each
+        part = 2.0 ** (-8 * n) * (1 if b_dtype == BF16 else 4 if fp32 else 2)
         size = a.abs() @ b.abs()
         # a plane's value below 2^-126, BF16's smallest normal one, counts as 0: a factor in n planes is off
         # by 2^-126 for each (an exponential of -88 times a token of 512 is 2^-118, and passes TINY)
         lost = n * 2.0 ** -126 * (b.abs().sum(0) + a.abs().sum(1, keepdim=True))
-        return a @ b, 1.01 * (a_tol @ b.abs()) + (1.01 * part + 4 * math.sqrt(3 * rows + 4) * U) * size + lost
+        return a @ b, 1.01 * (a_tol @ b.abs()) + (1.01 * part + 4 * math.sqrt(6 * rows + 4) * U) * size + lost
 
     dx, dx_tol = product(vocab, g, g_tol, w64, w.dtype, x.dtype == F32)
     x64 = torch.where(there, x64, 0.0)
