@@ -90,14 +90,6 @@ __device__ __forceinline__ void store_out(const F8Matmul &f, int64_t at, int hav
 constexpr int kSliceBytes = kF8Block;  // bytes, i.e. values, of k per row and slice
 constexpr int kStages = 2;
 
-// The same of 4 bytes a lane (see load16_lds).
-__device__ __forceinline__ void load4_lds(uint32_t lds, uint32_t offset, u32x4 buffer) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds), "v"(offset), "s"(buffer)
-                 : "memory");
-}
-
 // LDS byte of 16-byte chunk c of a slice's row r.
 __device__ __forceinline__ uint32_t slice_at(int r, int c) {
     return (uint32_t)(r * kSliceBytes + ((c ^ ((r >> 1) & 7)) << 4));

@@ -180,7 +180,7 @@ struct LossPlan {
     int64_t piece, pitch;
     int32_t splits;               // of dx
     bool accumulate;              // dx over several pieces in a buffer of its own
-    size_t x, w, partial, state, target, g, dx, sums, total;
+    size_t x, w, partial, state, target, row[3], g, dx, sums, total;
 };
 
 LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int w_dtype) {
@@ -228,6 +228,7 @@ LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t 
     };
     p.x = section(loss_planes(x_dtype) * rows * p.pitch * 2);
     p.w = section(w_row * p.piece);
+    for (size_t &r : p.row) r = section(rows * 4);
     p.g = section(entry * rows * p.piece);
     p.dx = section(p.accumulate ? rows * cols * (int64_t)sizeof(float) : 0);
     p.sums = section(p.splits > 1 ? p.splits * rows * cols * (int64_t)sizeof(float) : 0);
@@ -265,21 +266,16 @@ void loss_operand(const void *(&planes)[sm::kLossPlanes], int n, const void *at,
     for (int i = 0; i < n; ++i) planes[i] = static_cast<const uint16_t *>(at) + i * plane_entries;
 }
 
-int loss_split_planes(const void *in, int dtype, int64_t rows, int64_t cols, int64_t pitch, void *to,
-                      const void *targets, bool targets64, int64_t vocab, hipStream_t st) {
+sm::LossPlanes loss_to_planes(const void *in, int dtype, int64_t rows, int64_t cols, int64_t pitch, void *to) {
     sm::LossPlanes f{};
     f.in = in;
     f.planes = loss_planes(dtype);
     for (int i = 0; i < f.planes; ++i) f.out[i] = static_cast<uint16_t *>(to) + i * rows * pitch;
-    f.targets = targets;
-    f.targets64 = targets64;
     f.rows = rows;
     f.cols = cols;
     f.pitch = pitch;
-    f.vocab = vocab;
     f.bf16 = dtype == SIGNMUON_BF16;
-    sm::launch_loss_planes(f, st);
-    return sm::launch_status();
+    return f;
 }
 
 inline int64_t entry_bytes(int dtype) { return dtype == SIGNMUON_BF16 ? 2 : 4; }
@@ -649,14 +645,17 @@ int signmuon_linear_cross_entropy(const void *x, signmuon_dtype x_dtype, const v
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const bool direct_x = loss_direct(x_dtype, cols), direct_w = loss_direct(w_dtype, cols);
     const int nx = loss_planes(x_dtype), nw = loss_planes(w_dtype);
-    if (!direct_x)
-        if (int rc = loss_split_planes(x, x_dtype, tokens, cols, p.pitch, ws + p.x, nullptr, false, vocab, st)) return rc;
+    if (!direct_x) {
+        sm::launch_loss_planes(loss_to_planes(x, x_dtype, tokens, cols, p.pitch, ws + p.x), st);
+        if (int rc = sm::launch_status()) return rc;
+    }
     for (int64_t v0 = 0; v0 < vocab; v0 += p.piece) {
         const int64_t here = vocab - v0 < p.piece ? vocab - v0 : p.piece;
         const void *rows = at_entry(w, v0 * cols, w_dtype);
-        if (!direct_w)
-            if (int rc = loss_split_planes(rows, w_dtype, here, cols, p.pitch, ws + p.w, nullptr, false, vocab, st))
-                return rc;
+        if (!direct_w) {
+            sm::launch_loss_planes(loss_to_planes(rows, w_dtype, here, cols, p.pitch, ws + p.w), st);
+            if (int rc = sm::launch_status()) return rc;
+        }
         sm::LossTile f{};
         loss_operand(f.a, nx, direct_x ? x : ws + p.x, tokens * p.pitch);
         loss_operand(f.b, nw, direct_w ? rows : ws + p.w, here * p.pitch);
@@ -667,13 +666,11 @@ int signmuon_linear_cross_entropy(const void *x, signmuon_dtype x_dtype, const v
         f.batch = 1;
         loss_pairs(f, nx, nw);
         loss_tiles(f, 1, sm::kLossSlice);
-        f.targets = targets;
-        f.targets64 = target_type == SIGNMUON_I64;
+        f.rows[0] = targets;
+        f.row_step = target_type == SIGNMUON_I64 ? 8 : 4;
         f.partial = reinterpret_cast<float2 *>(ws + p.partial);
         f.target = reinterpret_cast<float *>(ws + p.target);
-        f.vocab = vocab;
         f.vocab0 = v0;
-        f.scale = scale;
         f.factor = scale * kLog2E;
         sm::launch_loss_logits(f, false, st);
         if (int rc = sm::launch_status()) return rc;
@@ -682,7 +679,7 @@ int signmuon_linear_cross_entropy(const void *x, signmuon_dtype x_dtype, const v
         j.state = reinterpret_cast<float2 *>(ws + p.state);
         j.target = f.target;
         j.targets = targets;
-        j.targets64 = f.targets64;
+        j.targets64 = target_type == SIGNMUON_I64;
         j.loss = loss;
         j.lse = lse;
         j.rows = tokens;
@@ -724,21 +721,33 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
     char *ws = static_cast<char *>(workspace);
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const int64_t rows = workers * tokens;
-    const bool direct_w = loss_direct(w_dtype, cols), targets64 = target_type == SIGNMUON_I64;
+    const bool direct_w = loss_direct(w_dtype, cols);
     const bool x32 = x_dtype == SIGNMUON_F32, grad32 = grad_dtype == SIGNMUON_F32;
     const int nx = loss_planes(x_dtype), nw = loss_planes(w_dtype);
     void *const g = ws + p.g;
     const bool g32 = (x32 && dx) || (grad32 && dw);
     const int64_t g_entry = g32 ? 4 : 2, g_slice = g32 ? sm::kLossWideSlice : sm::kLossSlice;
-    if (int rc = loss_split_planes(x, x_dtype, rows, cols, p.pitch, ws + p.x, targets, targets64, vocab, st)) return rc;
+    sm::LossPlanes xs = loss_to_planes(x, x_dtype, rows, cols, p.pitch, ws + p.x);
+    xs.targets = targets;
+    xs.targets64 = target_type == SIGNMUON_I64;
+    xs.lse = lse;
+    xs.dloss = dloss;
+    xs.row_target = reinterpret_cast<int32_t *>(ws + p.row[0]);
+    xs.row_base = reinterpret_cast<float *>(ws + p.row[1]);
+    xs.row_d = reinterpret_cast<float *>(ws + p.row[2]);
+    xs.vocab = vocab;
+    xs.scale = scale;
+    sm::launch_loss_planes(xs, st);
+    if (int rc = sm::launch_status()) return rc;
     for (int64_t v0 = 0; v0 < vocab; v0 += p.piece) {
         const int64_t here = vocab - v0 < p.piece ? vocab - v0 : p.piece;
         const int64_t g_pitch = (here + sm::kLossTile - 1) / sm::kLossTile * sm::kLossTile;
         const bool first = v0 == 0, last = v0 + here == vocab;
         const void *w_rows = at_entry(w, v0 * cols, w_dtype);
-        if (!direct_w)
-            if (int rc = loss_split_planes(w_rows, w_dtype, here, cols, p.pitch, ws + p.w, nullptr, false, vocab, st))
-                return rc;
+        if (!direct_w) {
+            sm::launch_loss_planes(loss_to_planes(w_rows, w_dtype, here, cols, p.pitch, ws + p.w), st);
+            if (int rc = sm::launch_status()) return rc;
+        }
         sm::LossTile f{};
         loss_operand(f.a, nx, ws + p.x, rows * p.pitch);
         loss_operand(f.b, nw, direct_w ? w_rows : ws + p.w, here * p.pitch);
@@ -749,16 +758,12 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
         f.batch = 1;
         loss_pairs(f, nx, nw);
         loss_tiles(f, 1, sm::kLossSlice);
-        f.targets = targets;
-        f.targets64 = targets64;
-        f.lse = lse;
-        f.dloss = dloss;
+        for (int i = 0; i < 3; ++i) f.rows[i] = ws + p.row[i];
+        f.row_step = 4;
         f.g = g;
         f.g32 = g32;
         f.g_pitch = g_pitch;
-        f.vocab = vocab;
         f.vocab0 = v0;
-        f.scale = scale;
         f.factor = scale * kLog2E;
         sm::launch_loss_logits(f, true, st);
         if (int rc = sm::launch_status()) return rc;

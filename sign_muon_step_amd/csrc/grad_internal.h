@@ -172,8 +172,13 @@ inline int64_t loss_pitch(int64_t cols) { return (cols + 7) / 8 * 8; }  // entri
 struct LossPlanes {
     const void *in;
     uint16_t *out[kLossPlanes];
-    const void *targets;  // of the rows, or null: rows without a target become zeros
+    const void *targets;  // of the rows, or null: rows without a target become zeros, and
+                          // each row's target (-1: none), lse / log 2 and scale * dloss are written
+    const float *lse, *dloss;
+    int32_t *row_target;
+    float *row_base, *row_d;
     int64_t rows, cols, pitch, vocab;
+    float scale;
     int32_t planes;
     bool bf16, targets64;
 };
@@ -192,15 +197,14 @@ struct LossTile {
     int32_t planes;            // of an fp32 a: 1 or 3
     bool g32;                  // g is fp32, not BF16
     // logits
-    const void *targets;
-    const float *lse, *dloss;
+    const void *rows[3];       // 4 bytes a row, row_step bytes apart: the targets, and for g what LossPlanes writes
+    int32_t row_step;
     float2 *partial;           // [columns of tile / 2][m]: maximum and sum, in units of log 2
     float *target;             // [m] logit of the target
     void *g;                   // [m][g_pitch]
     int64_t g_pitch;
-    int64_t vocab, vocab0;     // vocab0: the piece's first entry
-    float scale, factor;       // factor: scale / log 2
-    bool targets64;
+    int64_t vocab0;            // the piece's first entry
+    float factor;              // scale / log 2
     // values
     const void *prev;          // added; null: nothing
     void *out;
@@ -565,6 +569,14 @@ __device__ __forceinline__ void load16_lds(uint32_t lds, uint32_t offset, u32x4 
                  : "s"(lds), "v"(offset), "s"(buffer)
                  : "memory");
 }
+// The same of 4 bytes a lane, at lds + 4 * lane.
+__device__ __forceinline__ void load4_lds(uint32_t lds, uint32_t offset, u32x4 buffer) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(offset), "s"(buffer)
+                 : "memory");
+}
+
 // A raw buffer over `bytes` bytes (below 2^31) from p on.
 __device__ __forceinline__ u32x4 make_buffer(const uint8_t *p, int64_t bytes) {
     const uint64_t a = reinterpret_cast<uint64_t>(p);

@@ -36,7 +36,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-constexpr int kWaves = 4, kStages = 2;
+constexpr int kWaves = 4;
 
 // ---------------------------------------------------------------------------
 // Operands
@@ -88,21 +88,18 @@ struct Operand {
             return *reinterpret_cast<const bf16x8 *>(slice + row * kLine + ((c ^ ((row >> 1) & 7)) << 4));
         }
     }
-    // The same of an fp32 operand.
-    static __device__ __forceinline__ void read(const char *slice, int w0, int i, int s, int lane, float (&v)[8]) {
+    // The same of an fp32 operand, the lane's first or last 4 k.
+    static __device__ __forceinline__ void read(const char *slice, int w0, int i, int s, int lane, int part, float (&v)[8]) {
         const int half = lane >> 5;
         if constexpr (KIND == kCols32) {
             const char *p = slice + (2 * s + half) * (8 * kLine + kPad) + (w0 + i * 32 + (lane & 31)) * 4;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const float *>(p + j * kLine);
+            for (int j = 4 * part; j < 4 * part + 4; ++j) v[j] = *reinterpret_cast<const float *>(p + j * kLine);
         } else {
-            const int row = w0 + i * 32 + (lane & 31), c = 4 * s + 2 * half;
+            const int row = w0 + i * 32 + (lane & 31), c = 4 * s + 2 * half + part;
+            const f32x4 q = *reinterpret_cast<const f32x4 *>(slice + row * kLine + ((c ^ ((row >> 1) & 7)) << 4));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const f32x4 q = *reinterpret_cast<const f32x4 *>(slice + row * kLine + (((c + h) ^ ((row >> 1) & 7)) << 4));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[4 * h + j] = q[j];
-            }
+            for (int j = 0; j < 4; ++j) v[4 * part + j] = q[j];
         }
     }
 };
@@ -139,20 +136,26 @@ __device__ __forceinline__ Tile tile_at(const LossTile &f, int v, int total) {
 // stay; a slice is a buffer's start and length. What lies outside an operand, and
 // slices past the last tile's, lie beyond the length and give zeros. Columns past
 // the last one of an operand whose rows are k hold what follows in memory, and end
-// in results that are not kept.
-template <int KA, int KB, int TILE, int SLICE>
+// in results that are not kept. A tile's row data (ROWS arrays of 4 bytes a row)
+// come with its first slice.
+template <int KA, int KB, int TILE, int SLICE, int STAGES, int ROWS>
 struct Loader {
     using A = Operand<KA, TILE, SLICE>;
     using B = Operand<KB, TILE, SLICE>;
-    static constexpr int kLoads = A::kLoads + B::kLoads, kStage = A::kBytes + B::kBytes;
+    static constexpr int kLoads = A::kLoads + B::kLoads, kStage = A::kBytes + B::kBytes, kStages = STAGES;
+    // row data lie apart, in a set for each tile whose data may still be read, or under
+    // way: with one slice a tile, the tile before and those of the next three slices
+    static constexpr int kRowSets = 4, kRowSet = ROWS * TILE * 4, kRowData = STAGES * kStage;
+    static constexpr int kBytes = kRowData + kRowSets * kRowSet;
     u32x4 buffer[2];
     uint32_t at[2], past[2], step[2];  // of the lane's first load, where the slice's k ends; between loads
     int chunk[2];
     int v, slice, end;  // the tile, the next slice to load and the end of its slices
     int per, ks, pair;  // slices of a pair of planes; the slice's place in them
+    unsigned tiles;     // so far
     Tile t;
 
-    __device__ __forceinline__ void start(const LossTile &f, int v_, int total, int wave, int lane) {
+    __device__ __forceinline__ void start(const LossTile &f, int v_, int total, uint32_t lds, int wave, int lane) {
         chunk[0] = A::chunk(wave, lane);
         chunk[1] = B::chunk(wave, lane);
         at[0] = (uint32_t)(A::row(wave, lane) * f.a_pitch + chunk[0] * 16);
@@ -161,9 +164,10 @@ struct Loader {
         step[1] = (uint32_t)first_lane((int)(kWaves * B::kRows * f.b_pitch));
         per = (int)((f.k + SLICE - 1) / SLICE);
         v = v_;
-        tile(f, total);
+        tiles = 0;
+        tile(f, total, lds, wave, lane);
     }
-    __device__ __forceinline__ void tile(const LossTile &f, int total) {
+    __device__ __forceinline__ void tile(const LossTile &f, int total, uint32_t lds, int wave, int lane) {
         const bool there = v < total;
         t = tile_at<TILE>(f, there ? v : 0, total);
         slice = t.split * f.chunk;
@@ -171,6 +175,15 @@ struct Loader {
         pair = first_lane(slice / per);
         ks = slice - pair * per;
         place(f, there);
+        const int have = (int)(f.m - t.row0 < TILE ? f.m - t.row0 : TILE);
+        if (ROWS && wave * kWave < TILE)
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i)
+                load4_lds(lds + kRowData + tiles % kRowSets * kRowSet + (uint32_t)(i * TILE * 4 + wave * 256),
+                          (uint32_t)((wave * kWave + lane) * f.row_step),
+                          make_buffer(static_cast<const uint8_t *>(f.rows[i]) + t.row0 * f.row_step,
+                                      there ? have * f.row_step : 0));
+        ++tiles;
     }
     // A slice's buffer, from the slice's k on, and where its k ends.
     template <class O>
@@ -218,10 +231,10 @@ struct Loader {
                    buffer[o]);
     }
     // On to the next slice.
-    __device__ __forceinline__ void advance(const LossTile &f, int total) {
+    __device__ __forceinline__ void advance(const LossTile &f, int total, uint32_t lds, int wave, int lane) {
         if (++slice == end) {
             v += gridDim.x;
-            tile(f, total);
+            tile(f, total, lds, wave, lane);
         } else if (++ks == per) {
             ks = 0;
             ++pair;
@@ -232,10 +245,6 @@ struct Loader {
         }
     }
 };
-
-__device__ __forceinline__ int64_t target_of(const LossTile &f, int64_t row) {
-    return f.targets64 ? static_cast<const int64_t *>(f.targets)[row] : static_cast<const int32_t *>(f.targets)[row];
-}
 
 // Column of value e of a lane's block n, from the wave's first on.
 __device__ __forceinline__ int column(int n, int e, int lane) { return n * 32 + e / 4 * 8 + (lane >> 5) * 4 + e % 4; }
@@ -257,16 +266,17 @@ __device__ __forceinline__ void clear(Acc<F> &acc) {
 // LDS so that whole lines are written. out: the wave's first entry, rows of `pitch`
 // entries, of which `rows` and `cols` exist. Where rows begin at whole vectors,
 // buffer stores, which drop what lies outside; otherwise plain stores.
-constexpr int out_bytes(int F) { return F * 32; }              // of a row at a time
-constexpr int out_pitch(int F) { return out_bytes(F) + 16; }
-constexpr int out_lds(int F) { return 32 * out_pitch(F); }     // of a wave
+// BYTES: of a row at a time.
+constexpr int out_lds(int bytes) { return 32 * (bytes + 16); }  // of a wave
+// Buffer stores of a wave and tile: as many as these at least where rows are whole vectors.
+constexpr int out_stores(int F, bool wide) { return F * F * 32 * 32 * (wide ? 4 : 2) / 1024; }
 
-template <int F, bool WIDE, class G>
+template <int F, bool WIDE, int BYTES, class G>
 __device__ __forceinline__ void write(Acc<F> &acc, char *mine, void *out, int64_t pitch, int rows, int cols, int lane,
                                       G &&group) {
-    constexpr int E = WIDE ? 4 : 2, W = 16 / E;                 // bytes of a value, values of a store
-    constexpr int kCols = out_bytes(F) / E;                     // columns at a time
-    constexpr int kLanes = out_bytes(F) / 16, kRows = kWave / kLanes;  // lanes of a row, rows of a store
+    constexpr int E = WIDE ? 4 : 2, W = 16 / E;               // bytes of a value, values of a store
+    constexpr int kCols = BYTES / E, kPitch = BYTES + 16;     // columns at a time
+    constexpr int kLanes = BYTES / 16, kRows = kWave / kLanes;  // lanes of a row, rows of a store
     static_assert(kCols % 8 == 0 && F * 32 % kCols == 0, "whole passes");
     // made anew for each tile, so that no address is kept in registers meanwhile
     asm volatile("" : "+v"(lane));
@@ -287,7 +297,7 @@ __device__ __forceinline__ void write(Acc<F> &acc, char *mine, void *out, int64_
             for (int n = n0 / 32; n < (n0 + kCols + 31) / 32; ++n) pin(acc[i][n]);
 #pragma unroll
             for (int n = n0; n < n0 + kCols; n += 8) {
-                char *to = mine + row * out_pitch(F) + (n - n0 + half * 4) * E;
+                char *to = mine + row * kPitch + (n - n0 + half * 4) * E;
                 float v[4];
                 group(i, n / 32, n % 32 / 8, v);
                 if constexpr (WIDE)
@@ -298,7 +308,7 @@ __device__ __forceinline__ void write(Acc<F> &acc, char *mine, void *out, int64_
             // lanes read what others wrote (LDS accesses of a wave keep their order)
             asm volatile("" ::: "memory");
             __builtin_amdgcn_wave_barrier();
-            auto staged = [&](int r) { return *reinterpret_cast<const u32x4 *>(mine + (r * kRows + r0) * out_pitch(F) + c16 * 16); };
+            auto staged = [&](int r) { return *reinterpret_cast<const u32x4 *>(mine + (r * kRows + r0) * kPitch + c16 * 16); };
             if (even) {
                 const uint32_t at = n0 + c16 * W < cols ? (uint32_t)(r0 * step + (n0 + c16 * W) * E) : kOutside;
                 u32x4 v[32 / kRows];
@@ -319,7 +329,7 @@ __device__ __forceinline__ void write(Acc<F> &acc, char *mine, void *out, int64_
 #pragma unroll 1
                     for (int c = here / W * W; c < here; ++c) {
                         char *q = p + (int64_t)(i * 32 + row) * step + (n0 + c) * E;
-                        const char *from = mine + row * out_pitch(F) + c * E;
+                        const char *from = mine + row * kPitch + c * E;
                         if constexpr (WIDE)
                             *reinterpret_cast<uint32_t *>(q) = *reinterpret_cast<const uint32_t *>(from);
                         else
@@ -336,63 +346,64 @@ __device__ __forceinline__ void write(Acc<F> &acc, char *mine, void *out, int64_
 // A row's maximum and sum of exponentials over the wave's columns, and the target's
 // logit, in units of log 2.
 template <int F>
-__device__ __forceinline__ void finish_lse(const LossTile &f, Acc<F> &acc, int64_t row0, int64_t col0, int lane) {
+__device__ __forceinline__ void finish_lse(const LossTile &f, Acc<F> &acc, const char *targets, int64_t row0,
+                                           int64_t col0, int lane) {
     constexpr int kCols = F * 32;
-    if (col0 < f.n) {
-        const int have = (int)(f.n - col0 < kCols ? f.n - col0 : kCols);
-        int target[F];  // column, or -1
+    const int have = (int)(f.n - col0 < 0 ? 0 : f.n - col0 < kCols ? f.n - col0 : kCols);
+    const int rows = (int)(f.m - row0 < 0 ? 0 : f.m - row0 < kCols ? f.m - row0 : kCols);
+    // stores that are always issued, so that their number is known: what lies outside is dropped
+    const __amdgpu_buffer_rsrc_t partial =
+        __builtin_amdgcn_make_buffer_rsrc(f.partial + (col0 / kCols) * f.m + row0, 0, have > 0 ? rows * 8 : 0, 0x00020000);
 #pragma unroll
-        for (int i = 0; i < F; ++i) {
-            const int64_t row = row0 + i * 32 + (lane & 31);
-            const int64_t at = row < f.m ? target_of(f, row) - f.vocab0 - col0 : -1;
-            target[i] = at >= 0 && at < have ? (int)at : -1;
+    for (int i = 0; i < F; ++i) {
+        const int row = i * 32 + (lane & 31);
+        // the low half of a target of 64 bits: one outside the vocabulary may seem to be inside, and its
+        // logit is not used
+        const uint32_t at = *reinterpret_cast<const uint32_t *>(targets + row * 4) - (uint32_t)(f.vocab0 + col0);
+        const int target = at < (uint32_t)have && row < rows ? (int)at : -1;
+        float l[F][16], top = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < F; ++n) {
+            pin(acc[i][n]);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) l[n][e] = acc[i][n][e] * f.factor;
         }
-#pragma unroll
-        for (int i = 0; i < F; ++i) {
-            const int64_t row = row0 + i * 32 + (lane & 31);
-            float l[F][16], top = -INFINITY;
-#pragma unroll
-            for (int n = 0; n < F; ++n) {
-                pin(acc[i][n]);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) l[n][e] = acc[i][n][e] * f.factor;
-            }
-            if (have < kCols)
-#pragma unroll
-                for (int n = 0; n < F; ++n)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) l[n][e] = column(n, e, lane) < have ? l[n][e] : -INFINITY;
+        if (have < kCols)
 #pragma unroll
             for (int n = 0; n < F; ++n)
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) top = fmaxf(fmaxf(l[n][e], l[n][e + 1]), top);
-            top = fmaxf(top, __shfl_xor(top, 32));
-            if (__any(target[i] >= 0)) {
+                for (int e = 0; e < 16; ++e) l[n][e] = column(n, e, lane) < have ? l[n][e] : -INFINITY;
 #pragma unroll
-                for (int n = 0; n < F; ++n)
+        for (int n = 0; n < F; ++n)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (column(n, e, lane) == target[i]) f.target[row] = l[n][e];
-            }
-            const float base = top == -INFINITY ? 0.0f : top;  // a block of minus infinities adds nothing
-            float sum[2] = {};
+            for (int e = 0; e < 16; e += 2) top = fmaxf(fmaxf(l[n][e], l[n][e + 1]), top);
+        top = fmaxf(top, __shfl_xor(top, 32));
+        if (__any(target >= 0)) {
 #pragma unroll
             for (int n = 0; n < F; ++n)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) sum[e & 1] += __builtin_amdgcn_exp2f(l[n][e] - base);
-            sum[0] += sum[1];
-            sum[0] += __shfl_xor(sum[0], 32);
-            if (row < f.m && lane < 32) f.partial[(col0 / kCols) * f.m + row] = make_float2(top, sum[0]);
-            __builtin_amdgcn_sched_barrier(0);
+                for (int e = 0; e < 16; ++e)
+                    if (column(n, e, lane) == target) f.target[row0 + row] = l[n][e];
         }
+        const float base = top == -INFINITY ? 0.0f : top;  // a block of minus infinities adds nothing
+        float sum[2] = {};
+#pragma unroll
+        for (int n = 0; n < F; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum[e & 1] += __builtin_amdgcn_exp2f(l[n][e] - base);
+        sum[0] += sum[1];
+        sum[0] += __shfl_xor(sum[0], 32);
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(top), __float_as_uint(sum[0])}, partial,
+                                              lane < 32 ? row * 8 : (int)kOutside, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
     }
     clear<F>(acc);
 }
 
 // g; zeros in the columns past the vocabulary that a tile has.
 template <int F, bool WIDE>
-__device__ __forceinline__ void finish_grad(const LossTile &f, Acc<F> &acc, char *mine, int64_t row0, int64_t col0,
-                                            int lane) {
+__device__ __forceinline__ void finish_grad(const LossTile &f, Acc<F> &acc, char *mine, const char *data, int64_t row0,
+                                            int64_t col0, int lane) {
     constexpr int kCols = F * 32;
     const int have = (int)(f.n - col0 < 0 ? 0 : f.n - col0 < kCols ? f.n - col0 : kCols);
     int target[F], limit[F];  // of the lane's rows: the target's column, and the columns that count
@@ -400,21 +411,21 @@ __device__ __forceinline__ void finish_grad(const LossTile &f, Acc<F> &acc, char
     bool any = false, whole = true;
 #pragma unroll
     for (int i = 0; i < F; ++i) {
-        const int64_t row = row0 + i * 32 + (lane & 31);
-        const bool in = row < f.m;
-        const int64_t t = in ? target_of(f, row) : -1, at = t - f.vocab0 - col0;
+        // the rows' targets (-1: none), lse / log 2 and scale * dloss
+        const char *p = data + (i * 32 + (lane & 31)) * 4;
+        const int t = *reinterpret_cast<const int *>(p);
+        base[i] = *reinterpret_cast<const float *>(p + 2 * kCols * 4);
+        d[i] = *reinterpret_cast<const float *>(p + 4 * kCols * 4);
+        const uint32_t at = (uint32_t)t - (uint32_t)(f.vocab0 + col0);
+        target[i] = t >= 0 && at < (uint32_t)have ? (int)at : -1;
         // a token without a target has no gradient, whatever its logits are
-        const bool there = t >= 0 && t < f.vocab;
-        d[i] = there ? f.scale * f.dloss[row] : 0.0f;
-        base[i] = there ? f.lse[row] * kLog2E : 0.0f;
-        target[i] = there && at >= 0 && at < have ? (int)at : -1;
-        limit[i] = there ? have : 0;
+        limit[i] = t >= 0 ? have : 0;
         any |= target[i] >= 0;
         whole &= limit[i] == kCols;
     }
     const bool plain = __all(whole && !any);
-    write<F, WIDE>(acc, mine, reinterpret_cast<char *>(f.g) + (row0 * f.g_pitch + col0) * (WIDE ? 4 : 2), f.g_pitch,
-                   (int)(f.m - row0 < kCols ? f.m - row0 : kCols), kCols, lane,
+    write<F, WIDE, F * 32>(acc, mine, static_cast<char *>(f.g) + (row0 * f.g_pitch + col0) * (WIDE ? 4 : 2), f.g_pitch,
+                           (int)(f.m - row0 < kCols ? f.m - row0 : kCols), kCols, lane,
                    [&](int i, int n, int q, float(&v)[4]) {
 #pragma unroll
                        for (int j = 0; j < 4; ++j)
@@ -433,12 +444,12 @@ __device__ __forceinline__ void finish_grad(const LossTile &f, Acc<F> &acc, char
 }
 
 // A product's values, added to what `prev` holds.
-template <int F, bool WIDE>
+template <int F, bool WIDE, int BYTES>
 __device__ __forceinline__ void finish_values(const LossTile &f, Acc<F> &acc, char *mine, const Tile &t, int64_t row0,
                                               int64_t col0, int lane) {
     const int64_t first = (f.out_batch * (t.split * (int64_t)f.batch + t.batch) + row0) * f.n + col0;
     const int rows = (int)(f.m - row0 < F * 32 ? f.m - row0 : F * 32), cols = (int)(f.n - col0 < F * 32 ? f.n - col0 : F * 32);
-    write<F, WIDE>(acc, mine, static_cast<char *>(f.out) + first * (WIDE ? 4 : 2), f.n, rows, cols, lane,
+    write<F, WIDE, BYTES>(acc, mine, static_cast<char *>(f.out) + first * (WIDE ? 4 : 2), f.n, rows, cols, lane,
                    [&](int i, int n, int q, float(&v)[4]) {
 #pragma unroll
                        for (int j = 0; j < 4; ++j) v[j] = acc[i][n][q * 4 + j];
@@ -466,7 +477,7 @@ __device__ __forceinline__ void hold(const bf16x8 &v) { asm volatile("" : : "v"(
 // run out of them.
 template <class L>
 __device__ __forceinline__ uint32_t stage_of(uint32_t lds, unsigned c, int wave) {
-    uint32_t to = lds + c % kStages * L::kStage + (uint32_t)wave * 1024u;
+    uint32_t to = lds + c % L::kStages * L::kStage + (uint32_t)wave * 1024u;
     asm volatile("" : "+s"(to));
     return to;
 }
@@ -479,24 +490,25 @@ enum { kLse, kGrad, kValues };
 // WIDE: results in fp32.
 template <int KA, int KB, int TILE, int END, bool WIDE>
 __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_tile_kernel(LossTile f, int total) {
-    using L = Loader<KA, KB, TILE, kLossSlice>;
+    constexpr int kRowArrays = END == kLse ? 1 : END == kGrad ? 3 : 0;
+    using L = Loader<KA, KB, TILE, kLossSlice, 2, kRowArrays>;
     using A = typename L::A;
     using B = typename L::B;
     constexpr int F = TILE / 64;  // 32 x 32 blocks of a wave, each way
-    constexpr int kOut = kStages * L::kStage;
-    __shared__ __attribute__((aligned(1024))) char lds[kOut + (END == kLse ? 0 : kWaves * out_lds(F))];
+    constexpr int kOut = L::kBytes, kOutWave = END == kLse ? 0 : out_lds(F * 32);
+    __shared__ __attribute__((aligned(1024))) char lds[kOut + kWaves * kOutWave];
     const int lane = threadIdx.x & (kWave - 1), wave = first_lane(threadIdx.x / kWave);
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char *)lds);
     const int wm = wave / 2 * (TILE / 2), wn = wave % 2 * (TILE / 2);
 
     L loader;
-    loader.start(f, blockIdx.x, total, wave, lane);
+    loader.start(f, blockIdx.x, total, lds0, wave, lane);
 #pragma unroll 1
-    for (unsigned c = 0; c < kStages; ++c) {
+    for (unsigned c = 0; c < L::kStages; ++c) {
         const uint32_t to = stage_of<L>(lds0, c, wave);
 #pragma unroll
         for (int i = 0; i < L::kLoads; ++i) loader.issue(i, to);
-        loader.advance(f, total);
+        loader.advance(f, total, lds0, wave, lane);
     }
 
     // The fragments of half a slice (32 k) in registers, b's F and a's F, 16 k each.
@@ -504,7 +516,7 @@ __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_tile_
     bf16x8 fr[2][2][2 * F];  // [half][16 k][block]
     auto read = [&](auto h, unsigned c, int r) {  // of half h of slice c
         constexpr int H = decltype(h)::value;
-        const char *stage = lds + c % kStages * L::kStage;
+        const char *stage = lds + c % L::kStages * L::kStage;
         const int s = r / (2 * F), i = r % (2 * F);
         fr[H][s][i] = i < F ? B::read(stage + A::kBytes, wn, i, 2 * H + s, lane) : A::read(stage, wm, i - F, 2 * H + s, lane);
     };
@@ -543,37 +555,52 @@ __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_tile_
         if (s + gone >= kMeet && (s + gone - kMeet) % kSpread == 0 && (s + gone - kMeet) / kSpread < L::kLoads)
             loader.issue((s + gone - kMeet) / kSpread, to);
     };
+    // A tile's results are on their way to memory during the next one's first slice:
+    // there, only what is older than their stores is waited for.
+    constexpr int kStores = END == kLse ? F : out_stores(F, WIDE), kBehind = kStores < 63 ? kStores : 63;
+    const bool even = END != kValues || f.n % (WIDE ? 4 : 8) == 0;  // the stores' number is known
+    bool behind = false;
     const int per = loader.per;
     unsigned c = 0;  // slices so far
+    // `newer`: operations that may be under way behind the loads of slice c + 1
+    auto slice = [&](auto newer) {
+        const uint32_t to = stage_of<L>(lds0, c, wave);
+        products(kLow, [&](int s) {
+            if (s == kMeet) {
+#pragma unroll
+                for (int r = 0; r < kReads; ++r) hold(fr[1][r / (2 * F)][r % (2 * F)]);
+                wait_loads<decltype(newer)::value>();
+                barrier();
+            }
+            steps(kHigh, c, to, s, 0);
+        });
+        products(kHigh, [&](int s) { steps(kLow, c + 1, to, s, kSteps); });
+#pragma unroll
+        for (int i = 0; i < F * F; ++i) pin(acc[i / F][i % F]);
+        loader.advance(f, total, lds0, wave, lane);
+        ++c;
+    };
+    unsigned tile = 0;
 #pragma unroll 1
-    for (int v = blockIdx.x; v < total; v += gridDim.x) {
+    for (int v = blockIdx.x; v < total; v += gridDim.x, ++tile) {
         const Tile t = tile_at<TILE>(f, v, total);
-        const int begin = t.split * f.chunk;
-        const int end = begin + f.chunk < f.pairs * per ? begin + f.chunk : f.pairs * per;
-#pragma unroll 1
-        for (int j = begin; j < end; ++j, ++c) {
-            const uint32_t to = stage_of<L>(lds0, c, wave);
-            products(kLow, [&](int s) {
-                if (s == kMeet) {
-#pragma unroll
-                    for (int r = 0; r < kReads; ++r) hold(fr[1][r / (2 * F)][r % (2 * F)]);
-                    wait_loads<0>();
-                    barrier();
-                }
-                steps(kHigh, c, to, s, 0);
-            });
-            products(kHigh, [&](int s) { steps(kLow, c + 1, to, s, kSteps); });
-#pragma unroll
-            for (int i = 0; i < F * F; ++i) pin(acc[i / F][i % F]);
-            loader.advance(f, total);
+        int j = t.split * f.chunk;
+        const int end = j + f.chunk < f.pairs * per ? j + f.chunk : f.pairs * per;
+        if (behind) {
+            slice(std::integral_constant<int, kBehind>{});
+            ++j;
         }
-        char *mine = lds + kOut + wave * out_lds(F);
+#pragma unroll 1
+        for (; j < end; ++j) slice(kLow);
+        char *mine = lds + kOut + wave * kOutWave;
+        const char *data = lds + L::kRowData + tile % L::kRowSets * L::kRowSet + wm * 4;
         if constexpr (END == kLse)
-            finish_lse<F>(f, acc, t.row0 + wm, t.col0 + wn, lane);
+            finish_lse<F>(f, acc, data, t.row0 + wm, t.col0 + wn, lane);
         else if constexpr (END == kGrad)
-            finish_grad<F, WIDE>(f, acc, mine, t.row0 + wm, t.col0 + wn, lane);
+            finish_grad<F, WIDE>(f, acc, mine, data, t.row0 + wm, t.col0 + wn, lane);
         else
-            finish_values<F, WIDE>(f, acc, mine, t, t.row0 + wm, t.col0 + wn, lane);
+            finish_values<F, WIDE, F * 32>(f, acc, mine, t, t.row0 + wm, t.col0 + wn, lane);
+        behind = even;
     }
     wait_loads<0>();  // loads past the last tile write LDS too
 }
@@ -583,53 +610,54 @@ __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_tile_
 // is 32 k: while 16 of them are multiplied, the next 16 are read and taken apart.
 template <int KA, int TILE, int PLANES, bool WIDE>
 __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_wide_kernel(LossTile f, int total) {
-    using L = Loader<KA, kCols16, TILE, kLossWideSlice>;
+    using L = Loader<KA, kCols16, TILE, kLossWideSlice, 3, 0>;
     using A = typename L::A;
     using B = typename L::B;
     constexpr int F = TILE / 64;
-    constexpr int kOut = kStages * L::kStage;
-    __shared__ __attribute__((aligned(1024))) char lds[kOut + kWaves * out_lds(F)];
+    constexpr int kOut = L::kBytes, kOutBytes = F * 16;
+    __shared__ __attribute__((aligned(1024))) char lds[kOut + kWaves * out_lds(kOutBytes)];
     const int lane = threadIdx.x & (kWave - 1), wave = first_lane(threadIdx.x / kWave);
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char *)lds);
     const int wm = wave / 2 * (TILE / 2), wn = wave % 2 * (TILE / 2);
 
     L loader;
-    loader.start(f, blockIdx.x, total, wave, lane);
+    loader.start(f, blockIdx.x, total, lds0, wave, lane);
 #pragma unroll 1
-    for (unsigned c = 0; c < kStages; ++c) {
+    for (unsigned c = 0; c < L::kStages; ++c) {
         const uint32_t to = stage_of<L>(lds0, c, wave);
 #pragma unroll
         for (int i = 0; i < L::kLoads; ++i) loader.issue(i, to);
-        loader.advance(f, total);
+        loader.advance(f, total, lds0, wave, lane);
     }
 
+    unsigned c = 0;  // slices so far
     float raw[F][8];
     u32x4 plane[2][PLANES][F];  // [half][plane][block]
     bf16x8 fb[2][F];
+    // Reads: a's blocks in two parts, then b's.
     auto read = [&](auto h, unsigned c, int r) {  // of half h of slice c
         constexpr int H = decltype(h)::value;
-        const char *stage = lds + c % kStages * L::kStage;
-        if (r < F)
-            A::read(stage, wm, r, H, lane, raw[r]);
+        const char *stage = lds + c % L::kStages * L::kStage;
+        if (r < 2 * F)
+            A::read(stage, wm, r / 2, H, lane, r % 2, raw[r / 2]);
         else
-            fb[H][r - F] = B::read(stage + A::kBytes, wn, r - F, H, lane);
+            fb[H][r - 2 * F] = B::read(stage + A::kBytes, wn, r - 2 * F, H, lane);
     };
-    constexpr int kReads = 2 * F, kParts = 4 * F;
-    auto part = [&](auto h, int p) {  // two values of a block into planes
+    constexpr int kReads = 3 * F, kParts = 4 * F * PLANES;
+    // A plane of two values of a block; what it leaves stays in their place.
+    auto part = [&](auto h, int p) {
         constexpr int H = decltype(h)::value;
-        const int i = p / 4, j = p % 4;
-        float x = raw[i][2 * j], y = raw[i][2 * j + 1];
-#pragma unroll
-        for (int q = 0; q < PLANES; ++q) {
-            const uint32_t w = to_bf16x2(x, y);
-            plane[H][q][i][j] = w;
-            x -= __uint_as_float(w << 16);
-            y -= __uint_as_float(w & 0xffff0000u);
+        const int q = p % PLANES, i = p / PLANES / 4, j = p / PLANES % 4;
+        const uint32_t w = to_bf16x2(raw[i][2 * j], raw[i][2 * j + 1]);
+        plane[H][q][i][j] = w;
+        if (q + 1 < PLANES) {
+            raw[i][2 * j] -= __uint_as_float(w << 16);
+            raw[i][2 * j + 1] -= __uint_as_float(w & 0xffff0000u);
         }
     };
     f32x16 acc[F][F];
     clear<F>(acc);
-    wait_loads<L::kLoads>();  // slice 0
+    wait_loads<2 * L::kLoads>();  // slice 0
     barrier();
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(kLow, 0, r);
@@ -637,12 +665,13 @@ __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_wide_
     for (int p = 0; p < kParts; ++p) part(kLow, p);
 
     // As above: the reads of the next 16 k first, then, at kMeet of the low half, the
-    // slice's place is free for the loads; the reads' values are taken apart from
-    // kMeet on.
-    constexpr int kRound = F * F, kPerRead = 4 / F, kMeet = kRound * 5 / 8 + (F == 2 ? 1 : 0);
-    static_assert(kPerRead * kMeet >= kReads && kMeet < kRound, "room for the reads");
-    auto half = [&](auto planes, auto h, unsigned c, uint32_t to) {
+    // slice's place is free for the loads of the one three on; the reads' values are
+    // taken apart from kMeet on, a plane of two of them at a time.
+    constexpr int kRound = F * F;
+    auto half = [&](auto planes, auto h, auto newer, uint32_t to) {
         constexpr int N = decltype(planes)::value, H = decltype(h)::value, kSteps = N * kRound;
+        constexpr int kPerRead = N == 1 ? 2 : 1, kMeet = kReads / kPerRead + (F == 4 ? 2 : 0);
+        static_assert(kMeet < kSteps, "room for the reads");
         // the loads: from kMeet of the low half to the end of the high one
         constexpr int kRest = 2 * kSteps - kMeet, kSpread = kRest / L::kLoads > 0 ? kRest / L::kLoads : 1;
         constexpr int kPerLoad = (L::kLoads + kRest - 1) / kRest;
@@ -655,7 +684,7 @@ __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_wide_
 #pragma unroll
                     for (int j = 0; j < 8; ++j) asm volatile("" : : "v"(raw[i][j]) : "memory");
                 }
-                wait_loads<0>();
+                wait_loads<decltype(newer)::value>();
                 barrier();
             }
 #pragma unroll
@@ -685,31 +714,41 @@ __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_wide_
             __builtin_amdgcn_sched_barrier(0);
         }
     };
+    constexpr int kStores = L::kLoads + out_stores(F, WIDE), kBehind = kStores < 63 ? kStores : 63;
+    const bool even = f.n % (WIDE ? 4 : 8) == 0;
+    bool behind = false;
+    auto slice = [&](auto planes, auto newer) {
+        const uint32_t to = stage_of<L>(lds0, c, wave);
+        half(planes, kLow, newer, to);
+        half(planes, kHigh, newer, to);
+#pragma unroll
+        for (int i = 0; i < F * F; ++i) pin(acc[i / F][i % F]);
+        loader.advance(f, total, lds0, wave, lane);
+        ++c;
+    };
     const int per = loader.per;
-    unsigned c = 0;  // slices so far
 #pragma unroll 1
     for (int v = blockIdx.x; v < total; v += gridDim.x) {
         const Tile t = tile_at<TILE>(f, v, total);
-        const int begin = t.split * f.chunk;
-        const int end = begin + f.chunk < f.pairs * per ? begin + f.chunk : f.pairs * per;
-        int j = begin;
+        int j = t.split * f.chunk;
+        const int end = j + f.chunk < f.pairs * per ? j + f.chunk : f.pairs * per;
+        constexpr std::integral_constant<int, L::kLoads> kNext{};  // slice c + 2's
         auto slices = [&](auto planes, int stop) {
-#pragma unroll 1
-            for (; j < stop; ++j, ++c) {
-                const uint32_t to = stage_of<L>(lds0, c, wave);
-                half(planes, kLow, c, to);
-                half(planes, kHigh, c, to);
-#pragma unroll
-                for (int i = 0; i < F * F; ++i) pin(acc[i / F][i % F]);
-                loader.advance(f, total);
+            if (behind && j < stop) {
+                slice(planes, std::integral_constant<int, kBehind>{});
+                behind = false;
+                ++j;
             }
+#pragma unroll 1
+            for (; j < stop; ++j) slice(planes, kNext);
         };
         if constexpr (PLANES == 3) {
             slices(std::integral_constant<int, 3>{}, end < per ? end : per);
             slices(std::integral_constant<int, 2>{}, end < 2 * per ? end : 2 * per);
         }
         slices(std::integral_constant<int, 1>{}, end);
-        finish_values<F, WIDE>(f, acc, lds + kOut + wave * out_lds(F), t, t.row0 + wm, t.col0 + wn, lane);
+        finish_values<F, WIDE, kOutBytes>(f, acc, lds + kOut + wave * out_lds(kOutBytes), t, t.row0 + wm, t.col0 + wn, lane);
+        behind = even;
     }
     wait_loads<0>();  // loads past the last tile write LDS too
 }
@@ -719,7 +758,7 @@ __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_wide_
 // ---------------------------------------------------------------------------
 // BF16 planes of a matrix, rows padded to whole vectors with zeros; rows without
 // a target are zeros where targets are given (what such a token holds, NaN too,
-// reaches no gradient).
+// reaches no gradient), and what g needs of each row is written beside them.
 template <bool BF16>
 __global__ __launch_bounds__(256) void loss_planes_kernel(LossPlanes f) {
     const int64_t vectors = f.pitch / 8, total = f.rows * vectors;
@@ -729,7 +768,13 @@ __global__ __launch_bounds__(256) void loss_planes_kernel(LossPlanes f) {
         if (f.targets) {
             const int64_t t = f.targets64 ? static_cast<const int64_t *>(f.targets)[row]
                                           : static_cast<const int32_t *>(f.targets)[row];
-            if (t < 0 || t >= f.vocab) have = 0;
+            const bool there = t >= 0 && t < f.vocab;
+            if (!there) have = 0;
+            if (c == 0) {
+                f.row_target[row] = there ? (int32_t)t : -1;
+                f.row_base[row] = there ? f.lse[row] * kLog2E : 0.0f;
+                f.row_d[row] = there ? f.scale * f.dloss[row] : 0.0f;
+            }
         }
         float v[8];
         load_n<BF16>(f.in, row * f.cols + c, have, v);

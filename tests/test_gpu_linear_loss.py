@@ -36,7 +36,7 @@ def inputs(workers, tokens, vocab, cols, x_dtype, w_dtype, seed, pad=True, ids=t
     w = (torch.randn(vocab, cols, generator=gen(seed + 1)) * (spread / math.sqrt(cols))).to(w_dtype)
     targets = torch.randint(0, vocab, (workers, tokens), generator=gen(seed + 2))
     if pad:  # about an eighth, by several kinds of number outside the vocabulary
-        outside = torch.tensor([-1, -100, vocab, vocab + 1000, 2 ** 31 - 1, -2 ** 31])
+        outside = torch.tensor([-1, -100, vocab, vocab + 1000, 2 ** 31 - 1, -2 ** 31 if ids == torch.int32 else 2 ** 32 + 3])
         which = torch.randint(0, 48, (workers, tokens), generator=gen(seed + 3))
         targets = torch.where(which < 6, outside[which.clamp(max=5)], targets)
     dloss = torch.randn(workers, tokens, generator=gen(seed + 4))
