@@ -160,9 +160,13 @@ int run_gradients(const signmuon_gradient *grads, int32_t n_grads, int32_t worke
 constexpr float kLog2E = 1.44269504088896340736f;
 // What a piece of the vocabulary may take of the workspace where more than one
 // tile's columns do: its maxima and sums, or its g, and the planes of its weights.
-constexpr int64_t kLossForward = (int64_t)128 << 20, kLossBackward = (int64_t)512 << 20;
+constexpr int64_t kLossForward = (int64_t)128 << 20, kLossBackward = (int64_t)1 << 30;
 
 inline int loss_planes(int dtype) { return dtype == SIGNMUON_F32 ? 3 : 1; }
+// Pairs of planes of a product of two operands (loss_pairs).
+inline int loss_products(int a, int b) {
+    return a == SIGNMUON_F32 && b == SIGNMUON_F32 ? 6 : a == SIGNMUON_F32 || b == SIGNMUON_F32 ? 3 : 1;
+}
 
 // Operands that the tiles read where they lie: BF16 rows of whole vectors.
 inline bool loss_direct(int dtype, int64_t cols) { return dtype == SIGNMUON_BF16 && cols % 8 == 0; }
@@ -176,11 +180,51 @@ int64_t loss_piece(int64_t vocab, int64_t most) {
     return (tiles + pieces - 1) / pieces * sm::kLossTile;
 }
 
+// The tile and the parts of k of a product with `slices` slices, by a model of its time in
+// slices of a tile of 256 (about 1.4 us): a round of tiles (one of 256 or two of 128 a compute
+// unit) takes its slices and 4.5 more for the results, tiles of 128 0.58 of that (8192 x
+// 32000 x 4096 1.75 against 2.02 ms, 8192 x 50257 x 768 0.61 against 0.70; 1503 x 5003 x 515 in
+// six pairs, 120 tiles or 480, 80 against 70 us), a slice of an fp32 g's product 1.65, or 0.75
+// where one plane of it is taken; adding parts 3 and 6.6 MB of them a slice. The compute
+// units are those of a whole MI355X, not asked for, since the workspace's size is told without a
+// device.
+struct LossTiles {
+    int32_t tile, splits;
+};
+
+LossTiles loss_tiles(int64_t m, int64_t n, int64_t batch, int64_t slices, double slice, bool even, int most_splits,
+                     bool parts_anyway = false) {
+    LossTiles best{};
+    double best_time = 0.0;
+    for (const int32_t tile : {256, 128}) {
+        if (tile == 256 && !even) continue;
+        const int64_t tiles = batch * ((m + tile - 1) / tile) * ((n + tile - 1) / tile), slots = tile == 256 ? 256 : 512;
+        for (int64_t splits = 1; splits <= most_splits; ++splits) {
+            const int64_t chunk = (slices + splits - 1) / splits, parts = (slices + chunk - 1) / chunk;
+            if (parts < splits) continue;
+            const double rounds = (double)((tiles * parts + slots - 1) / slots);
+            double time = rounds * (tile == 256 ? 1.0 : 0.58) * (slice * (double)chunk + 4.5);
+            if (parts > 1 || parts_anyway) time += 3.0 + (double)parts * (double)m * (double)n * 8.0 / 6.6e6;
+            if (best.tile == 0 || time < best_time) {
+                best_time = time;
+                best.tile = tile;
+                best.splits = (int32_t)parts;
+            }
+        }
+    }
+    return best;
+}
+
+inline int64_t loss_slices(int64_t k, bool g32) {
+    const int64_t slice = g32 ? sm::kLossWideSlice : sm::kLossSlice;
+    return (k + slice - 1) / slice;
+}
+
 struct LossPlan {
     int64_t piece, pitch;
-    int32_t splits;               // of dx
-    bool accumulate;              // dx over several pieces in a buffer of its own
-    size_t x, w, partial, state, target, row[3], g, dx, sums, total;
+    LossTiles logits, dx;
+    bool parts;                   // of dx, summed by a launch of their own
+    size_t x, w, partial, state, target, row[3], g, sum, part, total;
 };
 
 LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int w_dtype) {
@@ -190,6 +234,8 @@ LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int
     const int64_t w_row = loss_direct(w_dtype, cols) ? 0 : loss_planes(w_dtype) * p.pitch * 2;
     if (w_row && kLossForward / w_row < most) most = kLossForward / w_row;
     p.piece = loss_piece(vocab, most);
+    p.logits = loss_tiles(tokens, vocab < p.piece ? vocab : p.piece, 1,
+                          loss_products(x_dtype, w_dtype) * loss_slices(cols, false), 1.0, true, 1);
     size_t at = 0;
     auto section = [&](int64_t bytes) {
         const size_t here = at;
@@ -198,7 +244,7 @@ LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int
     };
     p.x = section(loss_direct(x_dtype, cols) ? 0 : loss_planes(x_dtype) * tokens * p.pitch * 2);
     p.w = section(w_row * p.piece);
-    p.partial = section(tokens * (p.piece / 128) * (int64_t)sizeof(float2));
+    p.partial = section(tokens * (p.piece / (p.logits.tile / 2)) * (int64_t)sizeof(float2));
     p.state = section(p.piece < vocab ? tokens * (int64_t)sizeof(float2) : 0);
     p.target = section(tokens * (int64_t)sizeof(float));
     p.total = at;
@@ -215,11 +261,12 @@ LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t 
     const int64_t w_row = loss_direct(w_dtype, cols) ? 0 : loss_planes(w_dtype) * p.pitch * 2;
     if (w_row && kLossBackward / w_row < most) most = kLossBackward / w_row;
     p.piece = loss_piece(vocab, most);
-    // parts of k until dx has a tile for every compute unit, eight slices at least in each
-    const int64_t tiles = ((rows + sm::kLossTile - 1) / sm::kLossTile) * ((cols + sm::kLossTile - 1) / sm::kLossTile);
-    const int64_t parts = 256 / tiles, slices = p.piece / sm::kLossSlice / 8;
-    p.splits = (int32_t)(parts < slices ? (parts > 1 ? parts : 1) : (slices > 1 ? slices : 1));
-    p.accumulate = p.piece < vocab && x_dtype == SIGNMUON_BF16;
+    const int64_t here = vocab < p.piece ? vocab : p.piece;
+    const bool g32 = entry == 4, x32 = x_dtype == SIGNMUON_F32;
+    p.logits = loss_tiles(rows, here, 1, loss_products(x_dtype, w_dtype) * loss_slices(cols, false), 1.0, true, 1);
+    p.dx = loss_tiles(rows, cols, 1, (x32 ? loss_planes(w_dtype) : 1) * loss_slices(here, g32),
+                      !g32 ? 1.0 : x32 ? 1.65 : 0.75, cols % (x32 ? 4 : 8) == 0, 32, p.piece < vocab);
+    p.parts = p.piece < vocab || p.dx.splits > 1;
     size_t at = 0;
     auto section = [&](int64_t bytes) {
         const size_t here = at;
@@ -230,8 +277,8 @@ LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t 
     p.w = section(w_row * p.piece);
     for (size_t &r : p.row) r = section(rows * 4);
     p.g = section(entry * rows * p.piece);
-    p.dx = section(p.accumulate ? rows * cols * (int64_t)sizeof(float) : 0);
-    p.sums = section(p.splits > 1 ? p.splits * rows * cols * (int64_t)sizeof(float) : 0);
+    p.sum = section(p.piece < vocab && !x32 ? rows * cols * (int64_t)sizeof(float) : 0);
+    p.part = section(p.parts ? p.dx.splits * rows * cols * (int64_t)sizeof(float) : 0);
     p.total = at;
     return p;
 }
@@ -254,10 +301,10 @@ void loss_pairs(sm::LossTile &f, int na, int nb, bool whole_a = false) {
 }
 
 // The tile, and the slices of each part of k.
-void loss_tiles(sm::LossTile &f, int32_t splits, int64_t slice) {
-    f.tile = sm::kLossTile;
-    const int64_t slices = f.pairs * ((f.k + slice - 1) / slice);
-    f.chunk = (int32_t)((slices + splits - 1) / splits);
+void loss_set_tiles(sm::LossTile &f, const LossTiles &t) {
+    f.tile = t.tile;
+    const int64_t slices = f.pairs * loss_slices(f.k, f.g32 && f.planes > 0);
+    f.chunk = (int32_t)((slices + t.splits - 1) / t.splits);
     f.splits = (int32_t)((slices + f.chunk - 1) / f.chunk);
 }
 
@@ -665,7 +712,7 @@ int signmuon_linear_cross_entropy(const void *x, signmuon_dtype x_dtype, const v
         f.k = cols;
         f.batch = 1;
         loss_pairs(f, nx, nw);
-        loss_tiles(f, 1, sm::kLossSlice);
+        loss_set_tiles(f, p.logits);
         f.rows[0] = targets;
         f.row_step = target_type == SIGNMUON_I64 ? 8 : 4;
         f.partial = reinterpret_cast<float2 *>(ws + p.partial);
@@ -726,7 +773,7 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
     const int nx = loss_planes(x_dtype), nw = loss_planes(w_dtype);
     void *const g = ws + p.g;
     const bool g32 = (x32 && dx) || (grad32 && dw);
-    const int64_t g_entry = g32 ? 4 : 2, g_slice = g32 ? sm::kLossWideSlice : sm::kLossSlice;
+    const int64_t g_entry = g32 ? 4 : 2;
     sm::LossPlanes xs = loss_to_planes(x, x_dtype, rows, cols, p.pitch, ws + p.x);
     xs.targets = targets;
     xs.targets64 = target_type == SIGNMUON_I64;
@@ -757,7 +804,7 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
         f.k = cols;
         f.batch = 1;
         loss_pairs(f, nx, nw);
-        loss_tiles(f, 1, sm::kLossSlice);
+        loss_set_tiles(f, p.logits);
         for (int i = 0; i < 3; ++i) f.rows[i] = ws + p.row[i];
         f.row_step = 4;
         f.g = g;
@@ -780,27 +827,22 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
             d.g32 = g32;
             d.planes = x32 ? 3 : 1;
             loss_pairs(d, d.planes, x32 ? nw : 1, g32);
-            loss_tiles(d, p.splits, g_slice);
+            loss_set_tiles(d, p.dx);
             d.out_batch = rows;
-            // over several pieces the sums so far lie in dx itself, or in fp32 beside it
-            float *const sums = x32 ? static_cast<float *>(dx) : reinterpret_cast<float *>(ws + p.dx);
-            float *const parts = reinterpret_cast<float *>(ws + p.sums);
-            const float *const prev = first ? nullptr : sums;
-            void *const out = last ? dx : sums;
-            const bool out_bf16 = last && !x32;
-            d.prev = d.splits > 1 ? nullptr : prev;
-            d.out = d.splits > 1 ? parts : out;
-            d.out_bf16 = d.splits > 1 ? false : out_bf16;
+            // in parts, or over several pieces, the sums so far lie in dx itself or in fp32 beside it
+            float *const sums = x32 ? static_cast<float *>(dx) : reinterpret_cast<float *>(ws + p.sum);
+            d.out = p.parts ? ws + p.part : dx;
+            d.out_bf16 = !p.parts && !x32;
             sm::launch_loss_dx(d, st);
             if (int rc = sm::launch_status()) return rc;
-            if (d.splits > 1) {
+            if (p.parts) {
                 sm::LossSums u{};
-                u.partial = parts;
-                u.prev = prev;
-                u.out = out;
+                u.partial = reinterpret_cast<const float *>(ws + p.part);
+                u.prev = first ? nullptr : sums;
+                u.out = last ? dx : sums;
                 u.total = rows * cols;
                 u.splits = d.splits;
-                u.out_bf16 = out_bf16;
+                u.out_bf16 = last && !x32;
                 sm::launch_loss_sums(u, st);
                 if (int rc = sm::launch_status()) return rc;
             }
@@ -820,12 +862,12 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
             d.g32 = g32;
             d.planes = grad32 ? 3 : 1;
             loss_pairs(d, d.planes, grad32 ? nx : 1, g32);
-            loss_tiles(d, 1, g_slice);
             d.out = const_cast<void *>(at_entry(dw, v0 * cols, grad_dtype));
             d.out_batch = vocab;
             d.out_bf16 = !grad32;
-            d.prev = accumulate ? d.out : nullptr;
-            d.prev_bf16 = d.out_bf16;
+            d.add = accumulate != 0;
+            loss_set_tiles(d, loss_tiles(here, cols, workers, d.pairs * loss_slices(tokens, g32),
+                                         !g32 ? 1.0 : grad32 ? 1.65 : 0.75, sm::loss_even(d), 1));
             sm::launch_loss_dw(d, st);
             if (int rc = sm::launch_status()) return rc;
         }

@@ -206,11 +206,12 @@ struct LossTile {
     int64_t vocab0;            // the piece's first entry
     float factor;              // scale / log 2
     // values
-    const void *prev;          // added; null: nothing
     void *out;
     int64_t out_batch;         // rows between batch entries, and between parts of k
-    bool prev_bf16, out_bf16;
+    bool out_bf16, add;        // add to what out holds (dw alone)
 };
+// Whether out's rows are whole vectors; where they are not, tiles are of 128.
+inline bool loss_even(const LossTile &f) { return f.n % (f.out_bf16 ? 8 : 4) == 0; }
 void launch_loss_logits(const LossTile &f, bool grad, hipStream_t s);
 void launch_loss_dx(const LossTile &f, hipStream_t s);
 void launch_loss_dw(const LossTile &f, hipStream_t s);

@@ -264,18 +264,25 @@ __device__ __forceinline__ void clear(Acc<F> &acc) {
 // The accumulators' values, four columns of a row at a time as group(i, n, q, v)
 // makes them of block (i, n), to out as BF16 or fp32 (WIDE), through a wave's part of
 // LDS so that whole lines are written. out: the wave's first entry, rows of `pitch`
-// entries, of which `rows` and `cols` exist. Where rows begin at whole vectors,
-// buffer stores, which drop what lies outside; otherwise plain stores.
-// BYTES: of a row at a time.
-constexpr int out_lds(int bytes) { return 32 * (bytes + 16); }  // of a wave
-// Buffer stores of a wave and tile: as many as these at least where rows are whole vectors.
-constexpr int out_stores(int F, bool wide) { return F * F * 32 * 32 * (wide ? 4 : 2) / 1024; }
+// entries, of which `rows` and `cols` exist.
+//  kEven    rows of whole vectors: buffer stores, which drop what lies outside;
+//  kAdd     the same, added to what out holds (in fp32, rounded once);
+//  kUneven  plain stores.
+// A tile's results are some thousand instructions that run once, so that each branch
+// among them is fetched every time: what does not change during a launch is a
+// parameter (with branches inside, at eight workers' 1024 tokens, 50257 x 768, dw took
+// 500 us a piece of 12800, and 420 without).
+enum { kEven, kAdd, kUneven };
+constexpr int out_lds(int bytes) { return 32 * (bytes + 16); }  // of a wave; bytes: of a row at a time
+// Buffer stores of a wave and tile.
+constexpr int out_stores(int F, bool wide, int how) { return F * F * 32 * 32 * (wide || how == kAdd ? 4 : 2) / 1024; }
 
-template <int F, bool WIDE, int BYTES, class G>
+template <int F, bool WIDE, int BYTES, int HOW, class G>
 __device__ __forceinline__ void write(Acc<F> &acc, char *mine, void *out, int64_t pitch, int rows, int cols, int lane,
                                       G &&group) {
-    constexpr int E = WIDE ? 4 : 2, W = 16 / E;               // bytes of a value, values of a store
-    constexpr int kCols = BYTES / E, kPitch = BYTES + 16;     // columns at a time
+    constexpr bool STAGE32 = WIDE || HOW == kAdd;              // the values' type in LDS
+    constexpr int S = STAGE32 ? 4 : 2, E = WIDE ? 4 : 2;       // bytes of a value there and in out
+    constexpr int W = 16 / S, kCols = BYTES / S, kPitch = BYTES + 16;  // values of a store, columns at a time
     constexpr int kLanes = BYTES / 16, kRows = kWave / kLanes;  // lanes of a row, rows of a store
     static_assert(kCols % 8 == 0 && F * 32 % kCols == 0, "whole passes");
     // made anew for each tile, so that no address is kept in registers meanwhile
@@ -285,7 +292,6 @@ __device__ __forceinline__ void write(Acc<F> &acc, char *mine, void *out, int64_
     cols = cols < 0 ? 0 : cols < F * 32 ? cols : F * 32;
     const int step = (int)pitch * E;
     char *p = static_cast<char *>(out);
-    const bool even = pitch % W == 0;
     const __amdgpu_buffer_rsrc_t buffer =
         __builtin_amdgcn_make_buffer_rsrc(p, 0, rows > 0 && cols > 0 ? (rows - 1) * step + cols * E : 0, 0x00020000);
 #pragma unroll
@@ -295,12 +301,25 @@ __device__ __forceinline__ void write(Acc<F> &acc, char *mine, void *out, int64_
             // no accumulator leaves its register before its turn
 #pragma unroll
             for (int n = n0 / 32; n < (n0 + kCols + 31) / 32; ++n) pin(acc[i][n]);
+            const uint32_t at = n0 + c16 * W < cols ? (uint32_t)(r0 * step + (n0 + c16 * W) * E) : kOutside;
+            auto offset = [&](int r) { return (int)(at + (uint32_t)((i * 32 + r * kRows) * step)); };
+            [[maybe_unused]] u32x4 held[32 / kRows];
+            if constexpr (HOW == kAdd)
+#pragma unroll
+                for (int r = 0; r < 32 / kRows; ++r) {
+                    if constexpr (WIDE) {
+                        held[r] = __builtin_amdgcn_raw_buffer_load_b128(buffer, offset(r), 0, 0);
+                    } else {
+                        const u32x2 h = __builtin_amdgcn_raw_buffer_load_b64(buffer, offset(r), 0, 0);
+                        held[r] = u32x4{h[0] << 16, h[0] & 0xffff0000u, h[1] << 16, h[1] & 0xffff0000u};
+                    }
+                }
 #pragma unroll
             for (int n = n0; n < n0 + kCols; n += 8) {
-                char *to = mine + row * kPitch + (n - n0 + half * 4) * E;
+                char *to = mine + row * kPitch + (n - n0 + half * 4) * S;
                 float v[4];
                 group(i, n / 32, n % 32 / 8, v);
-                if constexpr (WIDE)
+                if constexpr (STAGE32)
                     *reinterpret_cast<f32x4 *>(to) = f32x4{v[0], v[1], v[2], v[3]};
                 else
                     *reinterpret_cast<u32x2 *>(to) = u32x2{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3])};
@@ -309,14 +328,24 @@ __device__ __forceinline__ void write(Acc<F> &acc, char *mine, void *out, int64_
             asm volatile("" ::: "memory");
             __builtin_amdgcn_wave_barrier();
             auto staged = [&](int r) { return *reinterpret_cast<const u32x4 *>(mine + (r * kRows + r0) * kPitch + c16 * 16); };
-            if (even) {
-                const uint32_t at = n0 + c16 * W < cols ? (uint32_t)(r0 * step + (n0 + c16 * W) * E) : kOutside;
+            if constexpr (HOW != kUneven) {
                 u32x4 v[32 / kRows];
 #pragma unroll
                 for (int r = 0; r < 32 / kRows; ++r) v[r] = staged(r);
 #pragma unroll
-                for (int r = 0; r < 32 / kRows; ++r)
-                    __builtin_amdgcn_raw_buffer_store_b128(v[r], buffer, (int)(at + (uint32_t)((i * 32 + r * kRows) * step)), 0, 0);
+                for (int r = 0; r < 32 / kRows; ++r) {
+                    if constexpr (HOW == kAdd)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            v[r][j] = __float_as_uint(__uint_as_float(v[r][j]) + __uint_as_float(held[r][j]));
+                    if constexpr (HOW == kAdd && !WIDE)
+                        __builtin_amdgcn_raw_buffer_store_b64(
+                            u32x2{to_bf16x2(__uint_as_float(v[r][0]), __uint_as_float(v[r][1])),
+                                  to_bf16x2(__uint_as_float(v[r][2]), __uint_as_float(v[r][3]))},
+                            buffer, offset(r), 0, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b128(v[r], buffer, offset(r), 0, 0);
+                }
             } else {
                 const int here = cols - n0;  // columns from this pass's first on
 #pragma unroll 1
@@ -340,7 +369,6 @@ __device__ __forceinline__ void write(Acc<F> &acc, char *mine, void *out, int64_
             __builtin_amdgcn_wave_barrier();
             __builtin_amdgcn_sched_barrier(0);
         }
-    clear<F>(acc);
 }
 
 // A row's maximum and sum of exponentials over the wave's columns, and the target's
@@ -423,47 +451,49 @@ __device__ __forceinline__ void finish_grad(const LossTile &f, Acc<F> &acc, char
         any |= target[i] >= 0;
         whole &= limit[i] == kCols;
     }
-    const bool plain = __all(whole && !any);
-    write<F, WIDE, F * 32>(acc, mine, static_cast<char *>(f.g) + (row0 * f.g_pitch + col0) * (WIDE ? 4 : 2), f.g_pitch,
-                           (int)(f.m - row0 < kCols ? f.m - row0 : kCols), kCols, lane,
-                   [&](int i, int n, int q, float(&v)[4]) {
+    auto put = [&](auto &&group) {
+        write<F, WIDE, F * 32, kEven>(acc, mine, static_cast<char *>(f.g) + (row0 * f.g_pitch + col0) * (WIDE ? 4 : 2),
+                                     f.g_pitch, (int)(f.m - row0 < kCols ? f.m - row0 : kCols), kCols, lane, group);
+    };
+    auto exponential = [&](int i, int n, int e) {
+        return __builtin_amdgcn_exp2f(fmaf(acc[i][n][e], f.factor, -base[i]));
+    };
+    if (__all(whole && !any))
+        put([&](int i, int n, int q, float(&v)[4]) {
 #pragma unroll
-                       for (int j = 0; j < 4; ++j)
-                           v[j] = __builtin_amdgcn_exp2f(fmaf(acc[i][n][q * 4 + j], f.factor, -base[i]));
-                       if (plain) {
+            for (int j = 0; j < 4; ++j) v[j] = d[i] * exponential(i, n, q * 4 + j);
+        });
+    else
+        put([&](int i, int n, int q, float(&v)[4]) {
 #pragma unroll
-                           for (int j = 0; j < 4; ++j) v[j] *= d[i];
-                       } else {
-#pragma unroll
-                           for (int j = 0; j < 4; ++j) {
-                               const int c = column(n, q * 4 + j, lane);
-                               v[j] = c < limit[i] ? d[i] * (c == target[i] ? v[j] - 1.0f : v[j]) : 0.0f;
-                           }
-                       }
-                   });
+            for (int j = 0; j < 4; ++j) {
+                const int c = column(n, q * 4 + j, lane);
+                const float p = exponential(i, n, q * 4 + j);
+                v[j] = c < limit[i] ? d[i] * (c == target[i] ? p - 1.0f : p) : 0.0f;
+            }
+        });
+    clear<F>(acc);
 }
 
-// A product's values, added to what `prev` holds.
-template <int F, bool WIDE, int BYTES>
+// A product's values, added to what out holds where f.add.
+template <int F, bool WIDE, int BYTES, int HOW>
 __device__ __forceinline__ void finish_values(const LossTile &f, Acc<F> &acc, char *mine, const Tile &t, int64_t row0,
                                               int64_t col0, int lane) {
     const int64_t first = (f.out_batch * (t.split * (int64_t)f.batch + t.batch) + row0) * f.n + col0;
     const int rows = (int)(f.m - row0 < F * 32 ? f.m - row0 : F * 32), cols = (int)(f.n - col0 < F * 32 ? f.n - col0 : F * 32);
-    write<F, WIDE, BYTES>(acc, mine, static_cast<char *>(f.out) + first * (WIDE ? 4 : 2), f.n, rows, cols, lane,
-                   [&](int i, int n, int q, float(&v)[4]) {
+    write<F, WIDE, BYTES, HOW>(acc, mine, static_cast<char *>(f.out) + first * (WIDE ? 4 : 2), f.n, rows, cols, lane,
+                               [&](int i, int n, int q, float(&v)[4]) {
 #pragma unroll
-                       for (int j = 0; j < 4; ++j) v[j] = acc[i][n][q * 4 + j];
-                       if (!f.prev) return;
-                       const int row = i * 32 + (lane & 31), col = column(n, q * 4, lane);
-                       const int have = row >= rows ? 0 : left(cols, col) < 4 ? left(cols, col) : 4;
-                       float p[4];
-                       if (f.prev_bf16)
-                           load_n<true>(f.prev, first + row * f.n + col, have, p);
-                       else
-                           load_n<false>(f.prev, first + row * f.n + col, have, p);
+                                   for (int j = 0; j < 4; ++j) v[j] = acc[i][n][q * 4 + j];
+                                   if (HOW != kUneven || !f.add) return;
+                                   const int row = i * 32 + (lane & 31), col = column(n, q * 4, lane);
+                                   const int have = row >= rows ? 0 : left(cols, col) < 4 ? left(cols, col) : 4;
+                                   float p[4];
+                                   load_n<!WIDE>(f.out, first + row * f.n + col, have, p);
 #pragma unroll
-                       for (int j = 0; j < 4; ++j) v[j] += p[j];
-                   });
+                                   for (int j = 0; j < 4; ++j) v[j] += p[j];
+                               });
+    clear<F>(acc);
 }
 
 constexpr std::integral_constant<int, 0> kLow{};
@@ -487,8 +517,8 @@ enum { kLse, kGrad, kValues };
 // Products of BF16 operands. A workgroup takes every gridDim-th tile; four waves of
 // half a tile each way. The loads run two slices ahead of the products, on into the
 // next tile, so that a tile's first slices are there when the one before it is done.
-// WIDE: results in fp32.
-template <int KA, int KB, int TILE, int END, bool WIDE>
+// WIDE: results in fp32. HOW: of values.
+template <int KA, int KB, int TILE, int END, bool WIDE, int HOW>
 __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_tile_kernel(LossTile f, int total) {
     constexpr int kRowArrays = END == kLse ? 1 : END == kGrad ? 3 : 0;
     using L = Loader<KA, KB, TILE, kLossSlice, 2, kRowArrays>;
@@ -557,9 +587,8 @@ __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_tile_
     };
     // A tile's results are on their way to memory during the next one's first slice:
     // there, only what is older than their stores is waited for.
-    constexpr int kStores = END == kLse ? F : out_stores(F, WIDE), kBehind = kStores < 63 ? kStores : 63;
-    const bool even = END != kValues || f.n % (WIDE ? 4 : 8) == 0;  // the stores' number is known
-    bool behind = false;
+    constexpr int kStores = END == kLse ? F : out_stores(F, WIDE, HOW), kBehind = kStores < 63 ? kStores : 63;
+    bool behind = false;  // of buffer stores, whose number is known
     const int per = loader.per;
     unsigned c = 0;  // slices so far
     // `newer`: operations that may be under way behind the loads of slice c + 1
@@ -599,8 +628,8 @@ __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_tile_
         else if constexpr (END == kGrad)
             finish_grad<F, WIDE>(f, acc, mine, data, t.row0 + wm, t.col0 + wn, lane);
         else
-            finish_values<F, WIDE, F * 32>(f, acc, mine, t, t.row0 + wm, t.col0 + wn, lane);
-        behind = even;
+            finish_values<F, WIDE, F * 32, HOW>(f, acc, mine, t, t.row0 + wm, t.col0 + wn, lane);
+        behind = HOW != kUneven;
     }
     wait_loads<0>();  // loads past the last tile write LDS too
 }
@@ -608,7 +637,7 @@ __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_tile_
 // Products of an fp32 a, taken apart into planes in registers, and a BF16 b. PLANES:
 // of a; 1, or 3 for the first plane of b, 2 for its second and 1 for its third. A slice
 // is 32 k: while 16 of them are multiplied, the next 16 are read and taken apart.
-template <int KA, int TILE, int PLANES, bool WIDE>
+template <int KA, int TILE, int PLANES, bool WIDE, int HOW>
 __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_wide_kernel(LossTile f, int total) {
     using L = Loader<KA, kCols16, TILE, kLossWideSlice, 3, 0>;
     using A = typename L::A;
@@ -714,8 +743,7 @@ __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_wide_
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    constexpr int kStores = L::kLoads + out_stores(F, WIDE), kBehind = kStores < 63 ? kStores : 63;
-    const bool even = f.n % (WIDE ? 4 : 8) == 0;
+    constexpr int kStores = L::kLoads + out_stores(F, WIDE, HOW), kBehind = kStores < 63 ? kStores : 63;
     bool behind = false;
     auto slice = [&](auto planes, auto newer) {
         const uint32_t to = stage_of<L>(lds0, c, wave);
@@ -747,8 +775,9 @@ __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_wide_
             slices(std::integral_constant<int, 2>{}, end < 2 * per ? end : 2 * per);
         }
         slices(std::integral_constant<int, 1>{}, end);
-        finish_values<F, WIDE, kOutBytes>(f, acc, lds + kOut + wave * out_lds(kOutBytes), t, t.row0 + wm, t.col0 + wn, lane);
-        behind = even;
+        finish_values<F, WIDE, kOutBytes, HOW>(f, acc, lds + kOut + wave * out_lds(kOutBytes), t, t.row0 + wm,
+                                               t.col0 + wn, lane);
+        behind = HOW != kUneven;
     }
     wait_loads<0>();  // loads past the last tile write LDS too
 }
@@ -832,23 +861,24 @@ __global__ __launch_bounds__(1024) void loss_join_kernel(LossJoin f) {
     if (f.loss) f.loss[row] = t >= 0 && t < f.vocab ? (lse2 - f.target[row]) * kLn2 : 0.0f;
 }
 
-// out = the parts' sums, in order, added to what `prev` holds; 4 entries a thread.
+// out = the parts' sums, in order, added to what `prev` holds; 4 entries a thread at a
+// time.
 __global__ __launch_bounds__(256) void loss_sums_kernel(LossSums f) {
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (at >= f.total) return;
-    const int have = (int)(f.total - at < 4 ? f.total - at : 4);
-    float v[4];
-    load_n<false>(f.prev, at, f.prev ? have : 0, v);
-    for (int s = 0; s < f.splits; ++s) {
-        float p[4];
-        load_n<false>(f.partial, s * f.total + at, have, p);
+    for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; at < f.total; at += (int64_t)gridDim.x * 1024) {
+        const int have = (int)(f.total - at < 4 ? f.total - at : 4);
+        float v[4];
+        load_n<false>(f.prev, at, f.prev ? have : 0, v);
+        for (int s = 0; s < f.splits; ++s) {
+            float p[4];
+            load_n<false>(f.partial, s * f.total + at, have, p);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] += p[j];
+            for (int j = 0; j < 4; ++j) v[j] += p[j];
+        }
+        if (f.out_bf16)
+            store_n<true>(f.out, at, have, v);
+        else
+            store_n<false>(f.out, at, have, v);
     }
-    if (f.out_bf16)
-        store_n<true>(f.out, at, have, v);
-    else
-        store_n<false>(f.out, at, have, v);
 }
 
 int tiles_of(const LossTile &f) {
@@ -862,30 +892,39 @@ dim3 grid_of(const LossTile &f) {
     return dim3((unsigned)(total < most ? total : most));
 }
 
-template <int KA, int KB, int END, bool WIDE>
+template <int KA, int KB, int END, bool WIDE, int HOW = kEven>
 void launch_tiles(const LossTile &f, hipStream_t s) {
-    if (f.tile == 256)
-        loss_tile_kernel<KA, KB, 256, END, WIDE><<<grid_of(f), kWaves * kWave, 0, s>>>(f, tiles_of(f));
+    if (HOW != kUneven && f.tile == 256)
+        loss_tile_kernel<KA, KB, HOW == kUneven ? 128 : 256, END, WIDE, HOW><<<grid_of(f), kWaves * kWave, 0, s>>>(f, tiles_of(f));
     else
-        loss_tile_kernel<KA, KB, 128, END, WIDE><<<grid_of(f), kWaves * kWave, 0, s>>>(f, tiles_of(f));
+        loss_tile_kernel<KA, KB, 128, END, WIDE, HOW><<<grid_of(f), kWaves * kWave, 0, s>>>(f, tiles_of(f));
 }
 
-template <int KA, int PLANES, bool WIDE>
+template <int KA, int PLANES, bool WIDE, int HOW>
 void launch_wide(const LossTile &f, hipStream_t s) {
-    if (f.tile == 256)
-        loss_wide_kernel<KA, 256, PLANES, WIDE><<<grid_of(f), kWaves * kWave, 0, s>>>(f, tiles_of(f));
+    if (HOW != kUneven && f.tile == 256)
+        loss_wide_kernel<KA, HOW == kUneven ? 128 : 256, PLANES, WIDE, HOW><<<grid_of(f), kWaves * kWave, 0, s>>>(f, tiles_of(f));
     else
-        loss_wide_kernel<KA, 128, PLANES, WIDE><<<grid_of(f), kWaves * kWave, 0, s>>>(f, tiles_of(f));
+        loss_wide_kernel<KA, 128, PLANES, WIDE, HOW><<<grid_of(f), kWaves * kWave, 0, s>>>(f, tiles_of(f));
 }
 
-template <int K16, int K32>
-void launch_values(const LossTile &f, hipStream_t s) {
+template <int HOW>
+void launch_dx(const LossTile &f, hipStream_t s) {
     if (!f.g32)
-        f.out_bf16 ? launch_tiles<K16, kCols16, kValues, false>(f, s) : launch_tiles<K16, kCols16, kValues, true>(f, s);
+        f.out_bf16 ? launch_tiles<kRows16, kCols16, kValues, false, HOW>(f, s)
+                   : launch_tiles<kRows16, kCols16, kValues, true, HOW>(f, s);
     else if (f.planes == 3)
-        launch_wide<K32, 3, true>(f, s);
+        launch_wide<kRows32, 3, true, HOW>(f, s);
     else
-        f.out_bf16 ? launch_wide<K32, 1, false>(f, s) : launch_wide<K32, 1, true>(f, s);
+        f.out_bf16 ? launch_wide<kRows32, 1, false, HOW>(f, s) : launch_wide<kRows32, 1, true, HOW>(f, s);
+}
+
+template <int HOW>
+void launch_dw(const LossTile &f, hipStream_t s) {
+    if (!f.g32)
+        launch_tiles<kCols16, kCols16, kValues, false, HOW>(f, s);
+    else
+        f.planes == 3 ? launch_wide<kCols32, 3, true, HOW>(f, s) : launch_wide<kCols32, 1, false, HOW>(f, s);
 }
 
 }  // namespace
@@ -910,11 +949,20 @@ void launch_loss_join(const LossJoin &f, hipStream_t s) {
     loss_join_kernel<<<dim3((unsigned)((f.rows + kWave - 1) / kWave)), 1024, 0, s>>>(f);
 }
 
-void launch_loss_dx(const LossTile &f, hipStream_t s) { launch_values<kRows16, kRows32>(f, s); }
-void launch_loss_dw(const LossTile &f, hipStream_t s) { launch_values<kCols16, kCols32>(f, s); }
+void launch_loss_dx(const LossTile &f, hipStream_t s) {
+    loss_even(f) ? launch_dx<kEven>(f, s) : launch_dx<kUneven>(f, s);
+}
+
+void launch_loss_dw(const LossTile &f, hipStream_t s) {
+    if (!loss_even(f))
+        launch_dw<kUneven>(f, s);
+    else
+        f.add ? launch_dw<kAdd>(f, s) : launch_dw<kEven>(f, s);
+}
 
 void launch_loss_sums(const LossSums &f, hipStream_t s) {
-    loss_sums_kernel<<<dim3((unsigned)((f.total + 1023) / 1024)), 256, 0, s>>>(f);
+    const int64_t blocks = (f.total + 1023) / 1024;
+    loss_sums_kernel<<<dim3((unsigned)(blocks < 65536 ? blocks : 65536)), 256, 0, s>>>(f);
 }
 
 }  // namespace sm
