@@ -223,9 +223,10 @@ struct LossJoin {
     const void *targets;
     float *loss, *lse;
     int64_t rows, blocks, vocab;
+    int32_t group;  // rows of a workgroup
     bool first, last, targets64;
 };
-void launch_loss_join(const LossJoin &f, hipStream_t s);
+void launch_loss_join(LossJoin f, hipStream_t s);
 
 struct LossSums {
     const float *partial;  // [splits][total]

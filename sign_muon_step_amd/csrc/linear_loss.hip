@@ -273,11 +273,15 @@ __device__ __forceinline__ void clear(Acc<F> &acc) {
 // parameter (with branches inside, at eight workers' 1024 tokens, 50257 x 768, dw took
 // 500 us a piece of 12800, and 420 without).
 enum { kEven, kAdd, kUneven };
+// How the stores go through the caches: g, of which a piece is larger than they are, as
+// a stream (410 -> 395 us a piece of 25000 for eight workers, and 405 -> 370 for the dx that
+// reads it next); results as usual (as a stream, dw took 3 % longer).
+enum { kKept = 0, kStream = 2 };
 constexpr int out_lds(int bytes) { return 32 * (bytes + 16); }  // of a wave; bytes: of a row at a time
 // Buffer stores of a wave and tile.
 constexpr int out_stores(int F, bool wide, int how) { return F * F * 32 * 32 * (wide || how == kAdd ? 4 : 2) / 1024; }
 
-template <int F, bool WIDE, int BYTES, int HOW, class G>
+template <int F, bool WIDE, int BYTES, int HOW, int CACHE, class G>
 __device__ __forceinline__ void write(Acc<F> &acc, char *mine, void *out, int64_t pitch, int rows, int cols, int lane,
                                       G &&group) {
     constexpr bool STAGE32 = WIDE || HOW == kAdd;              // the values' type in LDS
@@ -344,7 +348,7 @@ __device__ __forceinline__ void write(Acc<F> &acc, char *mine, void *out, int64_
                                   to_bf16x2(__uint_as_float(v[r][2]), __uint_as_float(v[r][3]))},
                             buffer, offset(r), 0, 0);
                     else
-                        __builtin_amdgcn_raw_buffer_store_b128(v[r], buffer, offset(r), 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(v[r], buffer, offset(r), 0, CACHE);
                 }
             } else {
                 const int here = cols - n0;  // columns from this pass's first on
@@ -452,7 +456,7 @@ __device__ __forceinline__ void finish_grad(const LossTile &f, Acc<F> &acc, char
         whole &= limit[i] == kCols;
     }
     auto put = [&](auto &&group) {
-        write<F, WIDE, F * 32, kEven>(acc, mine, static_cast<char *>(f.g) + (row0 * f.g_pitch + col0) * (WIDE ? 4 : 2),
+        write<F, WIDE, F * 32, kEven, kStream>(acc, mine, static_cast<char *>(f.g) + (row0 * f.g_pitch + col0) * (WIDE ? 4 : 2),
                                      f.g_pitch, (int)(f.m - row0 < kCols ? f.m - row0 : kCols), kCols, lane, group);
     };
     auto exponential = [&](int i, int n, int e) {
@@ -481,7 +485,7 @@ __device__ __forceinline__ void finish_values(const LossTile &f, Acc<F> &acc, ch
                                               int64_t col0, int lane) {
     const int64_t first = (f.out_batch * (t.split * (int64_t)f.batch + t.batch) + row0) * f.n + col0;
     const int rows = (int)(f.m - row0 < F * 32 ? f.m - row0 : F * 32), cols = (int)(f.n - col0 < F * 32 ? f.n - col0 : F * 32);
-    write<F, WIDE, BYTES, HOW>(acc, mine, static_cast<char *>(f.out) + first * (WIDE ? 4 : 2), f.n, rows, cols, lane,
+    write<F, WIDE, BYTES, HOW, kKept>(acc, mine, static_cast<char *>(f.out) + first * (WIDE ? 4 : 2), f.n, rows, cols, lane,
                                [&](int i, int n, int q, float(&v)[4]) {
 #pragma unroll
                                    for (int j = 0; j < 4; ++j) v[j] = acc[i][n][q * 4 + j];
@@ -829,13 +833,14 @@ __global__ __launch_bounds__(256) void loss_planes_kernel(LossPlanes f) {
     }
 }
 
-// The partial maxima and sums of 64 rows: 16 waves take every 16th block of
-// columns, and the first joins them, with what earlier pieces of the vocabulary
-// left.
+// The partial maxima and sums of f.group rows (a power of 2, up to 64): 1024 / group
+// threads of a row take every so manieth block of columns, eight at a time, and
+// are joined in a tree, with what earlier pieces of the vocabulary left.
 __global__ __launch_bounds__(1024) void loss_join_kernel(LossJoin f) {
-    __shared__ float2 lds[16][kWave];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int64_t row = (int64_t)blockIdx.x * kWave + lane;
+    __shared__ float2 lds[1024];
+    const int slots = 1024 / f.group, slot = threadIdx.x / f.group;
+    const int64_t row = (int64_t)blockIdx.x * f.group + threadIdx.x % f.group;
+    const bool there = row < f.rows;
     float top = -INFINITY, sum = 0.0f;
     auto add = [&](float2 p) {
         const float m = fmaxf(top, p.x);
@@ -844,12 +849,22 @@ __global__ __launch_bounds__(1024) void loss_join_kernel(LossJoin f) {
               (p.y == 0.0f ? 0.0f : p.y * __builtin_amdgcn_exp2f(p.x - m));
         top = m;
     };
-    if (row < f.rows)
-        for (int64_t b = wave; b < f.blocks; b += 16) add(f.partial[b * f.rows + row]);
-    lds[wave][lane] = make_float2(top, sum);
-    __syncthreads();
-    if (wave || row >= f.rows) return;
-    for (int w = 1; w < 16; ++w) add(lds[w][lane]);
+    if (there)
+        for (int64_t b = slot; b < f.blocks; b += 8 * slots) {
+            float2 p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                p[i] = b + i * slots < f.blocks ? f.partial[(b + i * slots) * f.rows + row] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) add(p[i]);
+        }
+    for (int d = slots / 2; d > 0; d >>= 1) {
+        lds[threadIdx.x] = make_float2(top, sum);
+        __syncthreads();
+        if (slot < d) add(lds[threadIdx.x + d * f.group]);
+        __syncthreads();
+    }
+    if (slot || !there) return;
     if (!f.first) add(f.state[row]);
     if (!f.last) {
         f.state[row] = make_float2(top, sum);
@@ -945,8 +960,10 @@ void launch_loss_logits(const LossTile &f, bool grad, hipStream_t s) {
         f.g32 ? launch_tiles<kRows16, kRows16, kGrad, true>(f, s) : launch_tiles<kRows16, kRows16, kGrad, false>(f, s);
 }
 
-void launch_loss_join(const LossJoin &f, hipStream_t s) {
-    loss_join_kernel<<<dim3((unsigned)((f.rows + kWave - 1) / kWave)), 1024, 0, s>>>(f);
+void launch_loss_join(LossJoin f, hipStream_t s) {
+    // as few rows a workgroup as leave 256 of them
+    for (f.group = 64; f.group > 1 && f.rows <= f.group / 2 * 256; f.group /= 2) {}
+    loss_join_kernel<<<dim3((unsigned)((f.rows + f.group - 1) / f.group)), 1024, 0, s>>>(f);
 }
 
 void launch_loss_dx(const LossTile &f, hipStream_t s) {
