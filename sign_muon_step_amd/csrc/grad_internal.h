@@ -480,8 +480,18 @@ struct Team {
         }
     }
     __device__ __forceinline__ float sum(float a) {
-        float b = 0.0f;
-        sum2(a, b);
+#pragma unroll
+        for (int d = 1; d < (TS < kWave ? TS : kWave); d <<= 1) a += __shfl_xor(a, d);
+        if constexpr (TS > kWave) {
+            constexpr int W = TS / kWave;
+            float *at = lds + parity * 2 * W;
+            parity ^= 1;
+            if ((threadIdx.x & (kWave - 1)) == 0) at[threadIdx.x / kWave] = a;
+            __syncthreads();
+            a = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) a += at[w];
+        }
         return a;
     }
 };

@@ -27,6 +27,41 @@ __device__ __forceinline__ void round_type(float (&v)[8]) {
         }
 }
 
+// A row's columns c .. c + 7. WHOLE: rows of whole vectors, so that a lane has all
+// eight or none (those without load the row's first again). Otherwise rows begin
+// anywhere; keeping both in one kernel costs 163 registers and half of the waves
+// where this takes 60 (8192 x 768 to 8 bits 16.2 us, now XXX).
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ Raw<BF16, 8> fetch8(const void *p, int64_t row, int c, int cols) {
+    if constexpr (!WHOLE) return load_raw<BF16, 8>(p, row, c, cols);
+    Raw<BF16, 8> o;
+    const char *q = static_cast<const char *>(p) + (row + (c < cols ? c : 0)) * (BF16 ? 2 : 4);
+#pragma unroll
+    for (int h = 0; h < (BF16 ? 1 : 2); ++h) {
+        const u32x4 t = *reinterpret_cast<const u32x4 *>(q + 16 * h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o.w[4 * h + j] = t[j];
+    }
+    return o;
+}
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void open8(const Raw<BF16, 8> &o, int c, int cols, float (&v)[8], bool whole) {
+    if constexpr (!WHOLE) {
+        unpack(o, c, cols, v, whole);
+        return;
+    }
+    const bool there = c < cols;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t w = BF16 ? (j % 2 ? o.w[j / 2] & 0xffff0000u : o.w[j / 2] << 16) : o.w[BF16 ? 0 : j];
+        v[j] = there ? __uint_as_float(w) : 0.0f;
+    }
+}
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void put8(void *p, int64_t row, int c, int cols, const float (&v)[8]) {
+    store_n<BF16>(p, row + c, WHOLE ? (c < cols ? 8 : 0) : left(cols, c), v);
+}
+
 // Columns c .. c + 7 of an output row as 8 bits: lanes 16 i .. 16 i + 15 hold a
 // block. Every lane of the block calls; columns past the row's end are padding.
 template <bool E5M2>
@@ -61,7 +96,7 @@ __device__ __forceinline__ void put_f8(const RmsNorm &n, int64_t row, int64_t c,
 }
 
 // One team per row, `teams` of the grid taking every teams-th row.
-template <bool BF16, int TS, int NIT, int THREADS, int F8>
+template <bool BF16, bool WHOLE, int TS, int NIT, int THREADS, int F8>
 __global__ __launch_bounds__(THREADS) void rms_kernel(RmsNorm n) {
     __shared__ float lds[TS > kWave ? 4 * TS / kWave : 1];
     Team<TS> team{lds};
@@ -80,17 +115,17 @@ __global__ __launch_bounds__(THREADS) void rms_kernel(RmsNorm n) {
 #pragma unroll
         for (int i = 0; i < NIT; ++i) {
             const int c = (i * TS + tl) * 8;
-            rx[i] = load_raw<BF16, 8>(n.x, row * n.cols, c, cols);
-            if (n.residual) rr[i] = load_raw<BF16, 8>(n.residual, row * n.cols, c, cols);
+            rx[i] = fetch8<BF16, WHOLE>(n.x, row * n.cols, c, cols);
+            if (n.residual) rr[i] = fetch8<BF16, WHOLE>(n.residual, row * n.cols, c, cols);
         }
 #pragma unroll
         for (int i = 0; i < NIT; ++i) {
             const int c = (i * TS + tl) * 8;
             const bool whole = (i + 1) * TS * 8 <= cols;
-            unpack(rx[i], c, cols, v[i], whole);
+            open8<BF16, WHOLE>(rx[i], c, cols, v[i], whole);
             if (n.residual) {
                 float r[8];
-                unpack(rr[i], c, cols, r, whole);
+                open8<BF16, WHOLE>(rr[i], c, cols, r, whole);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] += r[j];
                 round_type<BF16>(v[i]);
@@ -102,11 +137,11 @@ __global__ __launch_bounds__(THREADS) void rms_kernel(RmsNorm n) {
         // behind the sum every lane has what it reads of the row: h may be x or the residual
 #pragma unroll
         for (int i = 0; i < NIT; ++i) {
-            const int c = (i * TS + tl) * 8, have = left(cols, c);
-            if (n.h) store_n<BF16>(n.h, row * n.cols + c, have, v[i]);
+            const int c = (i * TS + tl) * 8;
+            if (n.h) put8<BF16, WHOLE>(n.h, row * n.cols, c, cols, v[i]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * g[i][j];
-            if (n.y) store_n<BF16>(n.y, row * n.cols + c, have, v[i]);
+            if (n.y) put8<BF16, WHOLE>(n.y, row * n.cols, c, cols, v[i]);
             put_f8<F8>(n, row, c, v[i]);
         }
         if (tl == 0 && n.rstd) n.rstd[row] = rstd;
@@ -175,7 +210,7 @@ __device__ __forceinline__ void write_sum(const RmsGrad &n, int64_t worker, int6
 
 __device__ __forceinline__ int64_t rows_per_part(const RmsGrad &n) { return (n.rows + n.parts - 1) / n.parts; }
 
-template <bool BF16, int TS, int NIT, int THREADS>
+template <bool BF16, bool WHOLE, int TS, int NIT, int THREADS>
 __global__ __launch_bounds__(THREADS) void rms_grad_kernel(RmsGrad n) {
     constexpr int kTeams = THREADS / TS;
     __shared__ float sums[kTeams > 1 ? kTeams * NIT * TS * 8 : 1];  // [kTeams][NIT][TS][8]
@@ -199,25 +234,30 @@ __global__ __launch_bounds__(THREADS) void rms_grad_kernel(RmsGrad n) {
 #pragma unroll
         for (int i = 0; i < NIT; ++i) {
             const int c = (i * TS + tl) * 8;
-            rh[i] = load_raw<BF16, 8>(n.h, row * n.cols, c, cols);
-            rd[i] = load_raw<BF16, 8>(n.dy, row * n.cols, c, cols);
-            if (n.dh) rs[i] = load_raw<BF16, 8>(n.dh, row * n.cols, c, cols);
+            rh[i] = fetch8<BF16, WHOLE>(n.h, row * n.cols, c, cols);
+            rd[i] = fetch8<BF16, WHOLE>(n.dy, row * n.cols, c, cols);
+            if (n.dh) rs[i] = fetch8<BF16, WHOLE>(n.dh, row * n.cols, c, cols);
         }
         next_rstd = n.rstd[row];
     };
+    // a wave has room for the next row while it works on one; for more columns other waves
+    // fill the wait
+    constexpr bool kAhead = TS <= kWave && BF16;
+    if (kAhead && begin + tm < end) fetch(begin + tm);
     for (int64_t r = begin + tm; r < end; r += kTeams) {
         const int64_t row = worker * n.rows + r;
-        fetch(r);
+        if (!kAhead) fetch(r);
         float x[NIT][8], d[NIT][8], s[NIT][8];
 #pragma unroll
         for (int i = 0; i < NIT; ++i) {
             const int c = (i * TS + tl) * 8;
             const bool whole = (i + 1) * TS * 8 <= cols;
-            unpack(rh[i], c, cols, x[i], whole);
-            unpack(rd[i], c, cols, d[i], whole);
-            if (n.dh) unpack(rs[i], c, cols, s[i], whole);
+            open8<BF16, WHOLE>(rh[i], c, cols, x[i], whole);
+            open8<BF16, WHOLE>(rd[i], c, cols, d[i], whole);
+            if (n.dh) open8<BF16, WHOLE>(rs[i], c, cols, s[i], whole);
         }
         const float rstd = next_rstd;
+        if (kAhead && r + kTeams < end) fetch(r + kTeams);
         float along = 0.0f;
 #pragma unroll
         for (int i = 0; i < NIT; ++i)
@@ -239,7 +279,7 @@ __global__ __launch_bounds__(THREADS) void rms_grad_kernel(RmsGrad n) {
                 x[i][j] = rstd * (d[i][j] - x[i][j] * along);
                 if (n.dh) x[i][j] += s[i][j];
             }
-            store_n<BF16>(n.dx, row * n.cols + c, left(cols, c), x[i]);
+            put8<BF16, WHOLE>(n.dx, row * n.cols, c, cols, x[i]);
         }
     }
     if (!n.dgamma) return;
@@ -384,7 +424,11 @@ void launch_rms(const RmsNorm &n, hipStream_t s) {
     auto f = [&](auto w) {
         constexpr int TS = decltype(w)::TS, NIT = decltype(w)::NIT, THREADS = decltype(w)::THREADS;
         const int64_t teams = THREADS / TS, blocks = (n.rows + teams - 1) / teams;
-        rms_kernel<BF16, TS, NIT, THREADS, F8><<<dim3((unsigned)(blocks < 2048 ? blocks : 2048)), THREADS, 0, s>>>(n);
+        const dim3 grid((unsigned)(blocks < 2048 ? blocks : 2048));
+        if (n.cols % 8 == 0)
+            rms_kernel<BF16, true, TS, NIT, THREADS, F8><<<grid, THREADS, 0, s>>>(n);
+        else
+            rms_kernel<BF16, false, TS, NIT, THREADS, F8><<<grid, THREADS, 0, s>>>(n);
     };
     by_width(n.cols, f);
 }
@@ -412,7 +456,11 @@ void launch_grad(const RmsGrad &n, hipStream_t s) {
     }
     auto f = [&](auto w) {
         constexpr int TS = decltype(w)::TS, NIT = decltype(w)::NIT, THREADS = decltype(w)::THREADS;
-        rms_grad_kernel<BF16, TS, NIT, THREADS><<<dim3((unsigned)(n.workers * n.parts)), THREADS, 0, s>>>(n);
+        const dim3 grid((unsigned)(n.workers * n.parts));
+        if (n.cols % 8 == 0)
+            rms_grad_kernel<BF16, true, TS, NIT, THREADS><<<grid, THREADS, 0, s>>>(n);
+        else
+            rms_grad_kernel<BF16, false, TS, NIT, THREADS><<<grid, THREADS, 0, s>>>(n);
     };
     by_width(n.cols, f);
 }
