@@ -80,11 +80,12 @@ size_t rms_workspace(int32_t workers, int64_t rows, int64_t cols) {
 // Gradient norms and clipping
 // ---------------------------------------------------------------------------
 struct ClipPlan {
+    int32_t unit;   // entries
     int64_t units;  // of a worker
     size_t factors, total;
 };
 
-inline int64_t clip_units(int64_t n) { return (n + sm::kClipUnit - 1) / sm::kClipUnit; }
+inline int64_t clip_units(int64_t n, int32_t unit) { return (n + unit - 1) / unit; }
 
 // The sizes alone, then what a call reads and writes.
 int check_gradients(const signmuon_gradient *grads, int32_t n_grads, int32_t workers, ClipPlan &p) {
@@ -94,7 +95,13 @@ int check_gradients(const signmuon_gradient *grads, int32_t n_grads, int32_t wor
     for (int32_t i = 0; i < n_grads; ++i) {
         if (grads[i].n < 1) return SIGNMUON_EINVAL;
         if (grads[i].n > kMaxN) return SIGNMUON_ERANGE;
-        p.units += clip_units(grads[i].n);
+        p.units += clip_units(grads[i].n, sm::kClipUnit);
+    }
+    p.unit = sm::kClipUnit;
+    if (p.units * workers < 512) {  // two workgroups a compute unit
+        p.unit = sm::kClipSmallUnit;
+        p.units = 0;
+        for (int32_t i = 0; i < n_grads; ++i) p.units += clip_units(grads[i].n, p.unit);
     }
     p.factors = align_up((size_t)(p.units * workers) * sizeof(double));
     p.total = p.factors + (size_t)workers * sizeof(float);
@@ -115,15 +122,13 @@ int run_gradients(const signmuon_gradient *grads, int32_t n_grads, int32_t worke
     if (!aligned16(norms)) return SIGNMUON_EALIGN;
     if (int rc = check_workspace(workspace, workspace_bytes, p.total)) return rc;
     char *ws = static_cast<char *>(workspace);
-    auto batches = [&](auto launch) -> int {
-        int64_t unit = 0;
-        for (int32_t i0 = 0; i0 < n_grads; i0 += sm::kClipTensors) {
+    // the batches of tensors, from the first to the last or back
+    auto batches = [&](auto launch, bool back) -> int {
+        int64_t unit = back ? p.units : 0;
+        const int32_t last = (n_grads - 1) / sm::kClipTensors;
+        for (int32_t k = 0; k <= last; ++k) {
+            const int32_t i0 = (back ? last - k : k) * sm::kClipTensors;
             sm::ClipBatch b{};
-            b.partial = reinterpret_cast<double *>(ws);
-            b.factors = reinterpret_cast<const float *>(ws + p.factors);
-            b.units = p.units;
-            b.unit0 = unit;
-            b.workers = workers;
             int64_t here = 0;
             for (int32_t i = i0; i < n_grads && i < i0 + sm::kClipTensors; ++i) {
                 const int t = b.tensors++;
@@ -132,26 +137,37 @@ int run_gradients(const signmuon_gradient *grads, int32_t n_grads, int32_t worke
                 b.n[t] = grads[i].n;
                 b.first[t] = (int32_t)here;
                 b.bf16[t] = grads[i].dtype == SIGNMUON_BF16;
-                here += clip_units(grads[i].n);
+                here += clip_units(grads[i].n, p.unit);
             }
+            if (back) unit -= here;
+            b.partial = reinterpret_cast<double *>(ws);
+            b.factors = reinterpret_cast<const float *>(ws + p.factors);
+            b.norms = norms;
+            b.most = most;
+            b.unit = p.unit;
+            b.units = p.units;
+            b.unit0 = unit;
             b.batch_units = (int32_t)here;
-            unit += here;
+            b.workers = workers;
+            if (!back) unit += here;
             launch(b, st);
             if (int rc = sm::launch_status()) return rc;
         }
         return SIGNMUON_OK;
     };
-    if (int rc = batches(sm::launch_clip_norm)) return rc;
-    sm::ClipFinish f{};
-    f.partial = reinterpret_cast<const double *>(ws);
-    f.norms = norms;
-    f.factors = reinterpret_cast<float *>(ws + p.factors);
-    f.units = p.units;
-    f.most = clip ? most : 1.0f;
-    f.workers = workers;
-    sm::launch_clip_finish(f, st);
-    if (int rc = sm::launch_status()) return rc;
-    return clip ? batches(sm::launch_clip_scale) : SIGNMUON_OK;
+    if (int rc = batches(sm::launch_clip_norm, false)) return rc;
+    if (!clip || p.units > sm::kClipFew) {
+        sm::ClipFinish f{};
+        f.partial = reinterpret_cast<const double *>(ws);
+        f.norms = norms;
+        f.factors = reinterpret_cast<float *>(ws + p.factors);
+        f.units = p.units;
+        f.most = clip ? most : 1.0f;
+        f.workers = workers;
+        sm::launch_clip_finish(f, st);
+        if (int rc = sm::launch_status()) return rc;
+    }
+    return clip ? batches(sm::launch_clip_scale, true) : SIGNMUON_OK;
 }
 
 // ---------------------------------------------------------------------------

@@ -241,7 +241,9 @@ void launch_loss_sums(const LossSums &f, hipStream_t s);
 // ---------------------------------------------------------------------------
 // Gradient norms and clipping.
 // ---------------------------------------------------------------------------
-constexpr int kClipUnit = 16384;   // entries of a tensor and worker that a workgroup takes
+constexpr int kClipUnit = 16384;   // entries of a tensor and worker that a workgroup takes,
+constexpr int kClipSmallUnit = 2048;  // or, of few entries in all, these
+constexpr int kClipFew = 256;      // partial sums of a worker that every workgroup may add itself
 constexpr int kClipTensors = 96;   // of one launch: its descriptors are the kernel's argument
 
 struct ClipBatch {
@@ -251,7 +253,10 @@ struct ClipBatch {
     int32_t first[kClipTensors];     // unit of the batch that the tensor begins with
     bool bf16[kClipTensors];
     double *partial;                 // [workers][units]
-    const float *factors;            // [workers]
+    const float *factors;            // [workers], of more than kClipFew units
+    float *norms;                    // [workers], written by the scaling of up to kClipFew units
+    float most;
+    int32_t unit;                    // entries of one
     int64_t units;                   // of a worker, all batches
     int64_t unit0;                   // that this batch begins with
     int32_t batch_units, tensors, workers;
