@@ -339,3 +339,77 @@ def test_replays_and_streams_give_the_same_bits():
     torch.cuda.synchronize()
     for a, b in zip(outs, want):
         assert same_bits(a, b)
+
+
+WALKS = [(2, 1100, 9000, 200), (1, 4096, 20000, 520), (4, 512, 12000, 264), (1, 3000, 2500, 1030)]
+
+
+@pytest.mark.parametrize("workers,tokens,vocab,cols", WALKS)
+@pytest.mark.parametrize("x_dtype,w_dtype,grad_dtype", [(BF16, BF16, BF16), (BF16, BF16, F32), (BF16, F32, F32),
+                                                        (F32, F32, F32), (F32, BF16, BF16)])
+def test_workgroups_that_walk_several_tiles(workers, tokens, vocab, cols, x_dtype, w_dtype, grad_dtype):
+    """More tiles than run at once, of several slices: the loads of the next tile, and the stores of the one
+    before, are under way during a tile."""
+    x, w, targets, dloss = inputs(workers, tokens, vocab, cols, x_dtype, w_dtype, 71)
+    loss, lse = run_forward(x, w, targets, 1.0)
+    want = losses_in_64(*logits_in_64(x, w, 1.0), targets, vocab)
+    close(lse.flatten(), want[0], want[1], F32, "lse")
+    close(loss.flatten(), want[2], want[3], F32, "loss")
+    del want
+    dx, dw = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype)
+    want = gradients_in_64(x, w, targets, 1.0, lse, dloss, grad_dtype)
+    close(dx, want[0], want[1], x_dtype, "dx")
+    close(dw, want[2], want[3], grad_dtype, "dw")
+    again = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype)
+    assert same_bits(again[0], dx) and same_bits(again[1], dw)
+    start = torch.randn(dw.shape, generator=gen(3)).to(grad_dtype).to(DEV)
+    _, added = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype, start=start)
+    close(added, want[2] + start.double(), want[3] + U * (want[2].abs() + start.double().abs()), grad_dtype, "dw")
+
+
+def test_more_than_2_31_entries_of_x():
+    """Rows of x and dx at offsets past 2^31 entries; dw sums 2^21 tokens."""
+    tokens, vocab, cols = 1 << 21, 64, 1032
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.randn(1, tokens, cols, generator=g, device=DEV, dtype=BF16)
+    w = (torch.randn(vocab, cols, generator=g, device=DEV) * (2 / math.sqrt(cols))).to(BF16)
+    targets = torch.randint(-2, vocab, (1, tokens), generator=g, device=DEV)
+    dloss = torch.randn(1, tokens, generator=g, device=DEV)
+    loss, lse = run_forward(x, w, targets, 1.0)
+    dx, dw = run_backward(x, w, targets, 1.0, lse, dloss, F32)
+    total = torch.zeros(1, vocab, cols, dtype=torch.float64, device=DEV)
+    total_tol = torch.zeros_like(total)
+    for t0 in range(0, tokens, 1 << 17):
+        part = slice(t0, t0 + (1 << 17))
+        args = x[:, part], w, targets[:, part], 1.0, lse[:, part], dloss[:, part], F32
+        want = gradients_in_64(*args)
+        close(dx[:, part], want[0], want[1], BF16, "dx")
+        total += want[2]
+        total_tol += want[3] + 4 * math.sqrt(tokens) * U * want[2].abs().amax()
+        losses = losses_in_64(*logits_in_64(x[:, part], w, 1.0), targets[:, part], vocab)
+        close(loss[0, part], losses[2], losses[3], F32, "loss")
+    close(dw, total, total_tol, F32, "dw")
+
+
+def test_more_than_2_31_entries_of_dw():
+    workers, tokens, vocab, cols = 2, 3, 1 << 20, 2040
+    g = torch.Generator(device=DEV).manual_seed(6)
+    x = torch.randn(workers, tokens, cols, generator=g, device=DEV, dtype=BF16)
+    w = torch.randn(vocab, cols, generator=g, device=DEV, dtype=BF16).mul_(0.05)
+    targets = torch.tensor([[0, vocab - 1, 524288], [-1, 77, vocab - 2]], device=DEV)
+    dloss = torch.ones(workers, tokens, device=DEV)
+    loss, lse = run_forward(x, w, targets, 1.0)
+    dx, dw = run_backward(x, w, targets, 1.0, lse, dloss, BF16)
+    l, l_tol = logits_in_64(x, w, 1.0)
+    losses = losses_in_64(l, l_tol, targets, vocab)
+    close(loss.flatten(), losses[2], losses[3], F32, "loss")
+    rows = torch.cat([torch.arange(0, vocab, 9973, device=DEV), torch.tensor([0, 77, 524288, vocab - 2, vocab - 1], device=DEV)])
+    p = torch.exp(l - lse.double().flatten()[:, None]).view(workers, tokens, vocab)
+    for m in range(workers):
+        one = (rows[None, :] == targets[m][:, None]).double()
+        gr = torch.where((targets[m] >= 0)[:, None], p[m][:, rows] - one, 0.0)
+        want = gr.t() @ x[m].double()
+        # g in one plane, and a sum of three products; exponentials of logits that are off by l_tol
+        size = gr.abs().t() @ x[m].double().abs()
+        tol = (2.0 ** -8 + 8 * U) * size + (p[m][:, rows] * (l_tol.view(workers, tokens, vocab)[m][:, rows] + 60 * U)).t() @ x[m].double().abs()
+        close(dw[m, rows], want, tol, BF16, "dw")
