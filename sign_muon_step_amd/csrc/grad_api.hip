@@ -231,6 +231,11 @@ LossTiles loss_tiles(int64_t m, int64_t n, int64_t batch, int64_t slices, double
     return best;
 }
 
+// Planes of an operand with `planes` that meet g: all for an fp32 result. A BF16 result, whose
+// own rounding and g's are as large as one plane's, takes two (2.4e-3 of the result's norm off
+// in all, where one plane would leave 2.9e-3 and the result's rounding alone is 1.7e-3).
+inline int loss_meet(int planes, bool result32) { return result32 || planes == 1 ? planes : 2; }
+
 inline int64_t loss_slices(int64_t k, bool g32) {
     const int64_t slice = g32 ? sm::kLossWideSlice : sm::kLossSlice;
     return (k + slice - 1) / slice;
@@ -280,7 +285,7 @@ LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t 
     const int64_t here = vocab < p.piece ? vocab : p.piece;
     const bool g32 = entry == 4, x32 = x_dtype == SIGNMUON_F32;
     p.logits = loss_tiles(rows, here, 1, loss_products(x_dtype, w_dtype) * loss_slices(cols, false), 1.0, true, 1);
-    p.dx = loss_tiles(rows, cols, 1, (x32 ? loss_planes(w_dtype) : 1) * loss_slices(here, g32),
+    p.dx = loss_tiles(rows, cols, 1, loss_meet(loss_planes(w_dtype), x32) * loss_slices(here, g32),
                       !g32 ? 1.0 : x32 ? 1.65 : 0.75, cols % (x32 ? 4 : 8) == 0, 32, p.piece < vocab);
     p.parts = p.piece < vocab || p.dx.splits > 1;
     size_t at = 0;
@@ -842,7 +847,7 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
             d.batch = 1;
             d.g32 = g32;
             d.planes = x32 ? 3 : 1;
-            loss_pairs(d, d.planes, x32 ? nw : 1, g32);
+            loss_pairs(d, d.planes, loss_meet(nw, x32), g32);
             loss_set_tiles(d, p.dx);
             d.out_batch = rows;
             // in parts, or over several pieces, the sums so far lie in dx itself or in fp32 beside it
@@ -877,7 +882,7 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
             d.batch = workers;
             d.g32 = g32;
             d.planes = grad32 ? 3 : 1;
-            loss_pairs(d, d.planes, grad32 ? nx : 1, g32);
+            loss_pairs(d, d.planes, loss_meet(nx, grad32), g32);
             d.out = const_cast<void *>(at_entry(dw, v0 * cols, grad_dtype));
             d.out_batch = vocab;
             d.out_bf16 = !grad32;

@@ -16,11 +16,12 @@
 // product of planes is a longer sum: the pairs (h h), (h m), (m h), (m m),
 // (h l), (l h) leave out parts below 2^-22 of the operands' product (6e-9 of a sum of
 // random ones). Six BF16 products run at 2.6 times the rate of fp32's own matrix
-// instruction. Logits and fp32 results take all planes of their operands; a BF16
-// result takes one of g and of the operand that meets it, whose rounding is that of
-// the result. g is stored in fp32 where a result is, and its planes are made in
-// registers: it is read once for all of them. x and w are laid out as planes by a
-// pass of their own where they are not BF16 rows of whole vectors.
+// instruction. Logits and fp32 results take all planes of their operands. For a BF16
+// result g is rounded to one plane, an error as large as that of the result's own
+// rounding, and an fp32 operand that meets it is held in two. g is stored in fp32
+// where a result is, and its planes are made in registers: it is read once for all of
+// them. x and w are laid out as planes by a pass of their own where they are not BF16
+// rows of whole vectors.
 //
 // The products are computed as b a^T: the instruction's rows are out's columns,
 // so that a lane's accumulators hold four consecutive columns of one row of out,
@@ -639,7 +640,7 @@ __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_tile_
 }
 
 // Products of an fp32 a, taken apart into planes in registers, and a BF16 b. PLANES:
-// of a; 1, or 3 for the first plane of b, 2 for its second and 1 for its third. A slice
+// of a; 1 for each plane of b, or 3 for its first, 2 for its second and 1 for its third. A slice
 // is 32 k: while 16 of them are multiplied, the next 16 are read and taken apart.
 template <int KA, int TILE, int PLANES, bool WIDE, int HOW>
 __global__ __launch_bounds__(kWaves *kWave, TILE == 256 ? 1 : 2) void loss_wide_kernel(LossTile f, int total) {

@@ -115,8 +115,8 @@ def gradients_in_64(x, w, targets, scale, lse, dloss, grad_dtype):
 
     def product(rows, a, a_tol, b, b_dtype, fp32):
         n = 3 if fp32 else 1
-        # g; an fp32 operand that meets it; two pairs that are left out of three planes each
-        part = 2.0 ** (-8 * n) * (1 if b_dtype == BF16 else 4 if fp32 else 2)
+        # g; an fp32 operand that meets it (in three planes, or two); two pairs that are left out of three each
+        part = 2.0 ** (-8 * n) + (0.0 if b_dtype == BF16 else 3 * 2.0 ** -24 if fp32 else 2.0 ** -16)
         size = a.abs() @ b.abs()
         # a plane's value below 2^-126, BF16's smallest normal one, counts as 0: a factor in n planes is off
         # by 2^-126 for each (an exponential of -88 times a token of 512 is 2^-118, and passes TINY)
