@@ -14,7 +14,7 @@ LIB = os.path.join(HERE, "libsignmuon.so")
 SOURCES = [os.path.join(HERE, "csrc", f) for f in (
     "api.hip", "elementwise.hip", "ns_gemm.hip", "spectral.hip", "grad_api.hip", "embedding.hip",
     "layer_norm.hip", "f8_quant.hip", "f8_matmul.hip", "rms_norm.hip",
-    "clip.hip", "linear_loss.hip")]
+    "clip.hip", "linear_loss.hip", "linear_loss_dx.hip", "linear_loss_dw.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

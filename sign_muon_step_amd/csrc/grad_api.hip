@@ -197,33 +197,48 @@ int64_t loss_piece(int64_t vocab, int64_t most) {
 }
 
 // The tile and the parts of k of a product with `slices` slices, by a model of its time in
-// slices of a tile of 256 (about 1.4 us): a round of tiles (one of 256 or two of 128 a compute
-// unit) takes its slices and 4.5 more for the results, tiles of 128 0.58 of that (8192 x
-// 32000 x 4096 1.75 against 2.02 ms, 8192 x 50257 x 768 0.61 against 0.70; 1503 x 5003 x 515 in
-// six pairs, 120 tiles or 480, 80 against 70 us), a slice of an fp32 g's product 1.65, or 0.75
-// where one plane of it is taken; adding parts 3 and 6.6 MB of them a slice. The compute
-// units are those of a whole MI355X, not asked for, since the workspace's size is told without a
-// device.
+// slices of a tile of 256 x 256 (about 1.4 us): a round of tiles (one a compute unit, or two of
+// 128 x 128) takes its slices and 4.5 more for the results, times a shape's two factors; a slice
+// of an fp32 g's product 1.65, or 0.75 where one plane of it is taken; adding parts 3 and 10 MB
+// of them a slice. The large tile has the least traffic into LDS, two small ones a compute unit
+// hide each other's results, and the middle one fills compute units that the large one leaves
+// empty (us, large / middle / small):
+//   logits 8192 x 50257 x 768                               571 / 666 / 660
+//   logits 2048 x 10000 x 1024                               64 /  60 /  52
+//   logits and dw, fp32, 1503 x 5003 x 512, three workers   159 / 118 / 127
+//   logits and dw, fp32 W and dw, 2048 x 4000 x 2048        276 / 211 / 229
+//   logits and dx 512 x 32000 x 4096                        256 / 310 / 322
+// The compute units are those of a whole MI355X, not asked for, since the workspace's size is
+// told without a device.
 struct LossTiles {
-    int32_t tile, splits;
+    int32_t tm, tn, splits;
 };
+enum LossKind { kLogits, kNarrow, kWide };
 
-LossTiles loss_tiles(int64_t m, int64_t n, int64_t batch, int64_t slices, double slice, bool even, int most_splits,
-                     bool parts_anyway = false) {
+LossTiles loss_tiles(LossKind kind, int64_t m, int64_t n, int64_t batch, int64_t slices, double slice, bool even,
+                     int most_splits, bool parts_anyway = false) {
+    struct Shape {
+        int32_t tm, tn, slots;
+        double slice, results;
+    };
+    const Shape shapes[3] = {{256, 256, 256, 1.0, 1.0},
+                             {kind == kWide ? 128 : 256, kind == kWide ? 256 : 128, 256, kind == kNarrow ? 0.6 : 0.55, 0.7},
+                             {128, 128, 512, kind == kNarrow ? 0.66 : 0.58, 0.5}};
     LossTiles best{};
     double best_time = 0.0;
-    for (const int32_t tile : {256, 128}) {
-        if (tile == 256 && !even) continue;
-        const int64_t tiles = batch * ((m + tile - 1) / tile) * ((n + tile - 1) / tile), slots = tile == 256 ? 256 : 512;
+    for (const Shape &t : shapes) {
+        if (!even && t.tm * t.tn > 128 * 128) continue;
+        const int64_t tiles = batch * ((m + t.tm - 1) / t.tm) * ((n + t.tn - 1) / t.tn);
         for (int64_t splits = 1; splits <= most_splits; ++splits) {
             const int64_t chunk = (slices + splits - 1) / splits, parts = (slices + chunk - 1) / chunk;
             if (parts < splits) continue;
-            const double rounds = (double)((tiles * parts + slots - 1) / slots);
-            double time = rounds * (tile == 256 ? 1.0 : 0.58) * (slice * (double)chunk + 4.5);
-            if (parts > 1 || parts_anyway) time += 3.0 + (double)parts * (double)m * (double)n * 8.0 / 6.6e6;
-            if (best.tile == 0 || time < best_time) {
+            const double rounds = (double)((tiles * parts + t.slots - 1) / t.slots);
+            double time = rounds * (t.slice * slice * (double)chunk + t.results * 4.5);
+            if (parts > 1 || parts_anyway) time += 3.0 + (double)parts * (double)m * (double)n * 8.0 / 1e7;
+            if (best.tm == 0 || time < best_time) {
                 best_time = time;
-                best.tile = tile;
+                best.tm = t.tm;
+                best.tn = t.tn;
                 best.splits = (int32_t)parts;
             }
         }
@@ -255,7 +270,7 @@ LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int
     const int64_t w_row = loss_direct(w_dtype, cols) ? 0 : loss_planes(w_dtype) * p.pitch * 2;
     if (w_row && kLossForward / w_row < most) most = kLossForward / w_row;
     p.piece = loss_piece(vocab, most);
-    p.logits = loss_tiles(tokens, vocab < p.piece ? vocab : p.piece, 1,
+    p.logits = loss_tiles(kLogits, tokens, vocab < p.piece ? vocab : p.piece, 1,
                           loss_products(x_dtype, w_dtype) * loss_slices(cols, false), 1.0, true, 1);
     size_t at = 0;
     auto section = [&](int64_t bytes) {
@@ -265,7 +280,7 @@ LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int
     };
     p.x = section(loss_direct(x_dtype, cols) ? 0 : loss_planes(x_dtype) * tokens * p.pitch * 2);
     p.w = section(w_row * p.piece);
-    p.partial = section(tokens * (p.piece / (p.logits.tile / 2)) * (int64_t)sizeof(float2));
+    p.partial = section(tokens * (p.piece / (p.logits.tn / 2)) * (int64_t)sizeof(float2));
     p.state = section(p.piece < vocab ? tokens * (int64_t)sizeof(float2) : 0);
     p.target = section(tokens * (int64_t)sizeof(float));
     p.total = at;
@@ -284,8 +299,8 @@ LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t 
     p.piece = loss_piece(vocab, most);
     const int64_t here = vocab < p.piece ? vocab : p.piece;
     const bool g32 = entry == 4, x32 = x_dtype == SIGNMUON_F32;
-    p.logits = loss_tiles(rows, here, 1, loss_products(x_dtype, w_dtype) * loss_slices(cols, false), 1.0, true, 1);
-    p.dx = loss_tiles(rows, cols, 1, loss_meet(loss_planes(w_dtype), x32) * loss_slices(here, g32),
+    p.logits = loss_tiles(kLogits, rows, here, 1, loss_products(x_dtype, w_dtype) * loss_slices(cols, false), 1.0, true, 1);
+    p.dx = loss_tiles(g32 ? kWide : kNarrow, rows, cols, 1, loss_meet(loss_planes(w_dtype), x32) * loss_slices(here, g32),
                       !g32 ? 1.0 : x32 ? 1.65 : 0.75, cols % (x32 ? 4 : 8) == 0, 32, p.piece < vocab);
     p.parts = p.piece < vocab || p.dx.splits > 1;
     size_t at = 0;
@@ -323,7 +338,8 @@ void loss_pairs(sm::LossTile &f, int na, int nb, bool whole_a = false) {
 
 // The tile, and the slices of each part of k.
 void loss_set_tiles(sm::LossTile &f, const LossTiles &t) {
-    f.tile = t.tile;
+    f.tm = t.tm;
+    f.tn = t.tn;
     const int64_t slices = f.pairs * loss_slices(f.k, f.g32 && f.planes > 0);
     f.chunk = (int32_t)((slices + t.splits - 1) / t.splits);
     f.splits = (int32_t)((slices + f.chunk - 1) / f.chunk);
@@ -751,7 +767,7 @@ int signmuon_linear_cross_entropy(const void *x, signmuon_dtype x_dtype, const v
         j.loss = loss;
         j.lse = lse;
         j.rows = tokens;
-        j.blocks = (here + f.tile / 2 - 1) / (f.tile / 2);
+        j.blocks = (here + f.tn / 2 - 1) / (f.tn / 2);
         j.vocab = vocab;
         j.first = v0 == 0;
         j.last = v0 + here == vocab;
@@ -887,7 +903,7 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
             d.out_batch = vocab;
             d.out_bf16 = !grad32;
             d.add = accumulate != 0;
-            loss_set_tiles(d, loss_tiles(here, cols, workers, d.pairs * loss_slices(tokens, g32),
+            loss_set_tiles(d, loss_tiles(g32 ? kWide : kNarrow, here, cols, workers, d.pairs * loss_slices(tokens, g32),
                                          !g32 ? 1.0 : grad32 ? 1.65 : 0.75, sm::loss_even(d), 1));
             sm::launch_loss_dw(d, st);
             if (int rc = sm::launch_status()) return rc;

@@ -193,13 +193,13 @@ struct LossTile {
     int32_t batch, pairs;
     int32_t splits, chunk;     // chunk: slices of a split, of all pairs' slices in a row
     uint32_t order_a, order_b;  // the planes of pair i in bits 2 i on
-    int32_t tile;              // 256 or 128
+    int32_t tm, tn;            // the tile: 256 x 256, 128 x 128, or between: 256 x 128, a fp32: 128 x 256
     int32_t planes;            // of an fp32 a: 1 or 3
     bool g32;                  // g is fp32, not BF16
     // logits
     const void *rows[3];       // 4 bytes a row, row_step bytes apart: the targets, and for g what LossPlanes writes
     int32_t row_step;
-    float2 *partial;           // [columns of tile / 2][m]: maximum and sum, in units of log 2
+    float2 *partial;           // [columns of tn / 2][m]: maximum and sum, in units of log 2
     float *target;             // [m] logit of the target
     void *g;                   // [m][g_pitch]
     int64_t g_pitch;
@@ -210,7 +210,7 @@ struct LossTile {
     int64_t out_batch;         // rows between batch entries, and between parts of k
     bool out_bf16, add;        // add to what out holds (dw alone)
 };
-// Whether out's rows are whole vectors; where they are not, tiles are of 128.
+// Whether out's rows are whole vectors; where they are not, tiles are of 128 x 128.
 inline bool loss_even(const LossTile &f) { return f.n % (f.out_bf16 ? 8 : 4) == 0; }
 void launch_loss_logits(const LossTile &f, bool grad, hipStream_t s);
 void launch_loss_dx(const LossTile &f, hipStream_t s);

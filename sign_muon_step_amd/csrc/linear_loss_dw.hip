@@ -1,0 +1,25 @@
+// linear_loss_dw.hip -- the loss's dw_m = g_m^T x_m (linear_loss.hip): both operands' rows
+// are k.
+#include "loss_tiles.h"
+
+namespace sm {
+namespace {
+
+template <int HOW>
+void launch_dw(const LossTile &f, hipStream_t s) {
+    if (!f.g32)
+        launch_tiles<kCols16, kCols16, kValues, false, HOW>(f, s);
+    else
+        f.planes == 3 ? launch_wide<kCols32, 3, true, HOW>(f, s) : launch_wide<kCols32, 1, false, HOW>(f, s);
+}
+
+}  // namespace
+
+void launch_loss_dw(const LossTile &f, hipStream_t s) {
+    if (!loss_even(f))
+        launch_dw<kUneven>(f, s);
+    else
+        f.add ? launch_dw<kAdd>(f, s) : launch_dw<kEven>(f, s);
+}
+
+}  // namespace sm
