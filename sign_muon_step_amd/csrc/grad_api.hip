@@ -199,8 +199,8 @@ int64_t loss_piece(int64_t vocab, int64_t most) {
 // The tile and the parts of k of a product with `slices` slices, by a model of its time in
 // slices of a tile of 256 x 256 (about 1.4 us): a round of tiles (one a compute unit, or two of
 // 128 x 128) takes its slices and 4.5 more for the results, times a shape's two factors; a slice
-// of an fp32 g's product 1.65, or 0.75 where one plane of it is taken; adding parts 3 and 10 MB
-// of them a slice. The large tile has the least traffic into LDS, two small ones a compute unit
+// of an fp32 g's product 1.65, or 0.75 where one plane of it is taken; adding parts 3, or 4.5
+// of logits, and 10 MB of them a slice. The large tile has the least traffic into LDS, two small ones a compute unit
 // hide each other's results, and the middle one fills compute units that the large one leaves
 // empty (us, large / middle / small):
 //   logits 8192 x 50257 x 768                               571 / 666 / 660
@@ -216,7 +216,7 @@ struct LossTiles {
 enum LossKind { kLogits, kNarrow, kWide };
 
 LossTiles loss_tiles(LossKind kind, int64_t m, int64_t n, int64_t batch, int64_t slices, double slice, bool even,
-                     int most_splits, bool parts_anyway = false) {
+                     int most_splits, bool summed = false) {
     struct Shape {
         int32_t tm, tn, slots;
         double slice, results;
@@ -234,7 +234,7 @@ LossTiles loss_tiles(LossKind kind, int64_t m, int64_t n, int64_t batch, int64_t
             if (parts < splits) continue;
             const double rounds = (double)((tiles * parts + t.slots - 1) / t.slots);
             double time = rounds * (t.slice * slice * (double)chunk + t.results * 4.5);
-            if (parts > 1 || parts_anyway) time += 3.0 + (double)parts * (double)m * (double)n * 8.0 / 1e7;
+            if (parts > 1 || summed) time += (kind == kLogits ? 4.5 : 3.0) + (double)parts * (double)m * (double)n * 8.0 / 1e7;
             if (best.tm == 0 || time < best_time) {
                 best_time = time;
                 best.tm = t.tm;
@@ -251,6 +251,11 @@ LossTiles loss_tiles(LossKind kind, int64_t m, int64_t n, int64_t batch, int64_t
 // in all, where one plane would leave 2.9e-3 and the result's rounding alone is 1.7e-3).
 inline int loss_meet(int planes, bool result32) { return result32 || planes == 1 ? planes : 2; }
 
+// Up to so many tokens of all workers, g is held in fp32 and met in three planes for a BF16
+// result too. The results of many tokens are off by g's rounding and their own, 2^(1/2) of the
+// latter alone; of few, an entry or two of g decide, their target's, and may be off by 2.4 times.
+constexpr int64_t kLossFew = 128;
+
 inline int64_t loss_slices(int64_t k, bool g32) {
     const int64_t slice = g32 ? sm::kLossWideSlice : sm::kLossSlice;
     return (k + slice - 1) / slice;
@@ -263,6 +268,25 @@ struct LossPlan {
     size_t x, w, partial, state, target, row[3], g, sum, part, total;
 };
 
+constexpr int kLossParts = 32;  // of k, at most
+inline int64_t loss_part_pitch(int64_t n) { return (n + 3) / 4 * 4; }
+// Bytes of the logits' parts of k.
+int64_t loss_logit_parts(const LossPlan &p, int64_t rows, int64_t vocab) {
+    const int64_t here = vocab < p.piece ? vocab : p.piece;
+    return p.logits.splits > 1 ? p.logits.splits * rows * loss_part_pitch(here) * (int64_t)sizeof(float) : 0;
+}
+// The logits' product of a piece, and what is made of parts of k.
+int loss_logits(sm::LossTile &f, void *parts, bool grad, hipStream_t st) {
+    f.out = parts;
+    f.out_batch = f.m;
+    f.out_pitch = loss_part_pitch(f.n);
+    sm::launch_loss_logits(f, grad, st);
+    if (int rc = sm::launch_status()) return rc;
+    if (f.splits == 1) return SIGNMUON_OK;
+    sm::launch_loss_parts(f, grad, st);
+    return sm::launch_status();
+}
+
 LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int w_dtype) {
     LossPlan p{};
     p.pitch = sm::loss_pitch(cols);
@@ -271,7 +295,7 @@ LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int
     if (w_row && kLossForward / w_row < most) most = kLossForward / w_row;
     p.piece = loss_piece(vocab, most);
     p.logits = loss_tiles(kLogits, tokens, vocab < p.piece ? vocab : p.piece, 1,
-                          loss_products(x_dtype, w_dtype) * loss_slices(cols, false), 1.0, true, 1);
+                          loss_products(x_dtype, w_dtype) * loss_slices(cols, false), 1.0, true, kLossParts);
     size_t at = 0;
     auto section = [&](int64_t bytes) {
         const size_t here = at;
@@ -281,6 +305,7 @@ LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int
     p.x = section(loss_direct(x_dtype, cols) ? 0 : loss_planes(x_dtype) * tokens * p.pitch * 2);
     p.w = section(w_row * p.piece);
     p.partial = section(tokens * (p.piece / (p.logits.tn / 2)) * (int64_t)sizeof(float2));
+    p.part = section(loss_logit_parts(p, tokens, vocab));
     p.state = section(p.piece < vocab ? tokens * (int64_t)sizeof(float2) : 0);
     p.target = section(tokens * (int64_t)sizeof(float));
     p.total = at;
@@ -292,17 +317,20 @@ LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t 
     LossPlan p{};
     const int64_t rows = workers * tokens;
     p.pitch = sm::loss_pitch(cols);
-    const int64_t entry = x_dtype == SIGNMUON_F32 || grad_dtype == SIGNMUON_F32 ? 4 : 2;  // bytes of g's
+    const bool few = rows <= kLossFew;
+    const int64_t entry = x_dtype == SIGNMUON_F32 || grad_dtype == SIGNMUON_F32 || few ? 4 : 2;  // bytes of g's
     int64_t most = kLossBackward / (entry * rows);
     const int64_t w_row = loss_direct(w_dtype, cols) ? 0 : loss_planes(w_dtype) * p.pitch * 2;
     if (w_row && kLossBackward / w_row < most) most = kLossBackward / w_row;
     p.piece = loss_piece(vocab, most);
     const int64_t here = vocab < p.piece ? vocab : p.piece;
     const bool g32 = entry == 4, x32 = x_dtype == SIGNMUON_F32;
-    p.logits = loss_tiles(kLogits, rows, here, 1, loss_products(x_dtype, w_dtype) * loss_slices(cols, false), 1.0, true, 1);
+    const bool summed = p.piece < vocab || (few && !x32);  // that product has fp32 results
+    p.logits = loss_tiles(kLogits, rows, here, 1, loss_products(x_dtype, w_dtype) * loss_slices(cols, false), 1.0, true,
+                          kLossParts);
     p.dx = loss_tiles(g32 ? kWide : kNarrow, rows, cols, 1, loss_meet(loss_planes(w_dtype), x32) * loss_slices(here, g32),
-                      !g32 ? 1.0 : x32 ? 1.65 : 0.75, cols % (x32 ? 4 : 8) == 0, 32, p.piece < vocab);
-    p.parts = p.piece < vocab || p.dx.splits > 1;
+                      !g32 ? 1.0 : x32 || few ? 1.65 : 0.75, cols % (x32 ? 4 : 8) == 0, kLossParts, summed);
+    p.parts = summed || p.dx.splits > 1;
     size_t at = 0;
     auto section = [&](int64_t bytes) {
         const size_t here = at;
@@ -314,7 +342,10 @@ LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t 
     for (size_t &r : p.row) r = section(rows * 4);
     p.g = section(entry * rows * p.piece);
     p.sum = section(p.piece < vocab && !x32 ? rows * cols * (int64_t)sizeof(float) : 0);
-    p.part = section(p.parts ? p.dx.splits * rows * cols * (int64_t)sizeof(float) : 0);
+    // the logits' parts are read before dx's are written
+    const int64_t dx_part = p.parts ? p.dx.splits * rows * cols * (int64_t)sizeof(float) : 0;
+    const int64_t logit_part = loss_logit_parts(p, rows, vocab);
+    p.part = section(dx_part > logit_part ? dx_part : logit_part);
     p.total = at;
     return p;
 }
@@ -756,8 +787,7 @@ int signmuon_linear_cross_entropy(const void *x, signmuon_dtype x_dtype, const v
         f.target = reinterpret_cast<float *>(ws + p.target);
         f.vocab0 = v0;
         f.factor = scale * kLog2E;
-        sm::launch_loss_logits(f, false, st);
-        if (int rc = sm::launch_status()) return rc;
+        if (int rc = loss_logits(f, ws + p.part, false, st)) return rc;
         sm::LossJoin j{};
         j.partial = f.partial;
         j.state = reinterpret_cast<float2 *>(ws + p.state);
@@ -767,7 +797,8 @@ int signmuon_linear_cross_entropy(const void *x, signmuon_dtype x_dtype, const v
         j.loss = loss;
         j.lse = lse;
         j.rows = tokens;
-        j.blocks = (here + f.tn / 2 - 1) / (f.tn / 2);
+        const int64_t block = f.splits > 1 ? sm::kLossBlock : f.tn / 2;
+        j.blocks = (here + block - 1) / block;
         j.vocab = vocab;
         j.first = v0 == 0;
         j.last = v0 + here == vocab;
@@ -809,7 +840,7 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
     const bool x32 = x_dtype == SIGNMUON_F32, grad32 = grad_dtype == SIGNMUON_F32;
     const int nx = loss_planes(x_dtype), nw = loss_planes(w_dtype);
     void *const g = ws + p.g;
-    const bool g32 = (x32 && dx) || (grad32 && dw);
+    const bool few = rows <= kLossFew, g32 = (x32 && dx) || (grad32 && dw) || few;
     const int64_t g_entry = g32 ? 4 : 2;
     sm::LossPlanes xs = loss_to_planes(x, x_dtype, rows, cols, p.pitch, ws + p.x);
     xs.targets = targets;
@@ -849,8 +880,7 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
         f.g_pitch = g_pitch;
         f.vocab0 = v0;
         f.factor = scale * kLog2E;
-        sm::launch_loss_logits(f, true, st);
-        if (int rc = sm::launch_status()) return rc;
+        if (int rc = loss_logits(f, ws + p.part, true, st)) return rc;
         if (dx) {
             sm::LossTile d{};
             d.a[0] = g;
@@ -862,10 +892,11 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
             d.k = here;
             d.batch = 1;
             d.g32 = g32;
-            d.planes = x32 ? 3 : 1;
+            d.planes = x32 || few ? 3 : 1;
             loss_pairs(d, d.planes, loss_meet(nw, x32), g32);
             loss_set_tiles(d, p.dx);
             d.out_batch = rows;
+            d.out_pitch = cols;
             // in parts, or over several pieces, the sums so far lie in dx itself or in fp32 beside it
             float *const sums = x32 ? static_cast<float *>(dx) : reinterpret_cast<float *>(ws + p.sum);
             d.out = p.parts ? ws + p.part : dx;
@@ -897,14 +928,16 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
             d.k = tokens;
             d.batch = workers;
             d.g32 = g32;
-            d.planes = grad32 ? 3 : 1;
+            d.planes = grad32 || few ? 3 : 1;
             loss_pairs(d, d.planes, loss_meet(nx, grad32), g32);
             d.out = const_cast<void *>(at_entry(dw, v0 * cols, grad_dtype));
             d.out_batch = vocab;
+            d.out_pitch = cols;
             d.out_bf16 = !grad32;
             d.add = accumulate != 0;
             loss_set_tiles(d, loss_tiles(g32 ? kWide : kNarrow, here, cols, workers, d.pairs * loss_slices(tokens, g32),
-                                         !g32 ? 1.0 : grad32 ? 1.65 : 0.75, sm::loss_even(d), 1));
+                                         !g32 ? 1.0 : d.planes == 3 ? 1.65 : 0.75,
+                                         sm::loss_even(d) && (grad32 || !few), 1));
             sm::launch_loss_dw(d, st);
             if (int rc = sm::launch_status()) return rc;
         }

@@ -208,11 +208,15 @@ struct LossTile {
     // values
     void *out;
     int64_t out_batch;         // rows between batch entries, and between parts of k
+    int64_t out_pitch;         // entries of a row: n, or for parts of logits more, which hold nothing
     bool out_bf16, add;        // add to what out holds (dw alone)
 };
 // Whether out's rows are whole vectors; where they are not, tiles are of 128 x 128.
-inline bool loss_even(const LossTile &f) { return f.n % (f.out_bf16 ? 8 : 4) == 0; }
+inline bool loss_even(const LossTile &f) { return f.out_pitch % (f.out_bf16 ? 8 : 4) == 0; }
+// Logits in parts of k go to out, and launch_loss_parts makes of them what the tiles make of whole ones.
 void launch_loss_logits(const LossTile &f, bool grad, hipStream_t s);
+constexpr int kLossBlock = 256;  // columns of a row that share a maximum and a sum there
+void launch_loss_parts(const LossTile &f, bool grad, hipStream_t s);
 void launch_loss_dx(const LossTile &f, hipStream_t s);
 void launch_loss_dw(const LossTile &f, hipStream_t s);
 

@@ -78,6 +78,65 @@ __global__ __launch_bounds__(256) void loss_planes_kernel(LossPlanes f) {
     }
 }
 
+// Logits whose sums over k came in parts, added in order: a wave takes kLossBlock
+// columns of a row, four a lane. Forward it leaves their maximum and sum, backward g.
+template <bool GRAD, bool WIDE>
+__global__ __launch_bounds__(256) void loss_parts_kernel(LossTile f) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int64_t blocks = (f.n + kLossBlock - 1) / kLossBlock, part = f.m * f.out_pitch;
+    for (int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; i < f.m * blocks; i += (int64_t)gridDim.x * 4) {
+        const int64_t row = i / blocks, block = i - row * blocks, col = block * kLossBlock + lane * 4;
+        const int have = left(f.n, col) < 4 ? left(f.n, col) : 4;
+        f32x4 l = {};
+        if (have > 0) {
+            const float *p = static_cast<const float *>(f.out) + row * f.out_pitch + col;
+            for (int s = 0; s < f.splits; s += 8) {  // loads before sums
+                f32x4 q[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    q[j] = *reinterpret_cast<const f32x4 *>(p + (s + j < f.splits ? s + j : s) * part);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (s + j < f.splits) l += q[j];
+            }
+        }
+        const int32_t t = *reinterpret_cast<const int32_t *>(static_cast<const char *>(f.rows[0]) + row * f.row_step);
+        const uint32_t at = (uint32_t)t - (uint32_t)(f.vocab0 + col);  // the target's place among the four
+        if constexpr (GRAD) {
+            const float base = static_cast<const float *>(f.rows[1])[row], d = static_cast<const float *>(f.rows[2])[row];
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = __builtin_amdgcn_exp2f(fmaf(l[j], f.factor, -base));
+                v[j] = j < have && t >= 0 ? d * (at == (uint32_t)j ? p - 1.0f : p) : 0.0f;
+            }
+            if constexpr (WIDE)
+                *reinterpret_cast<f32x4 *>(static_cast<float *>(f.g) + row * f.g_pitch + col) = f32x4{v[0], v[1], v[2], v[3]};
+            else
+                *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(f.g) + row * f.g_pitch + col) =
+                    u32x2{to_bf16x2(v[0], v[1]), to_bf16x2(v[2], v[3])};
+        } else {
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                l[j] = j < have ? l[j] * f.factor : -INFINITY;
+                top = fmaxf(top, l[j]);
+                // the low half of a target of 64 bits, as in the tiles
+                if (at == (uint32_t)j && j < have) f.target[row] = l[j];
+            }
+#pragma unroll
+            for (int d = 1; d < kWave; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+            const float base = top == -INFINITY ? 0.0f : top;
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum += __builtin_amdgcn_exp2f(l[j] - base);
+#pragma unroll
+            for (int d = 1; d < kWave; d *= 2) sum += __shfl_xor(sum, d);
+            if (lane == 0) f.partial[block * f.m + row] = make_float2(top, sum);
+        }
+    }
+}
+
 // The partial maxima and sums of f.group rows (a power of 2, up to 64): 1024 / group
 // threads of a row take every so manieth block of columns, eight at a time, and
 // are joined in a tree, with what earlier pieces of the vocabulary left.
@@ -128,11 +187,15 @@ __global__ __launch_bounds__(256) void loss_sums_kernel(LossSums f) {
         const int have = (int)(f.total - at < 4 ? f.total - at : 4);
         float v[4];
         load_n<false>(f.prev, at, f.prev ? have : 0, v);
-        for (int s = 0; s < f.splits; ++s) {
-            float p[4];
-            load_n<false>(f.partial, s * f.total + at, have, p);
+        for (int s = 0; s < f.splits; s += 8) {  // loads before sums
+            float p[8][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] += p[j];
+            for (int i = 0; i < 8; ++i) load_n<false>(f.partial, (s + i < f.splits ? s + i : s) * f.total + at, have, p[i]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (s + i < f.splits)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] += p[i][j];
         }
         if (f.out_bf16)
             store_n<true>(f.out, at, have, v);
@@ -153,10 +216,23 @@ void launch_loss_planes(const LossPlanes &f, hipStream_t s) {
 }
 
 void launch_loss_logits(const LossTile &f, bool grad, hipStream_t s) {
-    if (!grad)
+    if (f.splits > 1)
+        launch_tiles<kRows16, kRows16, kValues, true>(f, s);
+    else if (!grad)
         launch_tiles<kRows16, kRows16, kLse, true>(f, s);
     else
         f.g32 ? launch_tiles<kRows16, kRows16, kGrad, true>(f, s) : launch_tiles<kRows16, kRows16, kGrad, false>(f, s);
+}
+
+void launch_loss_parts(const LossTile &f, bool grad, hipStream_t s) {
+    const int64_t waves = f.m * ((f.n + kLossBlock - 1) / kLossBlock), blocks = (waves + 3) / 4;
+    const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536));
+    if (!grad)
+        loss_parts_kernel<false, true><<<grid, 256, 0, s>>>(f);
+    else if (f.g32)
+        loss_parts_kernel<true, true><<<grid, 256, 0, s>>>(f);
+    else
+        loss_parts_kernel<true, false><<<grid, 256, 0, s>>>(f);
 }
 
 void launch_loss_join(LossJoin f, hipStream_t s) {

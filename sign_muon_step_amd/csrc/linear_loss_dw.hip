@@ -9,6 +9,8 @@ template <int HOW>
 void launch_dw(const LossTile &f, hipStream_t s) {
     if (!f.g32)
         launch_tiles<kCols16, kCols16, kValues, false, HOW>(f, s);
+    else if (f.planes == 3 && f.out_bf16)  // of few tokens: bound by the results
+        loss_wide_kernel<kCols32, 128, 128, 3, false, HOW><<<grid_of(f), kWaves * kWave, 0, s>>>(f, tiles_of(f));
     else
         f.planes == 3 ? launch_wide<kCols32, 3, true, HOW>(f, s) : launch_wide<kCols32, 1, false, HOW>(f, s);
 }

@@ -461,9 +461,9 @@ __device__ __forceinline__ void finish_grad(const LossTile &f, Acc<FM, FN> &acc,
 template <int FM, int FN, bool WIDE, int BYTES, int HOW>
 __device__ __forceinline__ void finish_values(const LossTile &f, Acc<FM, FN> &acc, char *mine, const Tile &t, int64_t row0,
                                               int64_t col0, int lane) {
-    const int64_t first = (f.out_batch * (t.split * (int64_t)f.batch + t.batch) + row0) * f.n + col0;
-    const int rows = (int)(f.m - row0 < FM * 32 ? f.m - row0 : FM * 32), cols = (int)(f.n - col0 < FN * 32 ? f.n - col0 : FN * 32);
-    write<FM, FN, WIDE, BYTES, HOW, kKept>(acc, mine, static_cast<char *>(f.out) + first * (WIDE ? 4 : 2), f.n, rows, cols, lane,
+    const int64_t first = (f.out_batch * (t.split * (int64_t)f.batch + t.batch) + row0) * f.out_pitch + col0;
+    const int rows = (int)(f.m - row0 < FM * 32 ? f.m - row0 : FM * 32), cols = (int)(f.out_pitch - col0 < FN * 32 ? f.out_pitch - col0 : FN * 32);
+    write<FM, FN, WIDE, BYTES, HOW, kKept>(acc, mine, static_cast<char *>(f.out) + first * (WIDE ? 4 : 2), f.out_pitch, rows, cols, lane,
                                [&](int i, int n, int q, float(&v)[4]) {
 #pragma unroll
                                    for (int j = 0; j < 4; ++j) v[j] = acc[i][n][q * 4 + j];
@@ -471,7 +471,7 @@ __device__ __forceinline__ void finish_values(const LossTile &f, Acc<FM, FN> &ac
                                    const int row = i * 32 + (lane & 31), col = column(n, q * 4, lane);
                                    const int have = row >= rows ? 0 : left(cols, col) < 4 ? left(cols, col) : 4;
                                    float p[4];
-                                   load_n<!WIDE>(f.out, first + row * f.n + col, have, p);
+                                   load_n<!WIDE>(f.out, first + row * f.out_pitch + col, have, p);
 #pragma unroll
                                    for (int j = 0; j < 4; ++j) v[j] += p[j];
                                });

@@ -97,8 +97,8 @@ def run_backward(x, w, targets, scale, lse, dloss, grad_dtype, start=None, want=
     return outs
 
 
-def gradients_in_64(x, w, targets, scale, lse, dloss, grad_dtype):
-    """dx and dw from the given lse, and their tolerances."""
+def gradients_in_64(x, w, targets, scale, lse, dloss, grad_dtype, whole_g=False):
+    """dx and dw from the given lse, and their tolerances. whole_g: BF16 results of g in three planes."""
     workers, tokens, cols = x.shape
     vocab = w.shape[0]
     l, l_tol = logits_in_64(x, w, scale)
@@ -114,7 +114,7 @@ def gradients_in_64(x, w, targets, scale, lse, dloss, grad_dtype):
     x64, w64 = x.double().flatten(0, 1), w.double()
 
     def product(rows, a, a_tol, b, b_dtype, fp32):
-        n = 3 if fp32 else 1
+        n = 3 if fp32 or whole_g else 1
         # g; an fp32 operand that meets it (in three planes, or two); two pairs that are left out of three each
         part = 2.0 ** (-8 * n) + (0.0 if b_dtype == BF16 else 3 * 2.0 ** -24 if fp32 else 2.0 ** -16)
         size = a.abs() @ b.abs()
@@ -362,6 +362,78 @@ def test_workgroups_that_walk_several_tiles(workers, tokens, vocab, cols, x_dtyp
     close(dw, want[2], want[3], grad_dtype, "dw")
     again = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype)
     assert same_bits(again[0], dx) and same_bits(again[1], dw)
+    start = torch.randn(dw.shape, generator=gen(3)).to(grad_dtype).to(DEV)
+    _, added = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype, start=start)
+    close(added, want[2] + start.double(), want[3] + U * (want[2].abs() + start.double().abs()), grad_dtype, "dw")
+
+
+# (of one tile of 128 x 128 or a few, with hundreds of slices of k; rows that are no whole vectors)
+LONG = [(1, 1, 130, 8200), (2, 3, 257, 5000), (1, 129, 200, 4099), (3, 200, 333, 6152)]
+
+
+@pytest.mark.parametrize("workers,tokens,vocab,cols", LONG)
+@pytest.mark.parametrize("x_dtype,w_dtype,grad_dtype", [(BF16, BF16, BF16), (BF16, BF16, F32), (BF16, F32, F32),
+                                                        (F32, F32, F32), (F32, BF16, BF16)])
+def test_logits_of_long_rows(workers, tokens, vocab, cols, x_dtype, w_dtype, grad_dtype):
+    """Few logits of many columns, whose sums come in parts."""
+    x, w, targets, dloss = inputs(workers, tokens, vocab, cols, x_dtype, w_dtype, 83)
+    loss, lse = run_forward(x, w, targets, 1.0)
+    want = losses_in_64(*logits_in_64(x, w, 1.0), targets, vocab)
+    close(lse.flatten(), want[0], want[1], F32, "lse")
+    close(loss.flatten(), want[2], want[3], F32, "loss")
+    assert bool((loss.flatten()[~want[4]] == 0).all())
+    dx, dw = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype)
+    want = gradients_in_64(x, w, targets, 1.0, lse, dloss, grad_dtype)
+    close(dx, want[0], want[1], x_dtype, "dx")
+    close(dw, want[2], want[3], grad_dtype, "dw")
+    again = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype)
+    assert same_bits(again[0], dx) and same_bits(again[1], dw)
+    start = torch.randn(dw.shape, generator=gen(3)).to(grad_dtype).to(DEV)
+    _, added = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype, start=start)
+    close(added, want[2] + start.double(), want[3] + U * (want[2].abs() + start.double().abs()), grad_dtype, "dw")
+
+
+def test_long_rows_of_padding_and_masked_vocabulary():
+    """In parts of k too: tokens without a target hold anything, and a vocabulary entry of minus infinity in
+    BF16 counts as nothing."""
+    x, w, targets, dloss = inputs(2, 40, 300, 6144, BF16, BF16, 84)
+    x, w = x.abs(), w.clone()
+    w[17] = -math.inf
+    targets[targets == 17] = 18
+    targets[1, 3:] = -100
+    x[1, 3:] = math.nan
+    loss, lse = run_forward(x, w, targets, 1.0)
+    l, l_tol = logits_in_64(x.nan_to_num(), w[torch.arange(300, device=DEV) != 17], 1.0)
+    there = ((targets >= 0) & (targets < 300)).flatten()
+    rest = torch.where(targets > 17, targets - 1, targets)
+    want = losses_in_64(l, l_tol, torch.where(there.view(2, 40), rest, -1), 299)
+    # nought times infinity is no number: of tokens that hold a nought, nor is that logit
+    nought = (x == 0).any(-1).flatten() & there
+    assert int(nought.sum()) == 1
+    assert bool(lse.flatten()[nought].isnan().all()) and bool(loss.flatten()[nought].isnan().all())
+    counts = there & ~nought
+    close(lse.flatten()[counts], want[0][counts], want[1][counts], F32, "lse")
+    close(loss.flatten()[~nought], want[2][~nought], want[3][~nought], F32, "loss")
+    w[17] = 0
+    lse = torch.where(counts.view(2, 40), lse, 0)
+    dx, dw = run_backward(x, w, targets, 1.0, torch.where(there.view(2, 40), lse, math.nan), dloss, BF16)
+    want = gradients_in_64(x.nan_to_num(), w, targets, 1.0, lse, dloss, BF16)
+    close(dx, want[0], want[1], BF16, "dx")
+    close(dw, want[2], want[3], BF16, "dw")
+
+
+@pytest.mark.parametrize("workers,tokens,vocab,cols", [(1, 1, 900, 256), (1, 5, 2000, 130), (8, 2, 700, 264), (1, 128, 5000, 96),
+                                                       (3, 42, 300, 4100)])
+@pytest.mark.parametrize("x_dtype,w_dtype,grad_dtype", [(BF16, BF16, BF16), (BF16, F32, BF16), (F32, BF16, BF16),
+                                                        (BF16, BF16, F32)])
+def test_few_tokens_keep_g_whole(workers, tokens, vocab, cols, x_dtype, w_dtype, grad_dtype):
+    """Up to 128 tokens, BF16 results are off by their own rounding, and by no rounding of g."""
+    x, w, targets, dloss = inputs(workers, tokens, vocab, cols, x_dtype, w_dtype, 85, pad=tokens > 1)
+    _, lse = run_forward(x, w, targets, 1.0)
+    dx, dw = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype)
+    want = gradients_in_64(x, w, targets, 1.0, lse, dloss, grad_dtype, whole_g=True)
+    close(dx, want[0], want[1], x_dtype, "dx")
+    close(dw, want[2], want[3], grad_dtype, "dw")
     start = torch.randn(dw.shape, generator=gen(3)).to(grad_dtype).to(DEV)
     _, added = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype, start=start)
     close(added, want[2] + start.double(), want[3] + U * (want[2].abs() + start.double().abs()), grad_dtype, "dw")
