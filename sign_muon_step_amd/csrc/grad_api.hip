@@ -263,7 +263,8 @@ inline int64_t loss_slices(int64_t k, bool g32) {
 
 struct LossPlan {
     int64_t piece, pitch;
-    LossTiles logits, dx;
+    LossTiles logits, dx, dw;
+    bool few, g32;
     bool parts;                   // of dx, summed by a launch of their own
     size_t x, w, partial, state, target, row[3], g, sum, part, total;
 };
@@ -313,24 +314,31 @@ LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int
 }
 
 LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int w_dtype,
-                        int grad_dtype) {
+                        int grad_dtype, bool want_dw = true) {
     LossPlan p{};
     const int64_t rows = workers * tokens;
     p.pitch = sm::loss_pitch(cols);
-    const bool few = rows <= kLossFew;
-    const int64_t entry = x_dtype == SIGNMUON_F32 || grad_dtype == SIGNMUON_F32 || few ? 4 : 2;  // bytes of g's
+    const bool x32 = x_dtype == SIGNMUON_F32, grad32 = grad_dtype == SIGNMUON_F32, few = rows <= kLossFew;
+    const bool g32 = x32 || grad32 || few;
+    p.few = few;
+    p.g32 = g32;
+    const int64_t entry = g32 ? 4 : 2;  // bytes of g's
     int64_t most = kLossBackward / (entry * rows);
     const int64_t w_row = loss_direct(w_dtype, cols) ? 0 : loss_planes(w_dtype) * p.pitch * 2;
     if (w_row && kLossBackward / w_row < most) most = kLossBackward / w_row;
     p.piece = loss_piece(vocab, most);
     const int64_t here = vocab < p.piece ? vocab : p.piece;
-    const bool g32 = entry == 4, x32 = x_dtype == SIGNMUON_F32;
     const bool summed = p.piece < vocab || (few && !x32);  // that product has fp32 results
     p.logits = loss_tiles(kLogits, rows, here, 1, loss_products(x_dtype, w_dtype) * loss_slices(cols, false), 1.0, true,
                           kLossParts);
     p.dx = loss_tiles(g32 ? kWide : kNarrow, rows, cols, 1, loss_meet(loss_planes(w_dtype), x32) * loss_slices(here, g32),
                       !g32 ? 1.0 : x32 || few ? 1.65 : 0.75, cols % (x32 ? 4 : 8) == 0, kLossParts, summed);
     p.parts = summed || p.dx.splits > 1;
+    // one plane of g, or three, which meet as many of x, or fewer, times tokens
+    const bool whole = grad32 || few;
+    p.dw = loss_tiles(g32 ? kWide : kNarrow, here, cols, workers,
+                      loss_meet(loss_planes(x_dtype), grad32) * loss_slices(tokens, g32), !g32 ? 1.0 : whole ? 1.65 : 0.75,
+                      cols % (grad32 ? 4 : 8) == 0 && (grad32 || !few), kLossParts);
     size_t at = 0;
     auto section = [&](int64_t bytes) {
         const size_t here = at;
@@ -342,10 +350,11 @@ LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t 
     for (size_t &r : p.row) r = section(rows * 4);
     p.g = section(entry * rows * p.piece);
     p.sum = section(p.piece < vocab && !x32 ? rows * cols * (int64_t)sizeof(float) : 0);
-    // the logits' parts are read before dx's are written
+    // the parts of each product are read before the next one's are written
     const int64_t dx_part = p.parts ? p.dx.splits * rows * cols * (int64_t)sizeof(float) : 0;
-    const int64_t logit_part = loss_logit_parts(p, rows, vocab);
-    p.part = section(dx_part > logit_part ? dx_part : logit_part);
+    const int64_t dw_part = want_dw && p.dw.splits > 1 ? p.dw.splits * workers * here * cols * (int64_t)sizeof(float) : 0;
+    const int64_t logit_part = loss_logit_parts(p, rows, vocab), part = dx_part > dw_part ? dx_part : dw_part;
+    p.part = section(part > logit_part ? part : logit_part);
     p.total = at;
     return p;
 }
@@ -831,7 +840,7 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
         !dtype_ok(grad_dtype))
         return SIGNMUON_EDTYPE;
     if (!all_aligned(x, w, targets, lse, dloss, dx, dw)) return SIGNMUON_EALIGN;
-    const LossPlan p = loss_grad_plan(workers, tokens, vocab, cols, x_dtype, w_dtype, grad_dtype);
+    const LossPlan p = loss_grad_plan(workers, tokens, vocab, cols, x_dtype, w_dtype, grad_dtype, dw != nullptr);
     if (int rc = check_workspace(workspace, workspace_bytes, p.total)) return rc;
     char *ws = static_cast<char *>(workspace);
     const hipStream_t st = static_cast<hipStream_t>(stream);
@@ -840,7 +849,7 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
     const bool x32 = x_dtype == SIGNMUON_F32, grad32 = grad_dtype == SIGNMUON_F32;
     const int nx = loss_planes(x_dtype), nw = loss_planes(w_dtype);
     void *const g = ws + p.g;
-    const bool few = rows <= kLossFew, g32 = (x32 && dx) || (grad32 && dw) || few;
+    const bool few = p.few, g32 = p.g32;
     const int64_t g_entry = g32 ? 4 : 2;
     sm::LossPlanes xs = loss_to_planes(x, x_dtype, rows, cols, p.pitch, ws + p.x);
     xs.targets = targets;
@@ -908,7 +917,7 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
                 u.partial = reinterpret_cast<const float *>(ws + p.part);
                 u.prev = first ? nullptr : sums;
                 u.out = last ? dx : sums;
-                u.total = rows * cols;
+                u.total = u.pitch = rows * cols;
                 u.splits = d.splits;
                 u.out_bf16 = last && !x32;
                 sm::launch_loss_sums(u, st);
@@ -930,16 +939,31 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
             d.g32 = g32;
             d.planes = grad32 || few ? 3 : 1;
             loss_pairs(d, d.planes, loss_meet(nx, grad32), g32);
-            d.out = const_cast<void *>(at_entry(dw, v0 * cols, grad_dtype));
-            d.out_batch = vocab;
+            const bool parts = p.dw.splits > 1;
+            d.out = parts ? ws + p.part : const_cast<void *>(at_entry(dw, v0 * cols, grad_dtype));
+            d.out_batch = parts ? here : vocab;
             d.out_pitch = cols;
-            d.out_bf16 = !grad32;
-            d.add = accumulate != 0;
-            loss_set_tiles(d, loss_tiles(g32 ? kWide : kNarrow, here, cols, workers, d.pairs * loss_slices(tokens, g32),
-                                         !g32 ? 1.0 : d.planes == 3 ? 1.65 : 0.75,
-                                         sm::loss_even(d) && (grad32 || !few), 1));
+            d.out_bf16 = !parts && !grad32;
+            d.add = !parts && accumulate;
+            loss_set_tiles(d, p.dw);
             sm::launch_loss_dw(d, st);
             if (int rc = sm::launch_status()) return rc;
+            if (parts) {
+                // a piece of several workers' dw is in as many places
+                const int32_t places = here < vocab ? workers : 1;
+                sm::LossSums u{};
+                u.total = workers / places * here * cols;
+                u.splits = d.splits;
+                u.prev_bf16 = u.out_bf16 = !grad32;
+                for (int32_t i = 0; i < places; ++i) {
+                    u.out = const_cast<void *>(at_entry(dw, (i * vocab + v0) * cols, grad_dtype));
+                    u.partial = reinterpret_cast<const float *>(ws + p.part) + i * here * cols;
+                    u.prev = accumulate ? u.out : nullptr;
+                    u.pitch = workers * here * cols;
+                    sm::launch_loss_sums(u, st);
+                    if (int rc = sm::launch_status()) return rc;
+                }
+            }
         }
     }
     return SIGNMUON_OK;

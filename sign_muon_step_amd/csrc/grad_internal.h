@@ -233,12 +233,12 @@ struct LossJoin {
 void launch_loss_join(LossJoin f, hipStream_t s);
 
 struct LossSums {
-    const float *partial;  // [splits][total]
-    const float *prev;     // added; null: nothing
+    const float *partial;  // [splits], pitch entries apart
+    const void *prev;      // added; null: nothing
     void *out;
-    int64_t total;
+    int64_t total, pitch;
     int32_t splits;
-    bool out_bf16;
+    bool prev_bf16, out_bf16;
 };
 void launch_loss_sums(const LossSums &f, hipStream_t s);
 

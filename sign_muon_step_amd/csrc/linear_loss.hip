@@ -180,23 +180,27 @@ __global__ __launch_bounds__(1024) void loss_join_kernel(LossJoin f) {
     if (f.loss) f.loss[row] = t >= 0 && t < f.vocab ? (lse2 - f.target[row]) * kLn2 : 0.0f;
 }
 
-// out = the parts' sums, in order, added to what `prev` holds; 4 entries a thread at a
-// time.
+// out = the parts' sum, in order, and what `prev` holds; 4 entries a thread at a time.
 __global__ __launch_bounds__(256) void loss_sums_kernel(LossSums f) {
     for (int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; at < f.total; at += (int64_t)gridDim.x * 1024) {
         const int have = (int)(f.total - at < 4 ? f.total - at : 4);
-        float v[4];
-        load_n<false>(f.prev, at, f.prev ? have : 0, v);
+        float v[4] = {}, prev[4];
+        if (f.prev_bf16)
+            load_n<true>(f.prev, at, f.prev ? have : 0, prev);
+        else
+            load_n<false>(f.prev, at, f.prev ? have : 0, prev);
         for (int s = 0; s < f.splits; s += 8) {  // loads before sums
             float p[8][4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) load_n<false>(f.partial, (s + i < f.splits ? s + i : s) * f.total + at, have, p[i]);
+            for (int i = 0; i < 8; ++i) load_n<false>(f.partial, (s + i < f.splits ? s + i : s) * f.pitch + at, have, p[i]);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (s + i < f.splits)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[j] += p[i][j];
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += prev[j];
         if (f.out_bf16)
             store_n<true>(f.out, at, have, v);
         else

@@ -7,6 +7,11 @@ namespace {
 
 template <int HOW>
 void launch_dw(const LossTile &f, hipStream_t s) {
+    if constexpr (HOW != kAdd)
+        if (f.planes == 1 && !f.out_bf16) {  // parts of tokens
+            f.g32 ? launch_wide<kCols32, 1, true, HOW>(f, s) : launch_tiles<kCols16, kCols16, kValues, true, HOW>(f, s);
+            return;
+        }
     if (!f.g32)
         launch_tiles<kCols16, kCols16, kValues, false, HOW>(f, s);
     else if (f.planes == 3 && f.out_bf16)  // of few tokens: bound by the results

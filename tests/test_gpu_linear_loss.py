@@ -393,6 +393,56 @@ def test_logits_of_long_rows(workers, tokens, vocab, cols, x_dtype, w_dtype, gra
     close(added, want[2] + start.double(), want[3] + U * (want[2].abs() + start.double().abs()), grad_dtype, "dw")
 
 
+@pytest.mark.parametrize("workers,tokens,vocab,cols", [(8, 1000, 65, 44), (1, 5000, 256, 384), (3, 2100, 130, 330)])
+@pytest.mark.parametrize("x_dtype,w_dtype,grad_dtype", [(BF16, BF16, BF16), (BF16, F32, F32), (F32, F32, F32),
+                                                        (F32, BF16, BF16)])
+def test_small_vocabularies(workers, tokens, vocab, cols, x_dtype, w_dtype, grad_dtype):
+    """Few entries of dw, whose sums over many tokens come in parts."""
+    x, w, targets, dloss = inputs(workers, tokens, vocab, cols, x_dtype, w_dtype, 91)
+    lse = torch.logsumexp(logits_in_64(x, w, 1.0)[0], 1).float().view(workers, tokens)
+    dx, dw = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype)
+    want = gradients_in_64(x, w, targets, 1.0, lse, dloss, grad_dtype)
+    close(dx, want[0], want[1], x_dtype, "dx")
+    close(dw, want[2], want[3], grad_dtype, "dw")
+    again = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype)
+    assert same_bits(again[0], dx) and same_bits(again[1], dw)
+    start = torch.randn(dw.shape, generator=gen(3)).to(grad_dtype).to(DEV)
+    _, added = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype, start=start)
+    close(added, want[2] + start.double(), want[3] + U * (want[2].abs() + start.double().abs()), grad_dtype, "dw")
+    if grad_dtype == F32:  # one rounding
+        assert same_bits(added, dw + start)
+
+
+@pytest.mark.parametrize("x_dtype,w_dtype,grad_dtype,vocab", [(BF16, BF16, F32, 4500), (F32, BF16, BF16, 4500),
+                                                              (BF16, F32, BF16, 9000)])
+def test_pieces_of_many_tokens(x_dtype, w_dtype, grad_dtype, vocab):
+    """g of two pieces of the vocabulary, of two workers."""
+    x, w, targets, dloss = inputs(2, 32768, vocab, 24, x_dtype, w_dtype, 92)
+    _, lse = run_forward(x, w, targets, 1.0)
+    dx, dw = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype)
+    want = gradients_in_64(x, w, targets, 1.0, lse, dloss, grad_dtype)
+    close(dx, want[0], want[1], x_dtype, "dx")
+    close(dw, want[2], want[3], grad_dtype, "dw")
+    start = torch.randn(dw.shape, generator=gen(3)).to(grad_dtype).to(DEV)
+    _, added = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype, start=start)
+    close(added, want[2] + start.double(), want[3] + U * (want[2].abs() + start.double().abs()), grad_dtype, "dw")
+
+
+@pytest.mark.parametrize("tokens,vocab,cols", [(1500, 6000, 1304), (2048, 4000, 2048), (300, 130, 264), (7000, 300, 48)])
+@pytest.mark.parametrize("x_dtype,grad_dtype", [(BF16, F32), (F32, BF16), (BF16, BF16), (F32, F32)])
+def test_one_gradient_alone(tokens, vocab, cols, x_dtype, grad_dtype):
+    """At sizes of each tile. Where x and dw are of one type, what is asked for changes no bits of it."""
+    x, w, targets, dloss = inputs(1, tokens, vocab, cols, x_dtype, BF16, 93)
+    _, lse = run_forward(x, w, targets, 1.0)
+    dx = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype, want=(True, False))[0]
+    dw = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype, want=(False, True))[1]
+    want = gradients_in_64(x, w, targets, 1.0, lse, dloss, grad_dtype)
+    close(dx, want[0], want[1], x_dtype, "dx")
+    close(dw, want[2], want[3], grad_dtype, "dw")
+    both = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype)
+    assert same_bits(both[1], dw) and (x_dtype != grad_dtype or same_bits(both[0], dx))
+
+
 def test_long_rows_of_padding_and_masked_vocabulary():
     """In parts of k too: tokens without a target hold anything, and a vocabulary entry of minus infinity in
     BF16 counts as nothing."""
