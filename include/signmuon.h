@@ -539,8 +539,8 @@ size_t signmuon_linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t voc
  * signmuon_matrix.grad. accumulate = 1 adds to what dw holds (the gradient of an
  * embedding that shares the table, as signmuon_embedding_backward adds to this
  * one's). Either of dx and dw may be NULL (not wanted), not both. An F32 result is
- * summed with fp32's accuracy; for a BF16 one, g is rounded to BF16 first. What is
- * below 2^-126 of the factors counts as 0. workspace:
+ * summed with fp32's accuracy; for a BF16 one of more than 128 tokens (of all
+ * workers), g is rounded to BF16 first. What is below 2^-126 of the factors counts as 0. workspace:
  * signmuon_linear_cross_entropy_backward_workspace_bytes(workers, tokens, vocab, cols,
  * x_dtype, w_dtype, grad_dtype) bytes, which does not grow with tokens * vocab past
  * a piece of 1 GB.

@@ -9,7 +9,10 @@
 // All passes are bound by memory. A row is read once and held in registers by a
 // team of lanes, as layer norm's. A block of 128 values that shares a scale of
 // the 8-bit output lies in 16 neighbouring lanes: its largest size is four
-// exchanges away, and the output costs no pass of its own.
+// exchanges away, and the output costs no pass of its own. Measured: 8192 x 768 of
+// BF16 with residual to 8 bits 10.5 us a call (44 MB, 4.2 TB/s; one round of rows, so
+// latency shows), the gradients of 8 x 1024 x 768 13.5 (50 MB in two launches), one token 10
+// (the kernel takes 3.3, the rest is issuing the call).
 #include "grad_internal.h"
 
 namespace sm {
