@@ -150,11 +150,36 @@ __global__ __launch_bounds__(THREADS) void clip_finish_kernel(ClipFinish f) {
     f.factors[blockIdx.x] = factor_of(f.most, norm);
 }
 
+// v times the factor, for a store in the type that is to be the product's one rounding.
+// A BF16 value's product has up to 32 bits. Rounded to fp32 and then to 8 bits it comes out as
+// if rounded once, unless fp32's value is the middle of two BF16 ones and the product is not
+// (one in 2^17): such a value takes one step of fp32 towards the product, which fp64 holds.
+// (51 tensors of BF16: 67.5 us so, 68.7 with every product made in fp64 and cut.)
+template <bool BF16>
+__device__ __forceinline__ void scale8(float (&v)[8], float factor) {
+    float out[8];
+    bool middle = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        out[j] = v[j] * factor;
+        middle |= BF16 && (__float_as_uint(out[j]) & 0xffffu) == 0x8000u;
+    }
+    if (middle)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t bits = __float_as_uint(out[j]);
+            const double left = (double)v[j] * (double)factor - (double)out[j];
+            if ((bits & 0xffffu) == 0x8000u && left != 0.0)
+                out[j] = __uint_as_float((left < 0.0) == (out[j] < 0.0) ? bits + 1 : bits - 1);
+        }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = out[j];
+}
+
 template <bool BF16, int UNIT>
 __device__ __forceinline__ void scale_unit(const void *grad, void *out, int64_t base, const Unit &u, float factor) {
     each<BF16, UNIT>(grad, base, u, [&](int64_t at, int have, float(&v)[8]) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= factor;
+        scale8<BF16>(v, factor);
         store_n<BF16>(out, base + at, have, v);
     });
 }

@@ -122,6 +122,29 @@ def test_sizes_that_squares_in_fp32_do_not_hold():
     assert same_bits(outs[0].cpu()[2:], grads[0][2:])
 
 
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("kept", [129, 130, 180, 201, 254, 255])
+@pytest.mark.parametrize("value", [131, 171, 177, 213, 255])
+def test_products_are_rounded_once(value, kept, sign):
+    """Products a little beside the middle of two BF16 values, by less than a step of fp32: rounded to fp32 first they
+    would be in the middle. The norm is a power of 2, so that the factor is max_norm's bits."""
+    middle = kept * 2 ** 24 + 2 ** 23
+    factor = round(middle / value)
+    assert 2 ** 23 <= factor < 2 ** 25 and abs(factor * value - middle) <= value // 2 < 2 ** 7
+    factor -= factor % 2 if factor >= 2 ** 24 else 0
+    grads = torch.zeros(3, 17)
+    grads[:, 3], grads[0, 0], grads[1, 16], grads[2, 8] = 2.0 ** 40, sign * value, sign * value, sign * value
+    most = factor * 2.0 ** 10
+    norms, (out,) = clip([grads.bfloat16()], most)
+    assert norms.tolist() == [2.0 ** 40] * 3
+    # the exact product is a whole number of 2^-30, of 32 bits: to 8 bits, halves to even
+    product, drop = factor * value, (factor * value).bit_length() - 8
+    low, high = product >> drop, product & (2 ** drop - 1)
+    low += high > 2 ** (drop - 1) or (high == 2 ** (drop - 1) and low % 2)
+    want = sign * low * 2.0 ** (drop - 30)
+    assert [float(out[0, 0]), float(out[1, 16]), float(out[2, 8])] == [want] * 3
+
+
 def test_a_worker_that_fails_touches_no_other():
     grads = gradients(5, [1000, 70000], (torch.float32,), 8)
     grads[0][1, 3], grads[1][3, 69999] = float("nan"), float("inf")
