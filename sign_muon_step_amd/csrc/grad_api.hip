@@ -792,6 +792,9 @@ int signmuon_linear_cross_entropy(const void *x, signmuon_dtype x_dtype, const v
         f.batch = 1;
         loss_pairs(f, nx, nw);
         loss_set_tiles(f, p.logits);
+        f.plain_a = nx > 1 ? x : nullptr;
+        f.plain_b = rows;
+        f.plain_b16 = w_dtype == SIGNMUON_BF16;
         f.rows[0] = targets;
         f.row_step = target_type == SIGNMUON_I64 ? 8 : 4;
         f.partial = reinterpret_cast<float2 *>(ws + p.partial);
@@ -886,6 +889,9 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
         loss_set_tiles(f, p.logits);
         for (int i = 0; i < 3; ++i) f.rows[i] = ws + p.row[i];
         f.row_step = 4;
+        f.plain_a = nx > 1 ? x : nullptr;
+        f.plain_b = w_rows;
+        f.plain_b16 = w_dtype == SIGNMUON_BF16;
         f.g = g;
         f.g32 = g32;
         f.g_pitch = g_pitch;

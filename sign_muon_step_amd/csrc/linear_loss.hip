@@ -106,6 +106,10 @@ __global__ __launch_bounds__(256) void loss_parts_kernel(LossTile f) {
                 for (int j = 0; j < 8; ++j)
                     if (s + j < f.splits) l += q[j];
             }
+            if (f.plain_a)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < have && l[j] != l[j]) l[j] = plain_logit(f, row, col + j);
         }
         const int32_t t = *reinterpret_cast<const int32_t *>(static_cast<const char *>(f.rows[0]) + row * f.row_step);
         const uint32_t at = (uint32_t)t - (uint32_t)(f.vocab0 + col);  // the target's place among the four
@@ -230,7 +234,9 @@ void launch_loss_logits(const LossTile &f, bool grad, hipStream_t s) {
     if (f.splits > 1)
         launch_tiles<kRows16, kRows16, kValues, true>(f, s);
     else if (!grad)
-        launch_tiles<kRows16, kRows16, kLse, true>(f, s);
+        f.plain_a ? launch_tiles<kRows16, kRows16, kPlanesLse, true>(f, s) : launch_tiles<kRows16, kRows16, kLse, true>(f, s);
+    else if (f.plain_a)  // g is fp32 wherever x is
+        launch_tiles<kRows16, kRows16, kPlanesGrad, true>(f, s);
     else
         f.g32 ? launch_tiles<kRows16, kRows16, kGrad, true>(f, s) : launch_tiles<kRows16, kRows16, kGrad, false>(f, s);
 }

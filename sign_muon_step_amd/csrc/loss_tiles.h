@@ -353,9 +353,31 @@ __device__ __forceinline__ void write(Acc<FM, FN> &acc, char *mine, void *out, i
         }
 }
 
+// A logit (over its scale) whose products of planes add up to no number, from the operands
+// themselves. The planes of x behind the first are nought or of either sign, and an infinity of w, or a
+// first plane's product past fp32's range, meets each of them: a vocabulary entry that the weight
+// sends to minus infinity would be no number, where the sum of the operands' own products is
+// minus infinity.
+__device__ __forceinline__ float plain_logit(const LossTile &f, int64_t row, int64_t col) {
+    double sum = 0.0;
+#pragma unroll 1
+    for (int64_t k = 0; k < f.k && sum == sum; k += 8) {
+        const int have = left((int)f.k, (int)k);
+        float a[8], b[8];
+        load_n<false>(f.plain_a, row * f.k + k, have, a);
+        if (f.plain_b16)
+            load_n<true>(f.plain_b, col * f.k + k, have, b);
+        else
+            load_n<false>(f.plain_b, col * f.k + k, have, b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fma((double)a[j], (double)b[j], sum);
+    }
+    return (float)sum;
+}
+
 // A row's maximum and sum of exponentials over the wave's columns, and the target's
-// logit, in units of log 2.
-template <int FM, int FN>
+// logit, in units of log 2. PLANES: x is in several.
+template <int FM, int FN, bool PLANES>
 __device__ __forceinline__ void finish_lse(const LossTile &f, Acc<FM, FN> &acc, const char *targets, int64_t row0,
                                            int64_t col0, int lane) {
     constexpr int kRows = FM * 32, kCols = FN * 32;
@@ -402,6 +424,36 @@ __device__ __forceinline__ void finish_lse(const LossTile &f, Acc<FM, FN> &acc, 
 #pragma unroll
             for (int e = 0; e < 16; ++e) sum[e & 1] += __builtin_amdgcn_exp2f(l[n][e] - base);
         sum[0] += sum[1];
+        if constexpr (PLANES)
+            if (__any(sum[0] != sum[0])) {  // as it stays where the operands hold NaN, or the logit is infinite
+                uint64_t bad = 0;
+                sum[0] = 0.0f;
+                int lane1 = lane;  // made anew here, as what follows from it
+                asm volatile("" : "+v"(lane1));
+#pragma unroll
+                for (int n = 0; n < FN; ++n) {
+                    pin(acc[i][n]);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float v = column(n, e, lane1) < have ? acc[i][n][e] * f.factor : -INFINITY;
+                        bad |= v != v && row < rows ? 1ull << (n * 16 + e) : 0ull;
+                        sum[0] += v != v ? 0.0f : __builtin_amdgcn_exp2f(v - base);
+                    }
+                }
+#pragma unroll 1
+                for (; bad; bad &= bad - 1) {
+                    const int at = __builtin_ctzll(bad), col = column(at / 16, at % 16, lane1);
+                    const float v = plain_logit(f, row0 + row, col0 + col) * f.factor, most = fmaxf(top, v);
+                    if (col == target) f.target[row0 + row] = v;
+                    if (v == -INFINITY) continue;
+                    sum[0] = (sum[0] == 0.0f ? 0.0f : sum[0] * __builtin_amdgcn_exp2f(top - most)) +
+                             __builtin_amdgcn_exp2f(v - most);
+                    top = most;
+                }
+                const float other = __shfl_xor(top, 32), most = fmaxf(top, other);
+                sum[0] = sum[0] == 0.0f ? 0.0f : sum[0] * __builtin_amdgcn_exp2f(top - most);
+                top = most;
+            }
         sum[0] += __shfl_xor(sum[0], 32);
         __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(top), __float_as_uint(sum[0])}, partial,
                                               lane < 32 ? row * 8 : (int)kOutside, 0, 0);
@@ -410,8 +462,8 @@ __device__ __forceinline__ void finish_lse(const LossTile &f, Acc<FM, FN> &acc, 
     clear<FM, FN>(acc);
 }
 
-// g; zeros in the columns past the vocabulary that a tile has.
-template <int FM, int FN, bool WIDE>
+// g; zeros in the columns past the vocabulary that a tile has. PLANES: x is in several.
+template <int FM, int FN, bool WIDE, bool PLANES>
 __device__ __forceinline__ void finish_grad(const LossTile &f, Acc<FM, FN> &acc, char *mine, const char *data, int64_t row0,
                                             int64_t col0, int lane) {
     constexpr int kRows = FM * 32, kCols = FN * 32;
@@ -440,10 +492,18 @@ __device__ __forceinline__ void finish_grad(const LossTile &f, Acc<FM, FN> &acc,
     auto exponential = [&](int i, int n, int e) {
         return __builtin_amdgcn_exp2f(fmaf(acc[i][n][e], f.factor, -base[i]));
     };
+    float check = 0.0f;  // no number if one of the values is none, or infinite
+    [[maybe_unused]] auto watch = [&](float v) {
+        check = fmaf(v, 0.0f, check);
+        asm volatile("" : "+v"(check));  // here, while v is in a register
+    };
     if (__all(whole && !any))
         put([&](int i, int n, int q, float(&v)[4]) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = d[i] * exponential(i, n, q * 4 + j);
+            for (int j = 0; j < 4; ++j) {
+                v[j] = d[i] * exponential(i, n, q * 4 + j);
+                if constexpr (PLANES) watch(v[j]);
+            }
         });
     else
         put([&](int i, int n, int q, float(&v)[4]) {
@@ -452,8 +512,26 @@ __device__ __forceinline__ void finish_grad(const LossTile &f, Acc<FM, FN> &acc,
                 const int c = column(n, q * 4 + j, lane);
                 const float p = exponential(i, n, q * 4 + j);
                 v[j] = c < limit[i] ? d[i] * (c == target[i] ? p - 1.0f : p) : 0.0f;
+                if constexpr (PLANES) watch(v[j]);
             }
         });
+    if constexpr (PLANES)
+        if (__any(check != check)) {
+            wait_loads<0>();  // the wave reads what it wrote
+            const int rows = (int)(f.m - row0 < kRows ? f.m - row0 : kRows);
+#pragma unroll 1
+            for (int at = lane; at < rows * kCols; at += kWave) {
+                const int row = at / kCols, col = at % kCols;
+                const int t = *reinterpret_cast<const int *>(data + row * 4);
+                const int64_t entry = (row0 + row) * f.g_pitch + col0 + col;
+                float v = load1<!WIDE>(f.g, entry);
+                if (v == v || t < 0 || col >= have) continue;
+                v = __builtin_amdgcn_exp2f(fmaf(plain_logit(f, row0 + row, col0 + col), f.factor,
+                                                -*reinterpret_cast<const float *>(data + (row + 2 * kRows) * 4)));
+                if (t - f.vocab0 - col0 == col) v -= 1.0f;
+                store1<!WIDE>(f.g, entry, v * *reinterpret_cast<const float *>(data + (row + 4 * kRows) * 4));
+            }
+        }
     clear<FM, FN>(acc);
 }
 
@@ -494,7 +572,7 @@ __device__ __forceinline__ uint32_t stage_of(uint32_t lds, unsigned c, int wave)
     return to;
 }
 
-enum { kLse, kGrad, kValues };
+enum { kLse, kGrad, kValues, kPlanesLse, kPlanesGrad };  // kPlanes..: of an x in several planes
 
 // Products of BF16 operands. A workgroup takes every gridDim-th tile; four waves of
 // half a tile each way. The loads run two slices ahead of the products, on into the
@@ -502,12 +580,13 @@ enum { kLse, kGrad, kValues };
 // WIDE: results in fp32. HOW: of values.
 template <int KA, int KB, int TM, int TN, int END, bool WIDE, int HOW>
 __global__ __launch_bounds__(kWaves *kWave, TM *TN > 128 * 128 ? 1 : 2) void loss_tile_kernel(LossTile f, int total) {
-    constexpr int kRowArrays = END == kLse ? 1 : END == kGrad ? 3 : 0;
+    constexpr bool kIsLse = END == kLse || END == kPlanesLse, kIsGrad = END == kGrad || END == kPlanesGrad;
+    constexpr int kRowArrays = kIsLse ? 1 : kIsGrad ? 3 : 0;
     using L = Loader<KA, KB, TM, TN, kLossSlice, 2, kRowArrays>;
     using A = typename L::A;
     using B = typename L::B;
     constexpr int FM = TM / 64, FN = TN / 64;
-    constexpr int kOut = L::kBytes, kOutWave = END == kLse ? 0 : out_lds(FN * 32);
+    constexpr int kOut = L::kBytes, kOutWave = kIsLse ? 0 : out_lds(FN * 32);
     __shared__ __attribute__((aligned(1024))) char lds[kOut + kWaves * kOutWave];
     const int lane = threadIdx.x & (kWave - 1), wave = first_lane(threadIdx.x / kWave);
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char *)lds);
@@ -569,7 +648,7 @@ __global__ __launch_bounds__(kWaves *kWave, TM *TN > 128 * 128 ? 1 : 2) void los
     };
     // A tile's results are on their way to memory during the next one's first slice:
     // there, only what is older than their stores is waited for.
-    constexpr int kStores = END == kLse ? FM : out_stores(FM * FN, WIDE, HOW), kBehind = kStores < 63 ? kStores : 63;
+    constexpr int kStores = kIsLse ? FM : out_stores(FM * FN, WIDE, HOW), kBehind = kStores < 63 ? kStores : 63;
     bool behind = false;  // of buffer stores, whose number is known
     const int per = loader.per;
     unsigned c = 0;  // slices so far
@@ -605,10 +684,10 @@ __global__ __launch_bounds__(kWaves *kWave, TM *TN > 128 * 128 ? 1 : 2) void los
         for (; j < end; ++j) slice(kLow);
         char *mine = lds + kOut + wave * kOutWave;
         const char *data = lds + L::kRowData + tile % L::kRowSets * L::kRowSet + wm * 4;
-        if constexpr (END == kLse)
-            finish_lse<FM, FN>(f, acc, data, t.row0 + wm, t.col0 + wn, lane);
-        else if constexpr (END == kGrad)
-            finish_grad<FM, FN, WIDE>(f, acc, mine, data, t.row0 + wm, t.col0 + wn, lane);
+        if constexpr (kIsLse)
+            finish_lse<FM, FN, END == kPlanesLse>(f, acc, data, t.row0 + wm, t.col0 + wn, lane);
+        else if constexpr (kIsGrad)
+            finish_grad<FM, FN, WIDE, END == kPlanesGrad>(f, acc, mine, data, t.row0 + wm, t.col0 + wn, lane);
         else
             finish_values<FM, FN, WIDE, FN * 32, HOW>(f, acc, mine, t, t.row0 + wm, t.col0 + wn, lane);
         behind = HOW != kUneven;

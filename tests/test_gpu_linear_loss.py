@@ -290,6 +290,45 @@ def test_masked_vocabulary():
         assert bool(((a - b).abs() <= 16 * U * (1 + b.abs())).all())
 
 
+@pytest.mark.parametrize("workers,tokens,vocab,cols", [(2, 50, 520, 64), (3, 100, 1000, 515), (2, 40, 300, 6144),
+                                                       (1, 2100, 9000, 264)])
+@pytest.mark.parametrize("x_dtype", [F32, BF16])
+@pytest.mark.parametrize("w_dtype", [F32, BF16])
+def test_masked_vocabulary_of_every_type(workers, tokens, vocab, cols, x_dtype, w_dtype):
+    """A logit of minus infinity counts as nothing whatever the operands' types, whether an entry of the weight is
+    infinite or a product passes fp32's range; and a token that holds an infinity is no number, but no other is."""
+    x, w, targets, dloss = inputs(workers, tokens, vocab, cols, x_dtype, w_dtype, 36)
+    x[..., 0] = x[..., 0].abs() + 0.25
+    x[:, ::3, 0], x[..., 1] = 1.0, 1.1e30
+    w[:, :2] = 0.0
+    kind = torch.arange(vocab, device=DEV) % 5
+    keep = kind < 3
+    w[kind == 3] = 0.0
+    w[kind == 3, 0] = -math.inf
+    w[kind == 4, 1] = -1.3e30
+    inside = (targets >= 0) & (targets < vocab)
+    targets = torch.where(inside, targets // 5 * 5, targets)
+    loss, lse = run_forward(x, w, targets, 1.0)
+    rest = torch.where(inside, targets // 5 * 3, targets)  # among the entries that count
+    rest[rest >= vocab] = -1
+    kept = w[keep].contiguous()
+    want = losses_in_64(*logits_in_64(x, kept, 1.0), rest, int(keep.sum()))
+    close(lse.flatten(), want[0], want[1], F32, "lse")
+    close(loss.flatten(), want[2], want[3], F32, "loss")
+    for grad_dtype in (F32, BF16):
+        dx, dw = run_backward(x, w, targets, 1.0, lse, dloss, grad_dtype)
+        want = gradients_in_64(x, kept, rest, 1.0, lse, dloss, grad_dtype)
+        # nought times infinity in the column that holds them
+        close(dx[..., 1:], want[0][..., 1:], want[1][..., 1:], x_dtype, "dx")
+        assert bool((dw[:, ~keep] == 0).all())
+        close(dw[:, keep], want[2], want[3], grad_dtype, "dw")
+    x[0, 7] = math.inf
+    _, again = run_forward(x, w, targets, 1.0)
+    others = torch.ones(workers, tokens, dtype=torch.bool, device=DEV)
+    others[0, 7] = False
+    assert same_bits(again[others], lse[others]) and bool(again[~others].isnan().all())
+
+
 def test_backward_is_the_forwards_by_differences():
     """Central differences of a weighted sum of the losses along one direction of x and w, in 64 bits, against
     the kernel's gradients."""
