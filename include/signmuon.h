@@ -516,7 +516,10 @@ size_t signmuon_rms_norm_workspace_bytes(int32_t workers, int64_t rows, int64_t 
  * of plus infinity or NaN makes its token's loss and lse NaN, and no other's. tokens
  * is the count over all workers. workspace:
  * signmuon_linear_cross_entropy_workspace_bytes(tokens, vocab, cols, x_dtype, w_dtype)
- * bytes.
+ * bytes: a copy of x where its rows are not of whole BF16 vectors (2 bytes an entry, 6
+ * of F32), the same of w, 128 MB or 256 of its rows at a time, the maxima and sums of
+ * pieces of the vocabulary (256 MB at most, or 32 bytes a token), and, where few logits
+ * have long rows, their sums in parts of cols (512 MB at most).
  */
 int signmuon_linear_cross_entropy(const void *x, signmuon_dtype x_dtype, const void *w, signmuon_dtype w_dtype,
                                   const void *targets, signmuon_itype target_type, int64_t tokens,

@@ -177,6 +177,10 @@ constexpr float kLog2E = 1.44269504088896340736f;
 // What a piece of the vocabulary may take of the workspace where more than one
 // tile's columns do: its maxima and sums, or its g, and the planes of its weights.
 constexpr int64_t kLossForward = (int64_t)128 << 20, kLossBackward = (int64_t)1 << 30;
+// What parts of k may take, forward; backward (of logits and of each gradient) kLossBackward.
+// 14467 x 2202 x 8104 in fp32, 513 tiles for 256 places, takes 3.80 ms in five parts of 127 MB,
+// 3.69 in the four that this holds and 5.85 in one; 15892 x 5428 x 3544 3.80 in two of 345 and 3.93 in one.
+constexpr int64_t kLossForwardParts = (int64_t)512 << 20;
 
 inline int loss_planes(int dtype) { return dtype == SIGNMUON_F32 ? 3 : 1; }
 // Pairs of planes of a product of two operands (loss_pairs).
@@ -270,6 +274,11 @@ struct LossPlan {
 };
 
 constexpr int kLossParts = 32;  // of k, at most
+// Parts of k of rows x cols fp32 values that `budget` bytes hold.
+inline int loss_most_parts(int64_t budget, int64_t rows, int64_t cols) {
+    const int64_t most = budget / (rows * cols * (int64_t)sizeof(float));
+    return most < 1 ? 1 : most < kLossParts ? (int)most : kLossParts;
+}
 inline int64_t loss_part_pitch(int64_t n) { return (n + 3) / 4 * 4; }
 // Bytes of the logits' parts of k.
 int64_t loss_logit_parts(const LossPlan &p, int64_t rows, int64_t vocab) {
@@ -295,8 +304,9 @@ LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int
     const int64_t w_row = loss_direct(w_dtype, cols) ? 0 : loss_planes(w_dtype) * p.pitch * 2;
     if (w_row && kLossForward / w_row < most) most = kLossForward / w_row;
     p.piece = loss_piece(vocab, most);
-    p.logits = loss_tiles(kLogits, tokens, vocab < p.piece ? vocab : p.piece, 1,
-                          loss_products(x_dtype, w_dtype) * loss_slices(cols, false), 1.0, true, kLossParts);
+    const int64_t here = vocab < p.piece ? vocab : p.piece;
+    p.logits = loss_tiles(kLogits, tokens, here, 1, loss_products(x_dtype, w_dtype) * loss_slices(cols, false), 1.0, true,
+                          loss_most_parts(kLossForwardParts, tokens, loss_part_pitch(here)));
     size_t at = 0;
     auto section = [&](int64_t bytes) {
         const size_t here = at;
@@ -330,9 +340,10 @@ LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t 
     const int64_t here = vocab < p.piece ? vocab : p.piece;
     const bool summed = p.piece < vocab || (few && !x32);  // that product has fp32 results
     p.logits = loss_tiles(kLogits, rows, here, 1, loss_products(x_dtype, w_dtype) * loss_slices(cols, false), 1.0, true,
-                          kLossParts);
+                          loss_most_parts(kLossBackward, rows, loss_part_pitch(here)));
     p.dx = loss_tiles(g32 ? kWide : kNarrow, rows, cols, 1, loss_meet(loss_planes(w_dtype), x32) * loss_slices(here, g32),
-                      !g32 ? 1.0 : x32 || few ? 1.65 : 0.75, cols % (x32 ? 4 : 8) == 0, kLossParts, summed);
+                      !g32 ? 1.0 : x32 || few ? 1.65 : 0.75, cols % (x32 ? 4 : 8) == 0,
+                      loss_most_parts(kLossBackward, rows, cols), summed);
     p.parts = summed || p.dx.splits > 1;
     // Parts of the tokens only where half of the compute units' places would be empty: 225 x 44 of
     // eight workers takes 24 us in parts and 196 without, 5003 x 515 of three 110 and 89.
@@ -340,7 +351,7 @@ LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t 
     const int64_t dw_tiles = workers * ((here + 127) / 128) * ((cols + 127) / 128);
     p.dw = loss_tiles(g32 ? kWide : kNarrow, here, cols, workers,
                       loss_meet(loss_planes(x_dtype), grad32) * loss_slices(tokens, g32), !g32 ? 1.0 : whole ? 1.65 : 0.75,
-                      cols % (grad32 ? 4 : 8) == 0 && (grad32 || !few), dw_tiles <= 256 ? kLossParts : 1);
+                      cols % (grad32 ? 4 : 8) == 0 && (grad32 || !few), dw_tiles <= 256 ? loss_most_parts(kLossBackward, workers * here, cols) : 1);
     size_t at = 0;
     auto section = [&](int64_t bytes) {
         const size_t here = at;

@@ -4,9 +4,10 @@
 //   l[t][v] = scale x[t].w[v],  lse[t] = log sum_v exp l[t][v],  loss[t] = lse[t] - l[t][target]
 //   g[t][v] = scale dloss[t] (exp(l[t][v] - lse[t]) - [v = target]),  dx = g w,  dw_m = g_m^T x_m
 //
-// No logit leaves the chip. Forward, each tile of logits becomes one running
+// The logits are not kept. Forward, each tile of them becomes one running
 // maximum and one sum of exponentials a row and half a tile's columns, which are
-// joined afterwards. Backward, the logits of a piece of the vocabulary are computed
+// joined afterwards (where they have few tiles and long rows, the tiles' sums over parts of
+// k go through memory, up to 512 MB of them). Backward, the logits of a piece of the vocabulary are computed
 // again and stored as g, from which that piece's dw and its share of dx are two
 // more products; then the next piece overwrites it.
 //

@@ -2,6 +2,9 @@
 refused before any launch (fake, never dereferenced device addresses), and the
 binding refuses tensors of another type, shape, layout or device (no GPU
 needed)."""
+import math
+import random
+
 import pytest
 import torch
 
@@ -214,6 +217,28 @@ def test_linear_cross_entropy_backward_arguments(lib):
                                    (dict(workspace_bytes=need - 1), EWORKSPACE)]:
         assert calls_with(lib.signmuon_linear_cross_entropy_backward, names, good, **change) == status, change
     assert size(0, 10, 10, 10, 0, 0, 0) == size(1, 10, 10, 10, 0, 0, 3) == size(1, 10, 10, 10, 0, 5, 0) == 0
+
+
+LOSS_SIZES = [(15892, 5428, 3544), (14467, 2202, 8104), (7910, 23213, 7534), (1, 1 << 20, 2047), (1 << 25, 1, 1),
+              (1 << 23, 100, 64), (1 << 25, 65536, 64), (300, 3000, 1 << 19), (8192, 50257, 768), (65536, 32000, 4096)]
+
+
+def _loss_sizes():
+    rng = random.Random(5)
+    some = [tuple(int(math.exp(rng.uniform(0, math.log(most)))) for most in (1 << 20, 1 << 17, 1 << 14)) for _ in range(20000)]
+    return LOSS_SIZES + [(t, v, c) for t, v, c in some if v * c < 1 << 31]
+
+
+def test_linear_cross_entropy_workspace_holds_no_logits(lib):
+    """As the header bounds it: besides the operands' planes, what grows with tokens * vocab is held to a budget."""
+    size = lib.signmuon_linear_cross_entropy_workspace_bytes
+    for i, (t, v, c) in enumerate(_loss_sizes()):
+        pitch, mb = (c + 7) // 8 * 8, 1 << 20
+        for x, w in [(0, 0), (1, 1), (1, 0), (0, 1)][:4 if i < 2000 else 1]:
+            planes = 0 if x and c % 8 == 0 else (2 if x else 6) * t * pitch
+            weights = 0 if w and c % 8 == 0 else max(128 * mb, 256 * (2 if w else 6) * pitch)
+            most = planes + weights + max(256 * mb, 32 * t) + 512 * mb + 12 * t + 8 * 256
+            assert 0 < size(t, v, c, x, w) <= most, (t, v, c, x, w)
 
 
 def test_linear_cross_entropy_binding_refuses_other_tensors():
