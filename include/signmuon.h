@@ -544,11 +544,16 @@ size_t signmuon_linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t voc
  * signmuon_matrix.grad. accumulate = 1 adds to what dw holds (the gradient of an
  * embedding that shares the table, as signmuon_embedding_backward adds to this
  * one's). Either of dx and dw may be NULL (not wanted), not both. An F32 result is
- * summed with fp32's accuracy; for a BF16 one of more than 128 tokens (of all
- * workers), g is rounded to BF16 first. What is below 2^-126 of the factors counts as 0. workspace:
+ * summed with fp32's accuracy. For a BF16 one, an F32 w or x that meets g is rounded to
+ * 16 bits, and with more than 128 tokens (of all workers together, for each worker's dw
+ * too) g to BF16. What is below 2^-126 of the factors counts as 0. workspace:
  * signmuon_linear_cross_entropy_backward_workspace_bytes(workers, tokens, vocab, cols,
- * x_dtype, w_dtype, grad_dtype) bytes, which does not grow with tokens * vocab past
- * a piece of 1 GB.
+ * x_dtype, w_dtype, grad_dtype) bytes: a copy of x (2 bytes an entry, 6 of F32); one of
+ * w where its rows are not of whole BF16 vectors, 1 GB or 256 of its rows at a time; g
+ * for a piece of the vocabulary, of 1 GB at most, or of 256 entries where these take
+ * more (past 2^20 tokens: 1 KB a token, 512 bytes with BF16 x and dw); parts of sums, of
+ * 1 GB at most or 4 bytes an entry of dx; and 4 bytes an entry of a BF16 dx that is summed
+ * over several pieces.
  */
 int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype, const void *w,
                                            signmuon_dtype w_dtype, const void *targets,

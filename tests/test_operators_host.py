@@ -241,6 +241,22 @@ def test_linear_cross_entropy_workspace_holds_no_logits(lib):
             assert 0 < size(t, v, c, x, w) <= most, (t, v, c, x, w)
 
 
+def test_linear_cross_entropy_backward_workspace_holds_no_logits(lib):
+    """g is held to pieces of 1 GB, or to 256 columns of all tokens."""
+    size = lib.signmuon_linear_cross_entropy_backward_workspace_bytes
+    for i, (t, v, c) in enumerate(_loss_sizes()):
+        pitch, gb = (c + 7) // 8 * 8, 1 << 30
+        for x, w, grad in [(0, 0, 0), (1, 1, 0), (1, 1, 1), (1, 0, 0), (0, 1, 1)][:5 if i < 2000 else 1]:
+            planes = (2 if x else 6) * t * pitch
+            weights = 0 if w and c % 8 == 0 else max(gb, 256 * (2 if w else 6) * pitch)
+            few = t <= 128
+            g = max(gb, 256 * t * (2 if x and grad and not few else 4))
+            sums = 4 * t * c if x else 0
+            most = planes + weights + g + sums + max(gb, 4 * t * c) + 12 * t + 12 * 256
+            for workers in {1, 8 if t % 8 == 0 else 1}:
+                assert 0 < size(workers, t // workers, v, c, x, w, grad) <= most, (workers, t, v, c, x, w, grad)
+
+
 def test_linear_cross_entropy_binding_refuses_other_tensors():
     x, w, ids = torch.zeros(2, 5, 6), torch.zeros(7, 6), torch.zeros(2, 5, dtype=torch.int64)
     s, ws = torch.zeros(2, 5), torch.zeros(1 << 20, dtype=torch.uint8)
