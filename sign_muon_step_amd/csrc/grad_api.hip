@@ -214,9 +214,8 @@ int64_t loss_piece(int64_t vocab, int64_t most) {
 //   logits and dx 512 x 32000 x 4096                        256 / 310 / 322
 // The compute units are those of a whole MI355X, not asked for, since the workspace's size is
 // told without a device.
-struct LossTiles {
-    int32_t tm, tn, splits;
-};
+using sm::LossPlan;
+using sm::LossTiles;
 enum LossKind { kLogits, kNarrow, kWide };
 
 LossTiles loss_tiles(LossKind kind, int64_t m, int64_t n, int64_t batch, int64_t slices, double slice, bool even,
@@ -265,14 +264,6 @@ inline int64_t loss_slices(int64_t k, bool g32) {
     return (k + slice - 1) / slice;
 }
 
-struct LossPlan {
-    int64_t piece, pitch;
-    LossTiles logits, dx, dw;
-    bool few, g32;
-    bool parts;                   // of dx, summed by a launch of their own
-    size_t x, w, partial, state, target, row[3], g, sum, part, total;
-};
-
 constexpr int kLossParts = 32;  // of k, at most
 // Parts of k of rows x cols fp32 values that `budget` bytes hold.
 inline int loss_most_parts(int64_t budget, int64_t rows, int64_t cols) {
@@ -296,6 +287,10 @@ int loss_logits(sm::LossTile &f, void *parts, bool grad, hipStream_t st) {
     sm::launch_loss_parts(f, grad, st);
     return sm::launch_status();
 }
+
+}  // namespace
+
+namespace sm {
 
 LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int w_dtype) {
     LossPlan p{};
@@ -324,7 +319,7 @@ LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int
 }
 
 LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int w_dtype,
-                        int grad_dtype, bool want_dw = true) {
+                        int grad_dtype, bool want_dw) {
     LossPlan p{};
     const int64_t rows = workers * tokens;
     p.pitch = sm::loss_pitch(cols);
@@ -371,6 +366,10 @@ LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t 
     p.total = at;
     return p;
 }
+
+}  // namespace sm
+
+namespace {
 
 // The pairs of planes i of a and j of b with i + j below the longer one's count. An
 // fp32 a (in one piece) meets each plane of b with as many of its own.
@@ -763,7 +762,7 @@ int signmuon_clip_grads(const signmuon_gradient *grads, int32_t n_grads, int32_t
 size_t signmuon_linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols,
                                                      signmuon_dtype x_dtype, signmuon_dtype w_dtype) {
     if (check_embedding(1, tokens, vocab, cols) != SIGNMUON_OK || !dtype_ok(x_dtype) || !dtype_ok(w_dtype)) return 0;
-    return loss_plan(tokens, vocab, cols, x_dtype, w_dtype).total;
+    return sm::loss_plan(tokens, vocab, cols, x_dtype, w_dtype).total;
 }
 
 int signmuon_linear_cross_entropy(const void *x, signmuon_dtype x_dtype, const void *w, signmuon_dtype w_dtype,
@@ -776,7 +775,7 @@ int signmuon_linear_cross_entropy(const void *x, signmuon_dtype x_dtype, const v
     if ((target_type != SIGNMUON_I32 && target_type != SIGNMUON_I64) || !dtype_ok(x_dtype) || !dtype_ok(w_dtype))
         return SIGNMUON_EDTYPE;
     if (!all_aligned(x, w, targets, loss, lse)) return SIGNMUON_EALIGN;
-    const LossPlan p = loss_plan(tokens, vocab, cols, x_dtype, w_dtype);
+    const LossPlan p = sm::loss_plan(tokens, vocab, cols, x_dtype, w_dtype);
     if (int rc = check_workspace(workspace, workspace_bytes, p.total)) return rc;
     char *ws = static_cast<char *>(workspace);
     const hipStream_t st = static_cast<hipStream_t>(stream);
@@ -839,7 +838,7 @@ size_t signmuon_linear_cross_entropy_backward_workspace_bytes(int32_t workers, i
     if (check_embedding(workers, tokens, vocab, cols) != SIGNMUON_OK || !dtype_ok(x_dtype) || !dtype_ok(w_dtype) ||
         !dtype_ok(grad_dtype))
         return 0;
-    return loss_grad_plan(workers, tokens, vocab, cols, x_dtype, w_dtype, grad_dtype).total;
+    return sm::loss_grad_plan(workers, tokens, vocab, cols, x_dtype, w_dtype, grad_dtype, true).total;
 }
 
 int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype, const void *w,
@@ -856,7 +855,7 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
         !dtype_ok(grad_dtype))
         return SIGNMUON_EDTYPE;
     if (!all_aligned(x, w, targets, lse, dloss, dx, dw)) return SIGNMUON_EALIGN;
-    const LossPlan p = loss_grad_plan(workers, tokens, vocab, cols, x_dtype, w_dtype, grad_dtype, dw != nullptr);
+    const LossPlan p = sm::loss_grad_plan(workers, tokens, vocab, cols, x_dtype, w_dtype, grad_dtype, dw != nullptr);
     if (int rc = check_workspace(workspace, workspace_bytes, p.total)) return rc;
     char *ws = static_cast<char *>(workspace);
     const hipStream_t st = static_cast<hipStream_t>(stream);

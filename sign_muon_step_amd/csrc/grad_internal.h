@@ -184,6 +184,22 @@ struct LossPlanes {
 };
 void launch_loss_planes(const LossPlanes &f, hipStream_t s);
 
+// The tiles of a product, and the parts of k.
+struct LossTiles {
+    int32_t tm, tn, splits;
+};
+// Tiles and workspace of the loss (logits) and of its gradients. The types are signmuon_dtype's.
+struct LossPlan {
+    int64_t piece, pitch;  // entries of the vocabulary at a time; of a plane's row
+    LossTiles logits, dx, dw;
+    bool few, g32;
+    bool parts;            // of dx, summed by a launch of their own
+    size_t x, w, partial, state, target, row[3], g, sum, part, total;
+};
+LossPlan loss_plan(int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int w_dtype);
+LossPlan loss_grad_plan(int64_t workers, int64_t tokens, int64_t vocab, int64_t cols, int x_dtype, int w_dtype,
+                        int grad_dtype, bool want_dw);
+
 // A product a b^T of planes, out [m][n], sums over k and over pairs of planes.
 struct LossTile {
     const void *a[kLossPlanes], *b[kLossPlanes];  // BF16; a[0] fp32 where g32 and a is g

@@ -89,3 +89,30 @@ def embed_segment(workers, tokens, cols):
     fn = sm.library()._ZN2sm13embed_segmentEill
     fn.restype, fn.argtypes = ctypes.c_int32, [ctypes.c_int32, ctypes.c_int64, ctypes.c_int64]
     return fn(workers, tokens, cols)
+
+
+class _LossTiles(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("tm", "tn", "splits")]
+
+
+class _LossPlan(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_int64) for name in ("piece", "pitch")] +
+                [(name, _LossTiles) for name in ("logits", "dx", "dw")] +
+                [(name, ctypes.c_bool) for name in ("few", "g32", "parts")] +
+                [(name, ctypes.c_size_t) for name in ("x", "w", "partial", "state", "target", "row0", "row1", "row2", "g",
+                                                      "sum", "part", "total")])
+
+
+def loss_plan(tokens, vocab, cols, x_dtype, w_dtype):
+    """The library's own plan of an output layer's loss (csrc/grad_internal.h, LossPlan): tiles and parts of k. No GPU
+    needed. The types as the C interface numbers them, here and below."""
+    fn = sm.library()._ZN2sm9loss_planElllii
+    fn.restype, fn.argtypes = _LossPlan, [ctypes.c_int64] * 3 + [ctypes.c_int] * 2
+    return fn(tokens, vocab, cols, x_dtype, w_dtype)
+
+
+def loss_grad_plan(workers, tokens, vocab, cols, x_dtype, w_dtype, grad_dtype):
+    """The same of its gradients."""
+    fn = sm.library()._ZN2sm14loss_grad_planElllliiib
+    fn.restype, fn.argtypes = _LossPlan, [ctypes.c_int64] * 4 + [ctypes.c_int] * 3 + [ctypes.c_bool]
+    return fn(workers, tokens, vocab, cols, x_dtype, w_dtype, grad_dtype, True)
