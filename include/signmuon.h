@@ -589,9 +589,11 @@ typedef struct {
  * signmuon_clip_grads -- the norms as above, and
  *   out = grad * min(1, max_norm / norms[m])
  * for every entry of worker m, with the factor in fp32 and each product rounded
- * once. max_norm is positive and finite. A norm that is NaN makes every entry of
- * its worker NaN; an infinite one makes its finite entries 0 and the others NaN:
- * a worker that fails does not touch another's gradients. Where a worker's norm is
+ * once. max_norm is positive and finite. A NaN among a worker's entries makes all of
+ * them NaN; an infinity makes its finite entries 0 and the infinite ones NaN: a worker
+ * that fails does not touch another's gradients. Finite entries are clipped by the fp64
+ * norm, also where norms[m] cannot hold it and is infinite; a factor below 2^-126 has
+ * fewer bits, and one below 2^-150 is 0. Where a worker's norm is
  * at most max_norm, its gradients keep their bits (in place: they are not
  * touched). An out must not overlap any other buffer of the call than its own
  * grad.

@@ -136,7 +136,7 @@ __device__ __forceinline__ double worker_norm(const double *partial, int64_t uni
     return sqrt(block_sum<THREADS>(total));
 }
 
-// A norm that is not a number makes every entry of the worker one.
+// A norm that is not a number leaves the worker no entry that is one.
 __device__ __forceinline__ float factor_of(float most, double norm) {
     const double factor = (double)most / norm;
     return factor > 1.0 ? 1.0f : (float)factor;

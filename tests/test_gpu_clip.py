@@ -122,6 +122,20 @@ def test_sizes_that_squares_in_fp32_do_not_hold():
     assert same_bits(outs[0].cpu()[2:], grads[0][2:])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_finite_entries_are_clipped_by_a_norm_past_fp32(dtype):
+    grads = [torch.full((2, 5000), 3e38).to(dtype), torch.tensor([[1.0, -2e38], [1.0, 2.0]]).to(dtype)]
+    grads[0][1] = 0.5
+    norms, outs = clip(grads, 1e38)
+    want = norms_in_64(grads)
+    assert float(norms[0]) == float("inf") and float(want[0]) > 2e40 and norms[1].isfinite()
+    factor = float(torch.tensor(1e38, dtype=torch.float32)) / want[0]
+    for g, o in zip(grads, outs):
+        exact = g[0].double() * factor
+        assert bool(((o[0].cpu().double() - exact).abs() <= (HALF_STEP[dtype] + 2 * U) * exact.abs()).all())
+        assert same_bits(o[1].cpu(), g[1])
+
+
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 @pytest.mark.parametrize("kept", [129, 130, 180, 201, 254, 255])
 @pytest.mark.parametrize("value", [131, 171, 177, 213, 255])
