@@ -255,8 +255,11 @@ LossTiles loss_tiles(LossKind kind, int64_t m, int64_t n, int64_t batch, int64_t
 inline int loss_meet(int planes, bool result32) { return result32 || planes == 1 ? planes : 2; }
 
 // Up to so many tokens of all workers, g is held in fp32 and met in three planes for a BF16
-// result too. The results of many tokens are off by g's rounding and their own, 2^(1/2) of the
-// latter alone; of few, an entry or two of g decide, their target's, and may be off by 2.4 times.
+// result too. A result of many tokens is off by g's rounding and its own, 2^(1/2) of the latter
+// alone on average; where an entry or two of g decide, it may be off by 2.4 times: of few tokens that
+// is every row, of many a rare target's row of dw, within half a step for g and half a step for
+// itself; three planes would take three products for one there (dw of 8192 x 32000 x 4096: 1.65 ms).
+// The count is of all workers, since one g serves dx and every worker's dw.
 constexpr int64_t kLossFew = 128;
 
 inline int64_t loss_slices(int64_t k, bool g32) {
