@@ -107,7 +107,8 @@ __global__ __launch_bounds__(256) void loss_parts_kernel(LossTile f) {
                 for (int j = 0; j < 8; ++j)
                     if (s + j < f.splits) l += q[j];
             }
-            if (f.plain_a)
+            // (of a token whose lse is no number, g is none either)
+            if (f.plain_a && (!GRAD || fabsf(static_cast<const float *>(f.rows[1])[row]) < INFINITY))
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (j < have && l[j] != l[j]) l[j] = plain_logit(f, row, col + j);

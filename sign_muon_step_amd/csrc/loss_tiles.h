@@ -357,7 +357,9 @@ __device__ __forceinline__ void write(Acc<FM, FN> &acc, char *mine, void *out, i
 // themselves. The planes of x behind the first are nought or of either sign, and an infinity of w, or a
 // first plane's product past fp32's range, meets each of them: a vocabulary entry that the weight
 // sends to minus infinity would be no number, where the sum of the operands' own products is
-// minus infinity.
+// minus infinity. It is for few entries: 64 masked ones of 32000 take 8192 fp32 tokens of 1024
+// columns, forward and backward, from 11.9 to 22.3 ms. Where a token's sum, or its lse, is no number
+// whatever its other logits are, none is made.
 __device__ __forceinline__ float plain_logit(const LossTile &f, int64_t row, int64_t col) {
     double sum = 0.0;
 #pragma unroll 1
@@ -440,8 +442,9 @@ __device__ __forceinline__ void finish_lse(const LossTile &f, Acc<FM, FN> &acc, 
                         sum[0] += v != v ? 0.0f : __builtin_amdgcn_exp2f(v - base);
                     }
                 }
+                // (a sum that is no number stays none)
 #pragma unroll 1
-                for (; bad; bad &= bad - 1) {
+                for (; bad && sum[0] == sum[0]; bad &= bad - 1) {
                     const int at = __builtin_ctzll(bad), col = column(at / 16, at % 16, lane1);
                     const float v = plain_logit(f, row0 + row, col0 + col) * f.factor, most = fmaxf(top, v);
                     if (col == target) f.target[row0 + row] = v;
@@ -524,12 +527,14 @@ __device__ __forceinline__ void finish_grad(const LossTile &f, Acc<FM, FN> &acc,
                 const int row = at / kCols, col = at % kCols;
                 const int t = *reinterpret_cast<const int *>(data + row * 4);
                 const int64_t entry = (row0 + row) * f.g_pitch + col0 + col;
+                const float b = *reinterpret_cast<const float *>(data + (row + 2 * kRows) * 4);
+                const float times = *reinterpret_cast<const float *>(data + (row + 4 * kRows) * 4);
                 float v = load1<!WIDE>(f.g, entry);
-                if (v == v || t < 0 || col >= have) continue;
-                v = __builtin_amdgcn_exp2f(fmaf(plain_logit(f, row0 + row, col0 + col), f.factor,
-                                                -*reinterpret_cast<const float *>(data + (row + 2 * kRows) * 4)));
+                // (of a token whose loss is no number, neither are its gradients)
+                if (v == v || t < 0 || col >= have || (b - b) + (times - times) != 0.0f) continue;
+                v = __builtin_amdgcn_exp2f(fmaf(plain_logit(f, row0 + row, col0 + col), f.factor, -b));
                 if (t - f.vocab0 - col0 == col) v -= 1.0f;
-                store1<!WIDE>(f.g, entry, v * *reinterpret_cast<const float *>(data + (row + 4 * kRows) * 4));
+                store1<!WIDE>(f.g, entry, v * times);
             }
         }
     clear<FM, FN>(acc);

@@ -327,6 +327,10 @@ def test_masked_vocabulary_of_every_type(workers, tokens, vocab, cols, x_dtype, 
     others = torch.ones(workers, tokens, dtype=torch.bool, device=DEV)
     others[0, 7] = False
     assert same_bits(again[others], lse[others]) and bool(again[~others].isnan().all())
+    targets[0, 7] = 0
+    dx_bad, dw_bad = run_backward(x, w, targets, 1.0, again, dloss, BF16)
+    assert same_bits(dx_bad[others], dx[others]) and bool(dx_bad[~others].isnan().all())
+    assert same_bits(dw_bad[1:], dw[1:]) and bool(dw_bad[0].isnan().all())
 
 
 def test_backward_is_the_forwards_by_differences():
