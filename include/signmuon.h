@@ -513,7 +513,7 @@ size_t signmuon_rms_norm_workspace_bytes(int32_t workers, int64_t rows, int64_t 
  * least vocab (padding) has the loss 0. Logits are summed with fp32's accuracy,
  * BF16 and F32 operands alike (F32 ones at a third to a sixth of the rate). A logit
  * of minus infinity (an entry of the vocabulary that w masks) counts as nothing, though
- * with an F32 x it costs as much as thousands of others; one
+ * with an F32 operand it may cost as much as thousands of others; one
  * of plus infinity or NaN makes its token's loss and lse NaN, and no other's. tokens
  * is the count over all workers. workspace:
  * signmuon_linear_cross_entropy_workspace_bytes(tokens, vocab, cols, x_dtype, w_dtype)

@@ -805,7 +805,8 @@ int signmuon_linear_cross_entropy(const void *x, signmuon_dtype x_dtype, const v
         f.batch = 1;
         loss_pairs(f, nx, nw);
         loss_set_tiles(f, p.logits);
-        f.plain_a = nx > 1 ? x : nullptr;
+        f.plain_a = f.pairs > 1 ? x : nullptr;
+        f.plain_a16 = x_dtype == SIGNMUON_BF16;
         f.plain_b = rows;
         f.plain_b16 = w_dtype == SIGNMUON_BF16;
         f.rows[0] = targets;
@@ -902,7 +903,8 @@ int signmuon_linear_cross_entropy_backward(const void *x, signmuon_dtype x_dtype
         loss_set_tiles(f, p.logits);
         for (int i = 0; i < 3; ++i) f.rows[i] = ws + p.row[i];
         f.row_step = 4;
-        f.plain_a = nx > 1 ? x : nullptr;
+        f.plain_a = f.pairs > 1 ? x : nullptr;
+        f.plain_a16 = x_dtype == SIGNMUON_BF16;
         f.plain_b = w_rows;
         f.plain_b16 = w_dtype == SIGNMUON_BF16;
         f.g = g;

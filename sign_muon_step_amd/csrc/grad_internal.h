@@ -219,8 +219,8 @@ struct LossTile {
     float *target;             // [m] logit of the target
     void *g;                   // [m][g_pitch]
     int64_t g_pitch;
-    const void *plain_a, *plain_b;  // the operands that the planes were made of, where a is in several: [m][k]
-    bool plain_b16;            // (fp32) and [n][k] in BF16 or fp32
+    const void *plain_a, *plain_b;  // the operands that the planes were made of, where one is in several: [m][k]
+    bool plain_a16, plain_b16;      // and [n][k], in BF16 or fp32
     int64_t vocab0;            // the piece's first entry
     float factor;              // scale / log 2
     // values

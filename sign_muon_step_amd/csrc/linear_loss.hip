@@ -237,8 +237,8 @@ void launch_loss_logits(const LossTile &f, bool grad, hipStream_t s) {
         launch_tiles<kRows16, kRows16, kValues, true>(f, s);
     else if (!grad)
         f.plain_a ? launch_tiles<kRows16, kRows16, kPlanesLse, true>(f, s) : launch_tiles<kRows16, kRows16, kLse, true>(f, s);
-    else if (f.plain_a)  // g is fp32 wherever x is
-        launch_tiles<kRows16, kRows16, kPlanesGrad, true>(f, s);
+    else if (f.plain_a)
+        f.g32 ? launch_tiles<kRows16, kRows16, kPlanesGrad, true>(f, s) : launch_tiles<kRows16, kRows16, kPlanesGrad, false>(f, s);
     else
         f.g32 ? launch_tiles<kRows16, kRows16, kGrad, true>(f, s) : launch_tiles<kRows16, kRows16, kGrad, false>(f, s);
 }

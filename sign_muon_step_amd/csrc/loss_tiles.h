@@ -354,8 +354,8 @@ __device__ __forceinline__ void write(Acc<FM, FN> &acc, char *mine, void *out, i
 }
 
 // A logit (over its scale) whose products of planes add up to no number, from the operands
-// themselves. The planes of x behind the first are nought or of either sign, and an infinity of w, or a
-// first plane's product past fp32's range, meets each of them: a vocabulary entry that the weight
+// themselves. An operand's planes behind the first are nought or of either sign, and an infinity of
+// the other, or a product past fp32's range, comes with each of them: a vocabulary entry that the weight
 // sends to minus infinity would be no number, where the sum of the operands' own products is
 // minus infinity. It is for few entries: 64 masked ones of 32000 take 8192 fp32 tokens of 1024
 // columns, forward and backward, from 11.9 to 22.3 ms. Where a token's sum, or its lse, is no number
@@ -366,11 +366,11 @@ __device__ __forceinline__ float plain_logit(const LossTile &f, int64_t row, int
     for (int64_t k = 0; k < f.k && sum == sum; k += 8) {
         const int have = left((int)f.k, (int)k);
         float a[8], b[8];
-        load_n<false>(f.plain_a, row * f.k + k, have, a);
-        if (f.plain_b16)
-            load_n<true>(f.plain_b, col * f.k + k, have, b);
-        else
-            load_n<false>(f.plain_b, col * f.k + k, have, b);
+        auto load = [&](const void *p, int64_t at, bool bf16, float(&v)[8]) {
+            bf16 ? load_n<true>(p, at, have, v) : load_n<false>(p, at, have, v);
+        };
+        load(f.plain_a, row * f.k + k, f.plain_a16, a);
+        load(f.plain_b, col * f.k + k, f.plain_b16, b);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum = fma((double)a[j], (double)b[j], sum);
     }
@@ -378,7 +378,7 @@ __device__ __forceinline__ float plain_logit(const LossTile &f, int64_t row, int
 }
 
 // A row's maximum and sum of exponentials over the wave's columns, and the target's
-// logit, in units of log 2. PLANES: x is in several.
+// logit, in units of log 2. PLANES: an operand is in several.
 template <int FM, int FN, bool PLANES>
 __device__ __forceinline__ void finish_lse(const LossTile &f, Acc<FM, FN> &acc, const char *targets, int64_t row0,
                                            int64_t col0, int lane) {
@@ -465,7 +465,7 @@ __device__ __forceinline__ void finish_lse(const LossTile &f, Acc<FM, FN> &acc, 
     clear<FM, FN>(acc);
 }
 
-// g; zeros in the columns past the vocabulary that a tile has. PLANES: x is in several.
+// g; zeros in the columns past the vocabulary that a tile has. PLANES: an operand is in several.
 template <int FM, int FN, bool WIDE, bool PLANES>
 __device__ __forceinline__ void finish_grad(const LossTile &f, Acc<FM, FN> &acc, char *mine, const char *data, int64_t row0,
                                             int64_t col0, int lane) {
@@ -577,7 +577,7 @@ __device__ __forceinline__ uint32_t stage_of(uint32_t lds, unsigned c, int wave)
     return to;
 }
 
-enum { kLse, kGrad, kValues, kPlanesLse, kPlanesGrad };  // kPlanes..: of an x in several planes
+enum { kLse, kGrad, kValues, kPlanesLse, kPlanesGrad };  // kPlanes..: of an operand in several planes
 
 // Products of BF16 operands. A workgroup takes every gridDim-th tile; four waves of
 // half a tile each way. The loads run two slices ahead of the products, on into the

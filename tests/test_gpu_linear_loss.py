@@ -306,6 +306,7 @@ def test_masked_vocabulary_of_every_type(workers, tokens, vocab, cols, x_dtype, 
     w[kind == 3] = 0.0
     w[kind == 3, 0] = -math.inf
     w[kind == 4, 1] = -1.3e30
+    w[9::10, 1] = -1.303e30  # whose second plane is of the other sign
     inside = (targets >= 0) & (targets < vocab)
     targets = torch.where(inside, targets // 5 * 5, targets)
     loss, lse = run_forward(x, w, targets, 1.0)
