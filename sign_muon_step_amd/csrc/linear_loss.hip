@@ -29,9 +29,11 @@
 // and a row of logits lies in two lanes.
 //
 // Bound by the matrix pipe, and at full load by the card's power, which lowers its
-// clock. 8192 tokens of 32000 x 4096 in BF16: logits and their sums 1.66 to 1.73 ms, g 1.73,
-// dw 1.65, dx 1.56 (1.24 to 1.37 PFLOP/s of 2.1 TFLOP each; a large library product without
-// any of the epilogues takes 1.55); 4096 x 50257 x 768 forward 290 us (1.09 PFLOP/s). One token of
+// clock to 1.7 GHz of 2.4. 8192 tokens of 32000 x 4096 in BF16: logits and their sums 1.63 to 1.73 ms,
+// g 1.69, dw 1.60, dx 1.51 (1.24 to 1.43 PFLOP/s of 2.1 TFLOP each, matrix cores busy for 62 to 76 % of
+// the cycles; a large library product without any of the epilogues takes 1.55). With fewer slices a
+// tile, or g in fp32, results and barriers show: 4096 x 50257 x 768 forward 284 us (1.11 PFLOP/s, busy
+// for 49 %), eight workers' products 35 to 53 %. One token of
 // 32000 x 768 takes 18 us, 49 MB at 3.4 TB/s in the kernel and a second one that joins.
 // Where a product has few tiles, its k is split and a pass adds the parts.
 #include "loss_tiles.h"

@@ -9,10 +9,13 @@
 // All passes are bound by memory. A row is read once and held in registers by a
 // team of lanes, as layer norm's. A block of 128 values that shares a scale of
 // the 8-bit output lies in 16 neighbouring lanes: its largest size is four
-// exchanges away, and the output costs no pass of its own. Measured: 8192 x 768 of
+// exchanges away, and the output costs no pass of its own. It is quantised from fp32: of 6.3 M values
+// two to six lie so near the middle of two 8-bit ones that a rounding of rstd or y decides. Measured: 8192 x 768 of
 // BF16 with residual to 8 bits 10.5 us a call (44 MB, 4.2 TB/s; one round of rows, so
 // latency shows), the gradients of 8 x 1024 x 768 13.5 (50 MB in two launches), one token 10
-// (the kernel takes 3.3, the rest is issuing the call).
+// (the kernel takes 3.3, the rest is issuing the call). 8192 rows of 4096 in BF16 with residual 42 us
+// (6.5 TB/s), their gradients 46 (5.8); 4096 rows of 16384, which are read again for the result and
+// for dgamma, 115 and 169 (4.7 and 3.2 TB/s of what they hold).
 #include "grad_internal.h"
 
 namespace sm {
